@@ -363,6 +363,114 @@ GTR_API gtr_status_t gtr_stack_fwd(float *x, const gtr_block_weights *blocks, in
                                    size_t workspace_bytes, void *stream);
 
 /*
+ * Linear attention with one decay per head, over packed sequences (the paper
+ * has no counterpart; gtr_gla_fwd is the form with a decay per key dimension
+ * over image grids).  Tokens of sequence n are rows start_n .. end_n - 1 of
+ * the packed tensors; for head h of H, with key head h' = h / (H / Hk),
+ *
+ *     S_t = exp(g[t,h]) S_{t-1} + k[t,h']^T v[t,h]          (dk x dv, fp32)
+ *     o_t = scale * q[t,h'] S_t
+ *     out[t,h] = o_t                                          (outgate NULL)
+ *              = o_t / sqrt(mean(o_t^2) + 1e-5) * w * SiLU(z[t,h])
+ *
+ *   q, k     [T, Hk, dk], v, outgate (= z), out [T, H, dv] in `dtype`.  The
+ *            heads of a token are contiguous; ldq, ldk, ldv, ldz, ldo are the
+ *            elements from one token to the next (0 = dense), so that column
+ *            blocks of one projection can be passed as they are.
+ *   g        fp32 log-decays, [T, H], or [H] with g_per_head != 0 (the same
+ *            for every token).  A decay is at most one: g > 0 counts as 0, and
+ *            g below -110 (e^-110 is zero in fp32; -infinity too) as -110.  A
+ *            NaN propagates.
+ *   rms_w    [dv] fp32 or NULL (ones); must be NULL when outgate is.
+ *   cu_seqlens  device int32 [nseq + 1], non-decreasing from >= 0 to <= T:
+ *            sequence n is rows [cu_seqlens[n], cu_seqlens[n + 1]).  Rows
+ *            outside every sequence are neither read nor written.  NULL: nseq
+ *            equal sequences of T / nseq rows (nseq must divide T).  Lengths
+ *            of zero are allowed (the final state is then the initial one).
+ *   state_in, state_out  [nslots, H, dk, dv] fp32, either may be NULL (start
+ *            from zero; final states not wanted); the same pointer updates
+ *            the states in place.  Different pointers must not overlap.
+ *   slots    device int32 [nseq]: the state of sequence n (NULL: n; nslots >=
+ *            nseq then).  A negative slot skips the sequence: no output row
+ *            and no state is written.  A slot >= nslots is skipped too and
+ *            recorded for gtr_last_device_status.  Slots must be distinct.
+ *   seen     device int32 [nseq] or NULL: sequence n starts from state_in only
+ *            where seen[n] > 0 (the number of tokens its state has taken so
+ *            far), else from zero.  NULL: every sequence does.
+ *   dk, dv in {16, 32, 64, 128}; Hk divides H; T < 2^31.
+ * A non-finite q, k or v element reaches only its own sequence and head, but
+ * there any output of its block of 128 tokens and what follows.  States, decay
+ * sums and the norm are fp32; 16-bit products carry at least 16 significant
+ * bits of every inexact operand.
+ *   gtr_hla_workspace_bytes: bytes of `workspace` that gtr_hla_fwd needs for
+ *     these sizes on the current device (may be 0; (size_t)-1 for sizes it
+ *     refuses).  The caller owns the workspace (16-byte aligned); calls that
+ *     may run at the same time need one each.
+ *   gtr_hla_fwd: the prompt form.  16-bit types with dk, dv in {64, 128} run on
+ *     tcgen05 tensor-core kernels, chunk by chunk of 128 tokens; the others on
+ *     fp32 CUDA cores.  Never allocates, never synchronises, graph-capturable.
+ *   gtr_hla_step: one token per sequence (T = nseq rows, cu_seqlens, seen and
+ *     workspace unused and NULL): row n updates state slots[n] from state_in
+ *     into state_out, both required, and gives its output row.  Rows with a
+ *     negative slot are skipped.
+ * Errors: GTR_ERR_INVALID_ARG (NULL, negative or inconsistent sizes, Hk not
+ * dividing H), GTR_ERR_UNSUPPORTED (head dims), GTR_ERR_ALIGNMENT (q, k, v,
+ * outgate, out, states or workspace not 16-byte aligned, or a row pitch that is
+ * not a multiple of 16 bytes), GTR_ERR_NO_MEMORY (workspace too small).
+ */
+typedef struct gtr_hla_args {
+  const void *q, *k, *v;
+  const float *g;
+  const void *outgate;
+  const float *rms_w;
+  void *out;
+  const float *state_in;
+  float *state_out;
+  const int *slots, *seen, *cu_seqlens;
+  void *workspace;
+  size_t workspace_bytes;
+  long long ldq, ldk, ldv, ldz, ldo;
+  int nseq, T, Hk, H, dk, dv, nslots;
+  int g_per_head, dtype;
+  float scale;
+} gtr_hla_args;
+
+GTR_API size_t gtr_hla_workspace_bytes(int nseq, int T, int H, int dk, int dv, int dtype);
+GTR_API gtr_status_t gtr_hla_fwd(const gtr_hla_args *args, void *stream);
+GTR_API gtr_status_t gtr_hla_step(const gtr_hla_args *args, void *stream);
+
+/*
+ * The norms around a residual branch, with the branch's gate and scale, in one
+ * pass (gtr_stack_fwd's add + RMSNorm is the case without post-norm, gate and
+ * scale).  For each of N rows of width D:
+ *
+ *     r = y                          or  y / sqrt(mean(y^2) + eps) * post_w   (post_norm)
+ *     r = r * act(gate)              (gate given; act: gtr_gate_act_t)
+ *     x_out = x + alpha * res_scale * r
+ *     out = x_out / sqrt(mean(x_out^2) + eps) * pre_w                         (out given)
+ *
+ *   x, x_out  [N, D] in x_dtype (x_out may be x); y, gate, out in `dtype`.
+ *   x_dtype GTR_F32 goes with any dtype; else the two must be equal
+ *   (GTR_ERR_UNSUPPORTED).  All arithmetic is fp32, out is formed from the sum
+ *   before it is rounded to x_dtype.
+ *   y NULL: no branch (x_out = x; gate, post_norm and res_scale must be unset).
+ *   gate [N / gate_rows, D]: gate_rows consecutive rows share a gate row (1:
+ *   elementwise; a sequence's rows for one gate per sequence); gate_rows must
+ *   divide N.
+ *   post_w, res_scale, pre_w [D] fp32 or NULL (ones).
+ *   1 <= D <= 16384 (else GTR_ERR_UNSUPPORTED), any alignment of whole
+ *   elements; D a multiple of 8 with 16-byte aligned pointers moves 16 bytes
+ *   per access.  out and x_out must not overlap each other or any input other
+ *   than x_out = x (GTR_ERR_INVALID_ARG).  N = 0 is an empty problem.
+ */
+typedef enum { GTR_GATE_MUL = 0, GTR_GATE_SIGMOID = 1, GTR_GATE_SILU = 2 } gtr_gate_act_t;
+GTR_API gtr_status_t gtr_residual_norm(const void *x, void *x_out, int x_dtype, const void *y, int post_norm,
+                                       const float *post_w, const void *gate, int gate_act,
+                                       long long gate_rows, const float *res_scale, float alpha,
+                                       const float *pre_w, void *out, long long N, int D, float eps,
+                                       int dtype, void *stream);
+
+/*
  * Chunk-boundary states, for testing the first two stages on their own: the
  * state each chunk of `chunk` scan positions ends with,
  *   states [B, H, ceil(T/chunk), dk, dv] fp32, entry c = S after scan position

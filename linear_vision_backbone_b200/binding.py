@@ -7,8 +7,11 @@ Python or CPU fallback: if the library is missing the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -29,8 +32,9 @@ EXPORTS = (
     "gtr_gla_fwd_noalloc", "gtr_gate_packed_bytes", "gtr_gate_pack", "gtr_gate_fwd_packed",
     "gtr_gla_segment_count", "gtr_gla_fwd_gated", "gtr_gla_fwd_gated_timed", "gtr_mixer_in_proj",
     "gtr_mixer_out_proj", "gtr_sswiglu_mix", "gtr_sswiglu_fwd", "gtr_stack_workspace_bytes",
-    "gtr_stack_fwd",
+    "gtr_stack_fwd", "gtr_hla_workspace_bytes", "gtr_hla_fwd", "gtr_hla_step", "gtr_residual_norm",
 )
+GATE_ACTS = {"none": 0, "mul": 0, "sigmoid": 1, "silu": 2}
 
 BLOCK_FIELDS = ("norm_mixer", "w_in", "gate_packed", "gate_bias", "gla_norm", "w_o", "norm_ffn", "w_e",
                 "conv_w", "conv_b", "w_p")
@@ -90,6 +94,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "gtr_sswiglu_fwd": ([P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P], I),
             "gtr_stack_workspace_bytes": ([I, I, I, I, I, I, I, I], Z),
             "gtr_stack_fwd": ([P, P, I, P, I, I, I, I, I, I, I, I, F, I, I, P, Z, P], I),
+            "gtr_hla_workspace_bytes": ([I, I, I, I, I, I], Z),
+            "gtr_hla_fwd": ([ctypes.c_char_p, P], I),
+            "gtr_hla_step": ([ctypes.c_char_p, P], I),
+            "gtr_residual_norm": ([P, P, I, P, I, P, P, I, ctypes.c_longlong, P, F, P, P, ctypes.c_longlong, I, F,
+                                   I, P], I),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -424,6 +433,218 @@ def gla_fwd_noalloc(q, k, v, g, z, w=None, *, grid_h: int, grid_w: int, directio
                                     B, H, grid_h, grid_w, dk, dv, DIR_IDS[direction], int(chunk),
                                     DTYPE_IDS[q.dtype], _stream(stream))
     _check("gtr_gla_fwd_noalloc", rc)
+    return out
+
+
+# gtr_hla_args in the header's order: 13 pointers, the workspace size, five row
+# pitches, nine ints, the scale
+_HLA_ARGS = struct.Struct("@13PN5q9if")
+
+
+def _on(device: int, stream):
+    """The device's context where it is not the current one, and the raw stream to launch on."""
+    guard = None
+    if torch.cuda.current_device() != device:
+        guard = torch.cuda.device(device)
+    if stream is None:
+        return guard, torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors are on {device}")
+    return guard, stream.cuda_stream
+
+
+@contextlib.contextmanager
+def _allocating(guard, stream):
+    """Allocations belong to the stream that uses them."""
+    with contextlib.ExitStack() as stack:
+        if guard is not None:
+            stack.enter_context(guard)
+        if stream is not None:
+            stack.enter_context(torch.cuda.stream(stream))
+        yield
+
+
+@functools.lru_cache(maxsize=4096)
+def _hla_workspace(device: int, nseq: int, T: int, H: int, dk: int, dv: int, dtype: int) -> int:
+    with torch.cuda.device(device):
+        return int(load().gtr_hla_workspace_bytes(nseq, T, H, dk, dv, dtype))
+
+
+def _rows(t, name, lead, heads, d, dtype, device):
+    """Row pitch of a [*lead, heads, d] tensor whose tokens may be apart (0: dense)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{device}")
+    if t.shape != (*lead, heads, d):
+        raise ValueError(f"{name} must have shape {(*lead, heads, d)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    st = t.stride()
+    if st[-1] != 1 or (heads > 1 and st[-2] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]:
+        raise ValueError(f"{name}: sequences must follow each other at the tokens' pitch")
+    return st[-3] if lead[-1] > 1 else (st[0] if len(lead) == 2 and lead[0] > 1 else 0)
+
+
+def _vector(t, name, n, dtype, device):
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != dtype or t.shape != (n,) \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} on cuda:{device}")
+    return t.data_ptr()
+
+
+def _states(t, name, H, dk, dv, device):
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != torch.float32 or t.dim() != 4 \
+            or t.shape[1:] != (H, dk, dv) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor [n, {H}, {dk}, {dv}] on cuda:{device}")
+    return t.data_ptr()
+
+
+def _hla(fn, q, k, v, g, z, w, cu_seqlens, nseq, scale, state_in, state_out, slots, seen, out, stream):
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    if q.dtype not in DTYPE_IDS:
+        raise ValueError(f"q must be one of {list(DTYPE_IDS)}, got {q.dtype}")
+    device, dtype, lead = q.get_device(), q.dtype, q.shape[:-2]
+    if len(lead) not in (1, 2) or not isinstance(v, torch.Tensor) or v.dim() != q.dim():
+        raise ValueError("q, k, v must be [T, heads, d] or [B, T, heads, d]")
+    Hk, dk = q.shape[-2:]
+    H, dv = v.shape[-2:]
+    T = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    if len(lead) == 2 and cu_seqlens is not None:
+        raise ValueError("cu_seqlens goes with packed [T, heads, d] tensors")
+    ldq, ldk = _rows(q, "q", lead, Hk, dk, dtype, device), _rows(k, "k", lead, Hk, dk, dtype, device)
+    ldv = _rows(v, "v", lead, H, dv, dtype, device)
+    ldz = 0 if z is None else _rows(z, "z", lead, H, dv, dtype, device)
+    if not isinstance(g, torch.Tensor) or g.get_device() != device or g.dtype != torch.float32 \
+            or not g.is_contiguous() or g.shape not in ((H,), (*lead, H)):
+        raise ValueError(f"g must be a contiguous float32 tensor {(*lead, H)} or ({H},) on cuda:{device}")
+    if w is not None and z is None:
+        raise ValueError("w goes with z")
+    if nseq is None:
+        nseq = lead[0] if len(lead) == 2 else 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    if nseq < 0:
+        raise ValueError("cu_seqlens must have at least one entry")
+    nslots = -1
+    for name, t in (("state_in", state_in), ("state_out", state_out)):
+        if t is not None:
+            if nslots >= 0 and t.shape[0] != nslots:
+                raise ValueError("state_in and state_out must have the same number of states")
+            nslots = t.shape[0]
+    pi, po = _states(state_in, "state_in", H, dk, dv, device), _states(state_out, "state_out", H, dk, dv, device)
+    if nslots >= 0 and slots is None and nslots < nseq:
+        raise ValueError(f"{nseq} sequences need {nseq} states or slots, got {nslots}")
+    pw, ps = _vector(w, "w", dv, torch.float32, device), _vector(slots, "slots", nseq, torch.int32, device)
+    pn, pc = _vector(seen, "seen", nseq, torch.int32, device), _vector(cu_seqlens, "cu_seqlens", nseq + 1,
+                                                                       torch.int32, device)
+    guard, raw = _on(device, stream)
+    lib = load()
+    did = DTYPE_IDS[dtype]
+    need = _hla_workspace(device, nseq, T, H, dk, dv, did) if fn == "gtr_hla_fwd" else 0
+    ws = None
+    with _allocating(guard, stream) if guard is not None or stream is not None else contextlib.nullcontext():
+        if out is None:
+            out = torch.empty(v.shape, dtype=dtype, device=v.device)
+        ldo = _rows(out, "out", lead, H, dv, dtype, device)
+        if need and need < 1 << 62:
+            ws = torch.empty(need, dtype=torch.uint8, device=v.device)
+        args = _HLA_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                              0 if z is None else z.data_ptr(), pw, out.data_ptr(), pi, po, ps, pn, pc,
+                              0 if ws is None else ws.data_ptr(), 0 if ws is None else need, ldq, ldk, ldv, ldz, ldo,
+                              nseq, T, Hk, H, dk, dv, max(nslots, 0), g.dim() == 1, did, scale)
+        rc = getattr(lib, fn)(args, raw)
+    if rc:
+        _check(fn, rc)
+    return out
+
+
+def hla_fwd(q, k, v, g, z=None, w=None, *, cu_seqlens=None, scale: float = 1.0, state_in=None, state_out=None,
+            slots=None, seen=None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Linear attention with one decay per head over packed sequences (``gtr_hla_fwd``).
+
+    S_t = exp(g_t) S_{t-1} + k_t^T v_t and o_t = scale q_t S_t per sequence and
+    head; returns o, or RMSNorm(o) * w * SiLU(z) with z, as v's shape and type.
+    q, k: [T, Hk, dk]; v, z, out: [T, H, dv], H a multiple of Hk; sequence n is
+    rows cu_seqlens[n] .. cu_seqlens[n + 1] (int32 on the device; None: one
+    sequence).  Or [B, T, heads, d]: B sequences of T tokens.  A token's heads
+    are contiguous, tokens may be further apart.  g: fp32 [T, H] (or [B, T, H]),
+    or [H] for constant decays; w: [dv] fp32.  state_in / state_out: fp32 [n, H,
+    dk, dv], read at each sequence's start and written at its end, at row
+    slots[n] (int32; None: n; negative: the sequence is skipped); the same
+    tensor updates in place.  A sequence with seen[n] <= 0 (int32) starts from
+    zero.  Rows outside every sequence are left as they were.
+    """
+    return _hla("gtr_hla_fwd", q, k, v, g, z, w, cu_seqlens, None, scale, state_in, state_out, slots, seen, out,
+                stream)
+
+
+def hla_step(q, k, v, g, state_in, z=None, w=None, *, slots=None, scale: float = 1.0, state_out=None,
+             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of every sequence (``gtr_hla_step``): q, k [N, Hk, dk], v, z [N, H, dv],
+    g fp32 [N, H] or [H]; row n updates state slots[n] (None: n; negative: the row is
+    skipped and its output left as it was) of state_in, in place or into state_out, and
+    gives o_n as in :func:`hla_fwd`."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [N, Hk, dk]")
+    if state_in is None:
+        raise ValueError("state_in is needed")
+    return _hla("gtr_hla_step", q, k, v, g, z, w, None, q.shape[0], scale, state_in,
+                state_in if state_out is None else state_out, slots, None, out, stream)
+
+
+def residual_norm(x, y=None, *, post_norm: Optional[bool] = None, post_w=None, gate=None, gate_act: str = "sigmoid",
+                  res_scale=None, alpha: float = 1.0, pre_norm: Optional[bool] = None, pre_w=None, x_out=None,
+                  out=None, eps: float = 1e-5, stream=None):
+    """The norms around a residual branch y with its gate and scale (``gtr_residual_norm``):
+
+        r = y, or RMSNorm(y) * post_w;  r *= act(gate);  x_out = x + alpha * res_scale * r
+
+    Returns RMSNorm(x_out) * pre_w in y's type (x's without y), or None without
+    a pre-norm.  x: [..., D], updated in place unless x_out is given; gate: y's
+    shape, or [n, D] with n dividing the rows (row r takes gate row r // (rows /
+    n)); gate_act: "mul", "sigmoid" or "silu".  post_w, res_scale, pre_w: [D]
+    fp32 or None; post_norm / pre_norm default to whether their weight is given.
+    """
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in DTYPE_IDS or x.dim() < 1:
+        raise ValueError("x must be a CUDA tensor [..., D]")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    device, D = x.get_device(), x.shape[-1]
+    N = x.numel() // D if D else 0
+    dtype = x.dtype if y is None else y.dtype
+    post_norm = post_w is not None if post_norm is None else post_norm
+    pre_norm = pre_w is not None or out is not None if pre_norm is None else pre_norm
+    if post_w is not None and not post_norm:
+        raise ValueError("post_w goes with post_norm")
+    if (pre_w is not None or out is not None) and not pre_norm:
+        raise ValueError("pre_w and out go with pre_norm")
+    rows = 1
+    for name, t, dt in (("y", y, dtype), ("x_out", x_out, x.dtype), ("gate", gate, dtype), ("out", out, dtype)):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != dt or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dt} tensor on cuda:{device}")
+        if t.shape != x.shape:
+            if name != "gate" or t.dim() != 2 or t.shape[1] != D or t.shape[0] < 1 or N % t.shape[0]:
+                raise ValueError(f"{name} must have shape {tuple(x.shape)}, got {tuple(t.shape)}")
+            rows = max(1, N // t.shape[0])
+    guard, raw = _on(device, stream)
+    with _allocating(guard, stream) if guard is not None or stream is not None else contextlib.nullcontext():
+        if pre_norm and out is None:
+            out = torch.empty(x.shape, dtype=dtype, device=x.device)
+        rc = load().gtr_residual_norm(
+            x.data_ptr(), (x if x_out is None else x_out).data_ptr(), DTYPE_IDS[x.dtype],
+            0 if y is None else y.data_ptr(), post_norm, _vector(post_w, "post_w", D, torch.float32, device),
+            0 if gate is None else gate.data_ptr(), GATE_ACTS[gate_act], rows,
+            _vector(res_scale, "res_scale", D, torch.float32, device), alpha,
+            _vector(pre_w, "pre_w", D, torch.float32, device), 0 if out is None else out.data_ptr(), N, D, eps,
+            DTYPE_IDS[dtype], raw)
+    if rc:
+        _check("gtr_residual_norm", rc)
     return out
 
 

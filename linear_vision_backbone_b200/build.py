@@ -3,7 +3,9 @@
     python -m linear_vision_backbone_b200.build
 
 compiles the translation units ``csrc/*.cu`` (``gtr_gla.cu``: the gate and the
-GLA with their projections; ``sswiglu.cu``: the Spatial SwiGLU block) into
+GLA with their projections; ``sswiglu.cu``: the Spatial SwiGLU block;
+``stack.cu``: the block stack; ``hla.cu``: the head-decay linear attention;
+``residual_norm.cu``: the norms around a residual branch) into
 ``_build/libgtr_gla.so`` next to this file.  The library exports only the
 ``extern "C"`` entry points declared in ``include/gtr_gla.h``.
 """
@@ -25,7 +27,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-    "-shared", "-cudart", "static",
+    "-shared", "-cudart", "static", "--threads", "0",
 ]
 
 

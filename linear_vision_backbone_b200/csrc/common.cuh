@@ -24,6 +24,7 @@ enum StatusBits : unsigned {
   kStatusBadShape = 2u,      // a kernel met a shape its launch did not allow
   kStatusTmemAlloc = 4u,     // tensor-memory allocation returned an unusable address
   kStatusMbarTimeout = 8u,   // a bounded mbarrier wait ran out
+  kStatusBadSlot = 16u,      // a state slot outside the pool
 };
 
 // Segment s of nseg covers chunks [first(s), first(s + 1)) of a sequence of

@@ -657,6 +657,10 @@ int gla_fwd_noalloc_impl(const void* q, const void* k, const void* v, const floa
 // after the helpers above that it uses.
 #include "gemm_host.cuh"
 
+namespace gtr {
+int hla_take_status(unsigned* bits);   // hla.cu: its kernels' status bits, cleared
+}
+
 extern "C" {
 
 int gtr_abi_version(void) { return GTR_ABI_VERSION; }
@@ -1002,6 +1006,9 @@ gtr_status_t gtr_last_device_status(void* stream, unsigned long long* counters) 
   if (cudaMemcpyFromSymbol(&ex, g_gtr_exact_chunks, sizeof(ex)) != cudaSuccess) return GTR_ERR_CUDA;
   if (cudaMemcpyToSymbol(g_gtr_status, &zero, sizeof(zero)) != cudaSuccess) return GTR_ERR_CUDA;
   if (cudaMemcpyToSymbol(g_gtr_exact_chunks, &zero64, sizeof(zero64)) != cudaSuccess) return GTR_ERR_CUDA;
+  unsigned int hla = 0;
+  if (int rc = gtr::hla_take_status(&hla)) return (gtr_status_t)rc;
+  st |= hla;
   if (counters) { counters[0] = st; counters[1] = ex; }
   return st ? GTR_ERR_DEVICE_CHECK : GTR_OK;
 }

@@ -1,0 +1,196 @@
+// hla_simt.cuh -- the fp32 CUDA-core kernels of the head-decay linear
+// attention: prompts token by token (every dtype and head dim), and the form
+// for single tokens.
+#pragma once
+#include "hla_common.cuh"
+
+namespace gtr {
+namespace hla {
+
+constexpr int kSimtThreads = 256;
+constexpr int kSimtBatch = 16;     // tokens staged in shared memory per pass
+
+__host__ __device__ inline int simt_smem_floats(int dk, int dv, bool sum) {
+  return kSimtBatch * (1 + (sum ? 1 : 2) * dk + dv + (sum ? 0 : kSimtThreads));
+}
+
+// One segment of one head by the recurrence itself, the state spread over the
+// block: thread tid has column tid % dv and the ROWS rows from (tid / dv) ROWS,
+// so a warp reads a token's k and q values as broadcasts.  kSum: the state a
+// segment makes from zero and its decay (skipped for a sequence's last
+// segment); else its outputs from the state it starts from, and the
+// sequence's final state after its last segment.  Bound by the serial chain of
+// its tokens (two products and a sum per state element and token in fp32).
+template <typename T, int ROWS, bool kSum>
+__global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
+  extern __shared__ float sm[];
+  const int dk = p.dk, dv = p.dv;
+  float* as = sm;                            // [batch] decays
+  float* ks = as + kSimtBatch;               // [batch][dk]
+  float* qs = ks + kSimtBatch * dk;          // [batch][dk], outputs only
+  float* vs = qs + (kSum ? 0 : kSimtBatch * dk);   // [batch][dv]
+  float* part = vs + kSimtBatch * dv;        // [batch][threads]: partial o, outputs only
+  pdl_wait();
+  pdl_trigger();
+  const int h = blockIdx.y, hk = h / (p.H / p.Hk);
+  Segment g;
+  if (!find_segment(p, blockIdx.x, g)) return;
+  const bool last = g.i >= g.m - 1;
+  if (kSum && last) return;
+  const int tid = threadIdx.x, j = tid % dv, r0 = tid / dv * ROWS;
+  const size_t hs = (size_t)dk * dv;
+  float S[ROWS];
+  {
+    const float* src = nullptr;
+    if (!kSum && g.i > 0) src = p.wsS + ((size_t)(g.ws + g.i - 1) * p.H + h) * hs;
+    else if (!kSum && g.start) src = p.state_in + ((size_t)g.slot * p.H + h) * hs;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) S[r] = src ? src[(size_t)(r0 + r) * dv + j] : 0.f;
+  }
+  float total = 0.f;                         // thread 0: the segment's summed log2-decay
+  for (int b0 = 0; b0 < g.len; b0 += kSimtBatch) {
+    const int n = min(kSimtBatch, g.len - b0);
+    const long long t0 = (long long)g.t0 + b0;
+    __syncthreads();
+    if (tid < n) as[tid] = load_decay(p, (int)(t0 + tid), h);
+    for (int e = tid; e < n * dk; e += kSimtThreads) {
+      const int t = e / dk, i = e - t * dk;
+      ks[e] = ld_f((const T*)p.k + (t0 + t) * p.ldk + (long long)hk * dk + i);
+      if (!kSum) qs[e] = ld_f((const T*)p.q + (t0 + t) * p.ldq + (long long)hk * dk + i) * p.scale;
+    }
+    for (int e = tid; e < n * dv; e += kSimtThreads) {
+      const int t = e / dv, i = e - t * dv;
+      vs[e] = ld_f((const T*)p.v + (t0 + t) * p.ldv + (long long)h * dv + i);
+    }
+    __syncthreads();
+    for (int t = 0; t < n; ++t) {
+      const float l = as[t], a = exp2f(l), v = vs[t * dv + j];
+      total += l;
+      const float* k = ks + t * dk + r0;
+      const float* q = qs + t * dk + r0;
+      float o = 0.f;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        S[r] = fmaf(a, S[r], k[r] * v);
+        if (!kSum) o = fmaf(q[r], S[r], o);
+      }
+      if (!kSum) part[t * kSimtThreads + tid] = o;
+    }
+    if (!kSum) {
+      __syncthreads();
+      // one warp per token: the rows' partial sums, then the norm and the gate
+      const int lane = tid & 31;
+      for (int t = tid >> 5; t < n; t += kSimtThreads / 32) {
+        float o[4];
+        float ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = lane + 32 * c;
+          o[c] = 0.f;
+          if (col < dv)
+            for (int r = 0; r < kSimtThreads / dv; ++r) o[c] += part[t * kSimtThreads + r * dv + col];
+          ss = fmaf(o[c], o[c], ss);
+        }
+        float inv = 1.f;
+        if (p.z) inv = rsqrtf(warp_sum(ss) / (float)dv + kRmsEps);
+        T* orow = (T*)p.out + (t0 + t) * p.ldo + (long long)h * dv;
+        const T* zrow = p.z ? (const T*)p.z + (t0 + t) * p.ldz + (long long)h * dv : nullptr;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = lane + 32 * c;
+          if (col >= dv) continue;
+          float y = o[c];
+          if (zrow) y = y * inv * (p.w ? p.w[col] : 1.f) * silu_f(ld_f(zrow + col));
+          orow[col] = Elem<T>::from_f(y);
+        }
+      }
+    }
+  }
+  if (kSum) {
+    float* dst = p.wsS + ((size_t)(g.ws + g.i) * p.H + h) * hs;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) dst[(size_t)(r0 + r) * dv + j] = S[r];
+    if (tid == 0) p.wsA[(size_t)(g.ws + g.i) * p.H + h] = total;
+  } else if (last && p.state_out) {
+    float* dst = p.state_out + ((size_t)g.slot * p.H + h) * hs;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) dst[(size_t)(r0 + r) * dv + j] = S[r];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One token of one sequence and head: S = a S + k^T v, o = scale q S, read and
+// written once in fp32 (8 dk dv bytes, the floor of the call: about 96% of its
+// bytes at dk = dv = 128).  A block of 256 threads per (row, head); thread tid
+// has the four columns 4 (tid % (dv / 4)) and every (256 / (dv / 4))-th row,
+// R float4 of the state, all loaded before the first is used.
+constexpr int kStepThreads = 256;
+
+template <typename T, int R>
+__global__ void __launch_bounds__(kStepThreads) hla_step(const Params p) {
+  __shared__ float ks[128], qs[128], red[kStepThreads * 4], osum[4];
+  pdl_wait();
+  pdl_trigger();
+  const int n = blockIdx.x, h = blockIdx.y, hk = h / (p.H / p.Hk);
+  const int dk = p.dk, dv = p.dv, tid = threadIdx.x;
+  const long long slot = p.slots ? __ldg(p.slots + n) : n;
+  if (slot < 0) return;
+  if (slot >= p.nslots) {
+    if (tid == 0) gtr_flag(kStatusBadSlot);
+    return;
+  }
+  const int per_row = dv / 4, rows = kStepThreads / per_row;   // threads of a row; rows a pass
+  const int c4 = tid % per_row * 4, r0 = tid / per_row;
+  const size_t base = ((size_t)slot * p.H + h) * dk * dv;
+  const float* Si = p.state_in + base + c4;
+  float4 S[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = r0 + r * rows;
+    if (row < dk) S[r] = *reinterpret_cast<const float4*>(Si + (size_t)row * dv);
+  }
+  if (tid < dk) ks[tid] = ld_f((const T*)p.k + n * p.ldk + (long long)hk * dk + tid);
+  else if (tid >= 128 && tid < 128 + dk)
+    qs[tid - 128] = ld_f((const T*)p.q + n * p.ldq + (long long)hk * dk + tid - 128) * p.scale;
+  const T* vr = (const T*)p.v + n * p.ldv + (long long)h * dv + c4;
+  const float v0 = ld_f(vr), v1 = ld_f(vr + 1), v2 = ld_f(vr + 2), v3 = ld_f(vr + 3);
+  const float a = exp2f(load_decay(p, n, h));
+  __syncthreads();
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float* So = p.state_out + base + c4;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = r0 + r * rows;
+    if (row < dk) {
+      const float k = ks[row], q = qs[row];
+      float4 s = S[r];
+      s.x = fmaf(a, s.x, k * v0); s.y = fmaf(a, s.y, k * v1);
+      s.z = fmaf(a, s.z, k * v2); s.w = fmaf(a, s.w, k * v3);
+      *reinterpret_cast<float4*>(So + (size_t)row * dv) = s;
+      o.x = fmaf(q, s.x, o.x); o.y = fmaf(q, s.y, o.y);
+      o.z = fmaf(q, s.z, o.z); o.w = fmaf(q, s.w, o.w);
+    }
+  }
+  *reinterpret_cast<float4*>(red + r0 * dv + c4) = o;
+  __syncthreads();
+  float y = 0.f;
+  if (tid < dv) {
+    const int live = min(rows, dk);
+    for (int r = 0; r < live; ++r) y += red[r * dv + tid];
+  }
+  if (p.z) {
+    const float s = warp_sum(y * y);
+    if ((tid & 31) == 0 && tid < 128) osum[tid >> 5] = s;
+    __syncthreads();
+    if (tid < dv) {
+      float ss = 0.f;
+      for (int i = 0; i < (dv + 31) / 32; ++i) ss += osum[i];
+      y = y * rsqrtf(ss / (float)dv + kRmsEps) * (p.w ? p.w[tid] : 1.f) *
+          silu_f(ld_f((const T*)p.z + n * p.ldz + (long long)h * dv + tid));
+    }
+  }
+  if (tid < dv) ((T*)p.out)[n * p.ldo + (long long)h * dv + tid] = Elem<T>::from_f(y);
+}
+
+}  // namespace hla
+}  // namespace gtr

@@ -1,0 +1,279 @@
+// residual_norm.cu -- the norms around a residual branch with its gate and
+// scale, one pass over the rows (gtr_residual_norm).
+//
+//     r = y [/ sqrt(mean(y^2) + eps) * post_w] [* act(gate)]
+//     x_out = x + alpha * res_scale * r
+//     out = x_out / sqrt(mean(x_out^2) + eps) * pre_w
+//
+// Bytes bound it: x, y and gate are read once and x_out and out written once.
+// A row is held in the registers of its group of threads from the first load
+// to the last store, so the two means cost reductions and no second read; all
+// of a thread's loads are issued before the first is used.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "gtr_gla.h"
+#include "common.cuh"
+
+namespace {
+
+using namespace gtr;
+
+constexpr int kMaxD = 16384;             // 512 threads of 32 elements
+constexpr int kRowWarps = 8;            // rows per block where a warp has a row
+
+struct NormArgs {
+  const void* x; void* x_out; const void* y; const float* post_w; const void* gate;
+  const float* res_scale; const float* pre_w; void* out;
+  long long N, gate_rows;
+  int D, post_norm, act;
+  float alpha, eps;
+};
+
+// VEC consecutive elements as floats: 16-byte accesses for VEC = 8.
+template <typename T, int VEC> struct Pack {
+  static __device__ __forceinline__ void load(const T* p, float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+      v[0] = ld_f(p);
+    } else {
+      constexpr int kWords = VEC * (int)sizeof(T) / 16;
+      uint4 u[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) u[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+      T e[VEC];
+      memcpy(e, u, sizeof(e));
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = Elem<T>::to_f(e[i]);
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+      *p = Elem<T>::from_f(v[0]);
+    } else {
+      constexpr int kWords = VEC * (int)sizeof(T) / 16;
+      T e[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = Elem<T>::from_f(v[i]);
+      uint4 u[kWords];
+      memcpy(u, e, sizeof(e));
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+    }
+  }
+};
+// A weight vector: shared by every row, so it stays in the caches.
+template <int VEC> __device__ __forceinline__ void load_w(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = __ldg(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
+      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+    }
+  }
+}
+
+// Sum over the threads of a row: a warp (kWarpRow), or the whole block.
+template <bool kWarpRow>
+__device__ __forceinline__ float row_sum(float s, float* red) {
+  s = warp_sum(s);
+  if constexpr (!kWarpRow) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (lane == 0) red[warp] = s;
+    __syncthreads();
+    s = warp_sum(lane < nw ? red[lane] : 0.f);
+  }
+  return s;
+}
+
+// kV vectors of VEC elements per thread; vector j of a row is thread j % G's.
+template <typename TX, typename TY, int VEC, int kV, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 32 * kRowWarps : 512)
+residual_norm_kernel(const NormArgs a) {
+  __shared__ float red[2][32];
+  const int G = kWarpRow ? 32 : (int)blockDim.x;
+  const int t = kWarpRow ? (threadIdx.x & 31) : (int)threadIdx.x;
+  const long long row = kWarpRow ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
+                                 : (long long)blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  if (row >= a.N) return;                 // whole warps only where a block has several rows
+  const int nv = a.D / VEC;
+  const float inv_d = 1.0f / (float)a.D;
+  const TX* xr = (const TX*)a.x + row * a.D;
+  const TY* yr = a.y ? (const TY*)a.y + row * a.D : nullptr;
+  const TY* gr = a.gate ? (const TY*)a.gate + row / a.gate_rows * a.D : nullptr;
+  float x[kV][VEC], y[kV][VEC], gt[kV][VEC];
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    const int u = t + j * G;
+    if (u < nv) {
+      Pack<TX, VEC>::load(xr + (size_t)u * VEC, x[j]);
+      if (yr) Pack<TY, VEC>::load(yr + (size_t)u * VEC, y[j]);
+      if (gr) Pack<TY, VEC>::load(gr + (size_t)u * VEC, gt[j]);
+    }
+  }
+  if (yr) {
+    float inv = 1.f;
+    if (a.post_norm) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < kV; ++j)
+        if (t + j * G < nv)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) s = fmaf(y[j][e], y[j][e], s);
+      inv = rsqrtf(row_sum<kWarpRow>(s, red[0]) * inv_d + a.eps);
+    }
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      const int u = t + j * G;
+      if (u >= nv) continue;
+      float w[VEC];
+      if (a.post_norm) {
+        if (a.post_w) {
+          load_w<VEC>(a.post_w + u * VEC, w);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) y[j][e] *= inv * w[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) y[j][e] *= inv;
+        }
+      }
+      if (gr) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          // z sigmoid(z) and sigmoid(z) = 1 / (1 + e^-z)
+          const float z = gt[j][e];
+          const float sg = a.act == GTR_GATE_MUL ? z : 1.0f / (1.0f + __expf(-z));
+          y[j][e] *= a.act == GTR_GATE_SILU ? z * sg : sg;
+        }
+      }
+      if (a.res_scale) {
+        load_w<VEC>(a.res_scale + u * VEC, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) y[j][e] *= w[e];
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[j][e] = fmaf(a.alpha, y[j][e], x[j][e]);
+    }
+  }
+  TX* xo = (TX*)a.x_out + row * a.D;
+  if (yr || a.x_out != a.x) {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      const int u = t + j * G;
+      if (u < nv) Pack<TX, VEC>::store(xo + (size_t)u * VEC, x[j]);
+    }
+  }
+  if (!a.out) return;
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < kV; ++j)
+    if (t + j * G < nv)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s = fmaf(x[j][e], x[j][e], s);
+  const float inv = rsqrtf(row_sum<kWarpRow>(s, red[1]) * inv_d + a.eps);
+  TY* orow = (TY*)a.out + row * a.D;
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    const int u = t + j * G;
+    if (u >= nv) continue;
+    float w[VEC];
+    if (a.pre_w) {
+      load_w<VEC>(a.pre_w + u * VEC, w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) w[e] *= x[j][e] * inv;
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) w[e] = x[j][e] * inv;
+    }
+    Pack<TY, VEC>::store(orow + (size_t)u * VEC, w);
+  }
+}
+
+template <typename TX, typename TY, int VEC, int kV>
+int launch_v(const NormArgs& a, int threads, cudaStream_t st) {
+  if (threads == 32) {
+    const long long blocks = (a.N + kRowWarps - 1) / kRowWarps;
+    return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, true>, dim3((unsigned)blocks), dim3(32 * kRowWarps), 0,
+                      st, a);
+  }
+  return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, false>, dim3((unsigned)a.N), dim3((unsigned)threads), 0, st,
+                    a);
+}
+
+template <typename TX, typename TY>
+int launch_typed(const NormArgs& a, bool vec, cudaStream_t st) {
+  // threads of a row: 32 to 512 in powers of two, at most kPer elements each
+  const int kPer = 32;
+  int threads = 32;
+  while (threads * kPer < a.D) threads *= 2;
+  const int per = (a.D + threads - 1) / threads;   // elements per thread
+  if (vec) {
+    const int nv = (a.D / 8 + threads - 1) / threads;
+    if (nv <= 1) return launch_v<TX, TY, 8, 1>(a, threads, st);
+    if (nv <= 2) return launch_v<TX, TY, 8, 2>(a, threads, st);
+    return launch_v<TX, TY, 8, 4>(a, threads, st);
+  }
+  if (per <= 8) return launch_v<TX, TY, 1, 8>(a, threads, st);
+  return launch_v<TX, TY, 1, 32>(a, threads, st);
+}
+
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// [p, p + n) and [q, q + m) share a byte
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return p && q && n && m && a < b + m && b < a + n;
+}
+
+}  // namespace
+
+extern "C" GTR_API gtr_status_t gtr_residual_norm(const void* x, void* x_out, int x_dtype, const void* y, int post_norm,
+                                                  const float* post_w, const void* gate, int gate_act,
+                                                  long long gate_rows, const float* res_scale, float alpha,
+                                                  const float* pre_w, void* out, long long N, int D, float eps,
+                                                  int dtype, void* stream) {
+  if (x_dtype < 0 || x_dtype > 2 || dtype < 0 || dtype > 2) return GTR_ERR_INVALID_ARG;
+  if (N < 0 || D < 0 || gate_act < GTR_GATE_MUL || gate_act > GTR_GATE_SILU) return GTR_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || !(eps < 3.0e38f)) return GTR_ERR_INVALID_ARG;
+  if (x_dtype != GTR_F32 && x_dtype != dtype) return GTR_ERR_UNSUPPORTED;
+  if (D < 1 || D > kMaxD) return GTR_ERR_UNSUPPORTED;
+  if (N > 0x7fffffffLL) return GTR_ERR_INVALID_ARG;
+  if (N == 0) return GTR_OK;
+  if (!x || !x_out) return GTR_ERR_INVALID_ARG;
+  if (!y && (gate || post_norm || post_w || res_scale)) return GTR_ERR_INVALID_ARG;
+  if (post_w && !post_norm) return GTR_ERR_INVALID_ARG;
+  if (pre_w && !out) return GTR_ERR_INVALID_ARG;
+  if (gate && (gate_rows < 1 || N % gate_rows != 0)) return GTR_ERR_INVALID_ARG;
+  const size_t ex = x_dtype == GTR_F32 ? 4 : 2, ey = dtype == GTR_F32 ? 4 : 2;
+  const size_t nx = (size_t)N * D * ex, ny = (size_t)N * D * ey, nw = (size_t)D * 4;
+  const size_t ng = gate ? (size_t)(N / gate_rows) * D * ey : 0;
+  if (!aligned(x, ex) || !aligned(x_out, ex) || !aligned(y, ey) || !aligned(gate, ey) || !aligned(out, ey) ||
+      !aligned(post_w, 4) || !aligned(res_scale, 4) || !aligned(pre_w, 4))
+    return GTR_ERR_ALIGNMENT;
+  if ((x_out != x && overlap(x_out, nx, x, nx)) || overlap(x_out, nx, out, ny) || overlap(out, ny, x, nx))
+    return GTR_ERR_INVALID_ARG;
+  for (const void* w : {(const void*)x_out, (const void*)out}) {
+    const size_t n = w == (const void*)x_out ? nx : ny;
+    if (overlap(w, n, y, ny) || overlap(w, n, gate, ng) || overlap(w, n, post_w, nw) ||
+        overlap(w, n, res_scale, nw) || overlap(w, n, pre_w, nw))
+      return GTR_ERR_INVALID_ARG;
+  }
+  const bool vec = D % 8 == 0 && aligned(x, 16) && aligned(x_out, 16) && aligned(y, 16) && aligned(gate, 16) &&
+                   aligned(out, 16) && aligned(post_w, 16) && aligned(res_scale, 16) && aligned(pre_w, 16);
+  const NormArgs a{x, x_out, y, post_w, gate, res_scale, pre_w, out, N, gate ? gate_rows : 1, D, post_norm != 0,
+                   gate_act, alpha, eps};
+  const cudaStream_t st = (cudaStream_t)stream;
+  int rc;
+  if (x_dtype == GTR_F16) rc = launch_typed<__half, __half>(a, vec, st);
+  else if (x_dtype == GTR_BF16) rc = launch_typed<__nv_bfloat16, __nv_bfloat16>(a, vec, st);
+  else if (dtype == GTR_F32) rc = launch_typed<float, float>(a, vec, st);
+  else if (dtype == GTR_F16) rc = launch_typed<float, __half>(a, vec, st);
+  else rc = launch_typed<float, __nv_bfloat16>(a, vec, st);
+  return rc ? GTR_ERR_CUDA : GTR_OK;
+}

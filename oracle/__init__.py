@@ -319,3 +319,50 @@ def gtr_stack(x, blocks, *, gh: int, gw: int, H: int, tau: float = 16.0, directi
         d = STACK_DIRS[i % 4] if directions is None else directions[i]
         x = gtr_block(x, p, gh=gh, gw=gw, H=H, direction=d, tau=tau, act_dtype=act_dtype)
     return x
+
+
+def hla_fwd(q, k, v, g, z=None, w=None, *, cu_seqlens=None, scale=1.0, states=None, eps=1e-5):
+    """Linear attention with one decay per head, token by token in fp64.
+
+    q, k [T, Hk, dk], v, z [T, H, dv], g [T, H] or [H]: for every sequence (rows
+    cu_seqlens[n] .. cu_seqlens[n + 1]) and head, S_t = e^{g_t} S_{t-1} + k_t^T
+    v_t from states[n] (None: zero) and o_t = scale q_t S_t, then, with z,
+    RMSNorm(o) * w * SiLU(z).  Returns (out [T, H, dv], NaN outside the
+    sequences, final states [nseq, H, dk, dv])."""
+    f = lambda t: None if t is None else np.asarray(t.double().cpu() if hasattr(t, "cpu") else t, dtype=np.float64)  # noqa: E731
+    q, k, v, g, z, w, states = (f(t) for t in (q, k, v, g, z, w, states))
+    T, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    cu = [0, T] if cu_seqlens is None else [int(c) for c in cu_seqlens]
+    head = np.arange(H) // (H // Hk)
+    decay = np.exp(g)
+    out = np.full((T, H, dv), np.nan)
+    finals = np.zeros((len(cu) - 1, H, dk, dv))
+    for n in range(len(cu) - 1):
+        S = np.zeros((H, dk, dv)) if states is None else states[n].copy()
+        for t in range(cu[n], cu[n + 1]):
+            a = decay[t] if decay.ndim == 2 else decay
+            S = a[:, None, None] * S + k[t, head][:, :, None] * v[t][:, None, :]
+            out[t] = scale * np.einsum("hi,hij->hj", q[t, head], S)
+        finals[n] = S
+    if z is not None:
+        out = out / np.sqrt(np.mean(out * out, -1, keepdims=True) + eps) * (1.0 if w is None else w)
+        out = out * z / (1.0 + np.exp(-z))
+    return out, finals
+
+
+def residual_norm(x, y=None, *, post_norm=False, post_w=None, gate=None, gate_act="mul", res_scale=None, alpha=1.0,
+                  pre_w=None, eps=1e-5):
+    """(x_out, out) of the norms around a residual branch, in fp64: r = y or RMSNorm(y) post_w, times
+    act(gate) (gate rows repeated to x's), x_out = x + alpha res_scale r, out = RMSNorm(x_out) pre_w."""
+    f = lambda t: None if t is None else np.asarray(t.double().cpu() if hasattr(t, "cpu") else t, dtype=np.float64)  # noqa: E731
+    x, y, post_w, gate, res_scale, pre_w = (f(t) for t in (x, y, post_w, gate, res_scale, pre_w))
+    norm = lambda t, wt: t / np.sqrt(np.mean(t * t, -1, keepdims=True) + eps) * (1.0 if wt is None else wt)  # noqa: E731
+    if y is not None:
+        r = norm(y, post_w) if post_norm else y
+        if gate is not None:
+            gate = np.repeat(gate, x.shape[0] // gate.shape[0], axis=0)
+            sig = 1.0 / (1.0 + np.exp(-gate))
+            r = r * {"mul": gate, "sigmoid": sig, "silu": gate * sig}[gate_act]
+        x = x + alpha * r * (1.0 if res_scale is None else res_scale)
+    return x, norm(x, pre_w)

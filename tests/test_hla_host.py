@@ -1,0 +1,229 @@
+"""Head-decay linear attention and residual norm without a GPU: the oracle against
+other forms, the refusals of the C ABI and of the binding, the segment arithmetic."""
+import ctypes
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from linear_vision_backbone_b200 import binding, build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load()
+
+
+# ------------------------------------------------------------------- oracle
+def test_oracle_hla_equals_the_quadratic_form():
+    rng = np.random.default_rng(0)
+    T, Hk, H, dk, dv = 23, 2, 4, 5, 7
+    q, k = rng.normal(size=(2, T, Hk, dk))
+    v = rng.normal(size=(T, H, dv))
+    g = -rng.random((T, H))
+    S0 = rng.normal(size=(2, H, dk, dv))
+    cu = [2, 11, 20]                      # rows 0, 1 and 20.. belong to no sequence
+    out, final = oracle.hla_fwd(q, k, v, g, cu_seqlens=cu, scale=0.3, states=S0)
+    assert np.isnan(out[:2]).all() and np.isnan(out[20:]).all()
+    for n in range(2):
+        a, b = cu[n], cu[n + 1]
+        for h in range(H):
+            G = np.cumsum(g[a:b, h])
+            D = np.tril(np.exp(G[:, None] - G[None, :]))
+            want = 0.3 * ((q[a:b, h // 2] @ k[a:b, h // 2].T * D) @ v[a:b, h]
+                          + np.exp(G)[:, None] * (q[a:b, h // 2] @ S0[n, h]))
+            np.testing.assert_allclose(out[a:b, h], want, rtol=1e-12, atol=1e-12)
+            S = np.exp(G[-1]) * S0[n, h] + (k[a:b, h // 2] * np.exp(G[-1] - G)[:, None]).T @ v[a:b, h]
+            np.testing.assert_allclose(final[n, h], S, rtol=1e-12, atol=1e-12)
+
+
+def test_oracle_hla_equals_the_key_decay_oracle_with_equal_decays():
+    rng = np.random.default_rng(1)
+    T, H, d = 12, 2, 16
+    q, k, v, z = rng.normal(size=(4, 1, T, H, d))
+    g = -rng.random((1, T, H))
+    f = torch.from_numpy
+    full = oracle.gla_fwd(f(q).float(), f(k).float(), f(v).float(), f(np.repeat(g[..., None], d, -1)).float(),
+                          f(z).float(), None, gh=3, gw=4, direction="LR")
+    t32 = lambda a: a[0].astype(np.float32)  # noqa: E731
+    out, _ = oracle.hla_fwd(t32(q), t32(k), t32(v), t32(g), t32(z))
+    np.testing.assert_allclose(out, np.asarray(full)[0], rtol=1e-6, atol=1e-6)
+
+
+def test_oracle_residual_norm_equals_torch():
+    g = torch.Generator().manual_seed(2)
+    x, y = torch.randn(2, 6, 10, generator=g, dtype=torch.float64)
+    w1, w2, s = torch.randn(3, 10, generator=g, dtype=torch.float64)
+    gate = torch.randn(3, 10, generator=g, dtype=torch.float64)
+    xo, out = oracle.residual_norm(x, y, post_norm=True, post_w=w1, gate=gate, gate_act="silu", res_scale=s, alpha=0.5,
+                                   pre_w=w2)
+    rms = lambda t, w: torch.nn.functional.rms_norm(t, (10,), w, 1e-5)  # noqa: E731
+    want = x + 0.5 * s * rms(y, w1) * torch.nn.functional.silu(gate.repeat_interleave(2, 0))
+    np.testing.assert_allclose(xo, want.numpy(), rtol=1e-12)
+    np.testing.assert_allclose(out, rms(want, w2).numpy(), rtol=1e-12)
+
+
+# ----------------------------------------------------------------- refusals
+FIELDS = ["q", "k", "v", "g", "outgate", "rms_w", "out", "state_in", "state_out", "slots", "seen", "cu_seqlens",
+          "workspace", "workspace_bytes", "ldq", "ldk", "ldv", "ldz", "ldo", "nseq", "T", "Hk", "H", "dk", "dv",
+          "nslots", "g_per_head", "dtype", "scale"]
+
+
+def hla_args(**kw):
+    a = dict(q=4096, k=4096, v=4096, g=4096, outgate=0, rms_w=0, out=4096, state_in=0, state_out=0, slots=0, seen=0,
+             cu_seqlens=0, workspace=0, workspace_bytes=0, ldq=0, ldk=0, ldv=0, ldz=0, ldo=0, nseq=1, T=4, Hk=2, H=4,
+             dk=64, dv=64, nslots=0, g_per_head=0, dtype=1, scale=1.0)
+    a.update(kw)
+    return binding._HLA_ARGS.pack(*[a[n] for n in FIELDS])
+
+
+def test_hla_fwd_rejects_invalid_arguments_before_any_launch(lib):
+    call = lambda **kw: lib.gtr_hla_fwd(hla_args(**kw), None)  # noqa: E731
+    assert lib.gtr_hla_fwd(None, None) == -1
+    assert call(dtype=3) == -1
+    assert call(nseq=-1) == -1 and call(T=-1) == -1 and call(H=-1) == -1 and call(nslots=-1) == -1
+    assert call(dk=48) == -2 and call(dv=256) == -2
+    assert call(Hk=3) == -1 and call(Hk=0) == -1          # key heads must divide the heads
+    assert call(H=131072, Hk=1) == -2
+    assert call(nseq=3) == -1                             # equal sequences: nseq divides T
+    for name in ("q", "k", "v", "g", "out"):
+        assert call(**{name: 0}) == -1, name
+    assert call(rms_w=4096) == -1                         # a norm weight without a gate
+    assert call(state_in=4096, nslots=0) == -1            # a state per sequence
+    assert call(state_out=4096, nslots=0) == -1
+    assert call(state_in=1 << 20, state_out=(1 << 20) + 1024, nslots=1) == -1   # overlapping states
+    assert call(ldq=64) == -1                             # a pitch below the heads' width
+    assert call(ldv=260) == -3 and call(ldk=2 * 64 + 4) == -3   # pitch not a multiple of 16 bytes
+    assert call(ldo=1 << 40) == -1
+    for name in ("q", "k", "v", "outgate", "out", "workspace"):
+        assert call(**{name: 4104}) == -3, name
+    assert call(g=4098) == -3 and call(cu_seqlens=4097) == -3
+    # empty problems: pointers unused
+    assert call(nseq=0) == 0 and call(H=0, Hk=0) == 0
+    assert call(T=0, q=0, k=0, v=0, g=0, out=0) == 0
+
+
+def test_hla_step_rejects_invalid_arguments_before_any_launch(lib):
+    def call(**kw):
+        return lib.gtr_hla_step(hla_args(**dict(dict(nseq=4, state_in=1 << 20, state_out=1 << 20, nslots=4), **kw)),
+                                None)
+    assert call(nseq=3) == -1                             # one row per sequence
+    assert call(cu_seqlens=4096) == -1 and call(seen=4096) == -1
+    assert call(state_in=0) == -1 and call(state_out=0) == -1
+    assert call(nslots=3) == -1
+    assert call(dk=8) == -2
+    assert call(state_in=(1 << 20) + 8) == -3
+    assert call(nseq=0, T=0) == 0
+
+
+def test_hla_workspace_size(lib):
+    ws = lib.gtr_hla_workspace_bytes
+    bad = ctypes.c_size_t(-1).value
+    assert ws(-1, 4, 4, 64, 64, 1) == bad and ws(1, 4, 4, 48, 64, 1) == bad and ws(1, 4, 4, 64, 64, 7) == bad
+    assert ws(0, 4, 4, 64, 64, 1) == 0 and ws(1, 0, 4, 64, 64, 1) == 0 and ws(1, 4, 0, 64, 64, 1) == 0
+
+
+def test_residual_norm_rejects_invalid_arguments_before_any_launch(lib):
+    names = ["x", "x_out", "x_dtype", "y", "post_norm", "post_w", "gate", "gate_act", "gate_rows", "res_scale",
+             "alpha", "pre_w", "out", "N", "D", "eps", "dtype", "stream"]
+    base = dict(x=1 << 20, x_out=1 << 20, x_dtype=0, y=2 << 20, post_norm=0, post_w=None, gate=None, gate_act=0,
+                gate_rows=1, res_scale=None, alpha=1.0, pre_w=None, out=3 << 20, N=4, D=64, eps=1e-5, dtype=1,
+                stream=None)
+
+    def call(**kw):
+        a = dict(base, **kw)
+        return lib.gtr_residual_norm(*[a[n] for n in names])
+    assert call(x_dtype=5) == -1 and call(dtype=-1) == -1
+    assert call(N=-1) == -1 and call(D=-1) == -1 and call(N=1 << 32) == -1
+    assert call(D=0) == -2 and call(D=16385) == -2
+    assert call(x_dtype=1, dtype=2) == -2                 # a 16-bit stream has its branch's type
+    assert call(gate_act=3) == -1
+    assert call(eps=-1.0) == -1 and call(eps=float("nan")) == -1
+    assert call(x=None) == -1 and call(x_out=None) == -1
+    assert call(post_w=4 << 20) == -1                     # a weight without its norm
+    assert call(pre_w=4 << 20, out=None) == -1
+    assert call(y=None, post_norm=1) == -1 and call(y=None, gate=4 << 20) == -1 and call(y=None, res_scale=4 << 20) == -1
+    assert call(gate=4 << 20, gate_rows=3) == -1 and call(gate=4 << 20, gate_rows=0) == -1
+    assert call(x=(1 << 20) + 2, x_out=(1 << 20) + 2) == -3 and call(y=(2 << 20) + 1) == -3
+    assert call(x_out=(1 << 20) + 256) == -1              # x_out over part of x
+    assert call(out=1 << 20) == -1 and call(out=2 << 20) == -1
+    assert call(gate=3 << 20) == -1                       # out over the gate
+    assert call(N=0, x=None, x_out=None) == 0
+
+
+def test_binding_refuses_what_is_not_a_cuda_tensor():
+    t = torch.zeros(4, 2, 64)
+    with pytest.raises(ValueError, match="q must be"):
+        binding.hla_fwd(t, t, t, torch.zeros(4, 2))
+    with pytest.raises(ValueError, match="q must be"):
+        binding.hla_step(t, t, t, torch.zeros(4, 2), torch.zeros(4, 2, 64, 64))
+    with pytest.raises(ValueError, match="state_in"):
+        binding.hla_step(t, t, t, torch.zeros(4, 2), None)
+    with pytest.raises(ValueError, match="x must be"):
+        binding.residual_norm(torch.zeros(4, 64))
+
+
+def test_argument_struct_has_the_headers_size(tmp_path):
+    import subprocess
+    src = tmp_path / "s.c"
+    src.write_text(f'#include "{build.INCLUDE}/gtr_gla.h"\n#include <stdio.h>\n'
+                   'int main(void) { printf("%zu %zu", sizeof(gtr_hla_args), offsetof(gtr_hla_args, nseq)); }\n')
+    subprocess.run(["gcc", str(src), "-o", str(tmp_path / "s")], check=True)
+    size, nseq = map(int, subprocess.run([str(tmp_path / "s")], check=True, capture_output=True).stdout.split())
+    assert size == binding._HLA_ARGS.size
+    assert nseq == 13 * 8 + 8 + 5 * 8
+
+
+# ------------------------------------------------------- segment arithmetic
+def _segments(cu, T, L):
+    """The kernels' slot and workspace arithmetic (hla_common.cuh), for one cu_seqlens."""
+    nseq = len(cu) - 1
+    a = [min(max(c, 0), T) for c in cu[:-1]]
+    b = [min(max(c, x), T) for c, x in zip(cu[1:], a)]
+    found = []
+    for s in range(T // L + nseq):
+        count = sum(x // L + j <= s for j, x in enumerate(a))
+        if count == 0:
+            continue
+        n = count - 1
+        m = -(-(b[n] - a[n]) // L)
+        i = s - (a[n] // L + n)
+        if 0 <= i < max(m, 1):
+            found.append((n, i, m, a[n] // L + i))
+    return a, b, found
+
+
+def test_segment_slots_and_summaries_are_distinct_and_in_range():
+    rng = random.Random(3)
+    for _ in range(400):
+        L = rng.choice([128, 256, 1280])
+        lens = [rng.choice([0, 1, L - 1, L, L + 1, rng.randrange(5 * L)]) for _ in range(rng.randrange(1, 9))]
+        cu = [rng.randrange(3)]
+        for n in lens:
+            cu.append(cu[-1] + n)
+        T = cu[-1] + rng.randrange(3)
+        a, b, found = _segments(cu, T, L)
+        want = {(n, i) for n in range(len(lens)) for i in range(max(1, -(-lens[n] // L)))}
+        assert {(n, i) for n, i, _, _ in found} == want and len(found) == len(want)
+        entries = [w for _, i, m, w in found if i < m - 1]
+        assert len(set(entries)) == len(entries) and all(0 <= w < T // L + 1 for w in entries)
+        # the scan finds each sequence of several segments from its first entry
+        for n in range(len(lens)):
+            if -(-lens[n] // L) > 1:
+                last = sum(x // L <= a[n] // L for x in a) - 1
+                assert last == n
+
+
+def test_malformed_offsets_stay_in_range():
+    rng = random.Random(4)
+    for _ in range(300):
+        L, T = 128, rng.randrange(1, 2000)
+        cu = [rng.randrange(-3000, 5000) for _ in range(rng.randrange(2, 8))]
+        a, b, found = _segments(cu, T, L)
+        for n, i, m, w in found:
+            assert 0 <= a[n] + i * L <= T and 0 <= a[n] <= b[n] <= T
+            if i < m - 1:
+                assert 0 <= w < T // L + 1
