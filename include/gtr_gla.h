@@ -415,7 +415,7 @@ GTR_API gtr_status_t gtr_stack_fwd(float *x, const gtr_block_weights *blocks, in
  *     negative slot are skipped.
  * Errors: GTR_ERR_INVALID_ARG (NULL, negative or inconsistent sizes, Hk not
  * dividing H), GTR_ERR_UNSUPPORTED (head dims), GTR_ERR_ALIGNMENT (q, k, v,
- * outgate, out, states or workspace not 16-byte aligned, or a row pitch that is
+ * outgate, rms_w, out, states or workspace not 16-byte aligned, or a row pitch that is
  * not a multiple of 16 bytes), GTR_ERR_NO_MEMORY (workspace too small).
  */
 typedef struct gtr_hla_args {

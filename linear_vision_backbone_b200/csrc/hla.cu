@@ -1,12 +1,16 @@
 // hla.cu -- linear attention with one decay per head: the C ABI of
 // gtr_hla_fwd (prompts) and gtr_hla_step (single tokens), their argument
-// checks, the segment plan and the launches.  Kernels: hla_simt.cuh (fp32 CUDA
-// cores), hla_common.cuh (the scan over segments).
+// checks, the segment plan and the launches.  Kernels: hla_tc.cuh (tensor
+// cores), hla_simt.cuh (fp32 CUDA cores), hla_common.cuh (the scan over
+// segments).
+#include <cuda.h>
+
 #include <atomic>
 
 #include "gtr_gla.h"
 #include "hla_common.cuh"
 #include "hla_simt.cuh"
+#include "hla_tc.cuh"
 
 namespace {
 
@@ -31,39 +35,145 @@ int device_sms(int* sms) {
   return GTR_OK;
 }
 
+// 16-bit types and head dims the tensor-core kernels take
+bool tc_shape(int dk, int dv, int dtype) { return dtype != GTR_F32 && dk >= 64 && dv >= 64; }
+
 // Tokens per segment and what follows from it.
 struct Plan {
-  int L;               // tokens per segment
-  int nslot;           // segment slots (grid of the kernels)
-  long long entries;   // summaries
-  size_t off_a, bytes; // workspace: summaries, then log-decays
+  int L;                      // tokens per segment
+  int nslot;                  // segment slots (work items of a head)
+  long long entries;          // summaries
+  size_t off_0, off_a, bytes; // workspace: summaries, initial states, log-decays
 };
 
-// The plan without cu_seqlens knows every length (T / nseq); with it, only
-// their sum.  Shorter segments spread a long sequence over more SMs; each
-// costs the summary of its tokens a second time, so a call whose sequences
-// and heads fill the GPU takes long ones: L is about the tokens an SM gets
-// when the work is spread evenly.
-void make_plan(int nseq, int T, int H, int dk, int dv, bool equal, int sms, Plan* p) {
-  const long long per_sm = 4;                                // resident blocks
-  long long L = ((long long)T * H + sms * per_sm - 1) / (sms * per_sm);
-  L = (L + hla::kC - 1) / hla::kC * hla::kC;
-  if (L < hla::kC) L = hla::kC;
-  const long long longest = equal ? T / nseq : T;
-  long long cap = (longest + hla::kC - 1) / hla::kC * hla::kC;   // one segment holds any sequence
-  if (cap < hla::kC) cap = hla::kC;
-  if (L > cap) L = cap;
+// Shorter segments spread a long sequence over more SMs; each costs the
+// summary of its tokens, k and v read a second time.  `units`: blocks of
+// threads a segment slot takes, `slots`: resident blocks of threads.
+//
+// Lengths known (equal ones, or one sequence): the number m of segments that
+// minimises rounds x (blocks of 128 tokens of a segment + kStart), half as
+// much again for the summaries of m > 1, and kExtra for their two launches,
+// in units of one block of tokens.  The constants are fitted to measurements
+// of the tensor-core kernels: an item's first block costs about two more, the
+// two launches about four.
+// Only the sum of the lengths known: about half the tokens an SM gets, so the
+// longest segment adds at most a third to the time of an even spread.
+int segment_blocks(long long nseq, long long T, long long units, long long slots, bool known) {
+  const long long len = known ? (T + nseq - 1) / nseq : T;
+  const long long nb = (len + hla::kC - 1) / hla::kC;
+  if (nb <= 1) return 1;
+  if (!known) {
+    const long long share = ((T / hla::kC + nseq) * units / slots + 1) / 2;
+    return (int)(share < 1 ? 1 : share < nb ? share : nb);
+  }
+  constexpr double kStart = 2.0, kExtra = 4.0;
+  double best = 0;
+  long long best_b = nb;
+  for (long long m = 1; m <= nb && m <= 4096; ++m) {
+    const long long b = (nb + m - 1) / m;
+    const long long items = nseq * units * ((nb + b - 1) / b);
+    const double rounds = (double)((items + slots - 1) / slots);
+    double cost = rounds * ((double)b + kStart);
+    if (m > 1) cost = 1.5 * cost + kExtra;
+    if (m == 1 || cost < best) { best = cost; best_b = b; }
+  }
+  return (int)best_b;
+}
+
+void make_plan(int nseq, int T, int H, int dk, int dv, int dtype, bool equal, int sms, Plan* p) {
+  const bool tc = tc_shape(dk, dv, dtype);
+  const long long units = (long long)H * (tc ? dv / 64 : 1), slots = (long long)sms * (tc ? 1 : 4);
+  const long long L = (long long)segment_blocks(nseq, T, units, slots, equal || nseq == 1) * hla::kC;
   p->L = (int)(L < (1ll << 30) ? L : (1ll << 30));
   if (equal) {
-    const long long m = (longest + p->L - 1) / p->L;
+    const long long m = ((long long)(T / nseq) + p->L - 1) / p->L;
     p->nslot = (int)(nseq * (m > 1 ? m : 1));
     p->entries = m > 1 ? nseq * (m - 1) : 0;
   } else {
     p->nslot = T / p->L + nseq;
     p->entries = T > p->L ? T / p->L + 1 : 0;
   }
-  p->off_a = (size_t)p->entries * H * dk * dv * sizeof(float);
+  p->off_0 = (size_t)p->entries * H * dk * dv * sizeof(float);
+  p->off_a = 2 * p->off_0;
   p->bytes = p->off_a + (size_t)p->entries * H * sizeof(float);
+}
+
+// ---- tensor-core launches
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+  static std::atomic<EncodeTiledFn> fn{nullptr};
+  EncodeTiledFn f = fn.load();
+  if (!f) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess && ptr) {
+      f = (EncodeTiledFn)ptr;
+      fn.store(f);
+    } else {
+      (void)cudaGetLastError();
+    }
+  }
+  return f;
+}
+// [T][heads][d] 16-bit rows of pitch ld elements, as boxes of 128 tokens x 64
+// columns of one head in the 128-byte swizzle; tokens past T read as zero.
+int map_rows(CUtensorMap* map, int dtype, const void* base, int T, int heads, int d, long long ld) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return GTR_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)hla::kC};
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = enc(map, dtype == GTR_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                         const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GTR_OK : GTR_ERR_CUDA;
+}
+
+template <typename T, int DK, bool kSum, bool kPair>
+int launch_tc_kernel(const hla::Params& p, const hla::Maps& maps, int halves, int sms, cudaStream_t st) {
+  constexpr int smem = hla::Layout<T, DK, kSum>::kSmem;
+  const auto kern = hla::hla_tc<T, DK, kSum, kPair>;
+  static std::atomic<bool> done[kMaxDevices];
+  int dev;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GTR_ERR_CUDA;
+  if (!done[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return GTR_ERR_CUDA;
+    done[dev].store(true, std::memory_order_relaxed);
+  }
+  const long long items = (long long)p.nslot * p.H * halves;
+  const long long most = sms / halves * halves;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items < most ? items : most));
+  cfg.blockDim = dim3(kSum ? hla::kSumThreads : hla::kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, maps, halves) == cudaSuccess ? GTR_OK : GTR_ERR_CUDA;
+}
+template <typename T, int DK>
+int launch_tc_dk(const hla::Params& p, const hla::Maps& maps, bool sum, int sms, cudaStream_t st) {
+  const int halves = p.dv / 64;
+  if (sum) return launch_tc_kernel<T, DK, true, false>(p, maps, halves, sms, st);
+  if (halves == 2 && p.z) return launch_tc_kernel<T, DK, false, true>(p, maps, halves, sms, st);
+  return launch_tc_kernel<T, DK, false, false>(p, maps, halves, sms, st);
+}
+int launch_tc(const hla::Params& p, const hla::Maps& maps, int dtype, bool sum, int sms, cudaStream_t st) {
+  if (dtype == GTR_F16)
+    return p.dk == 64 ? launch_tc_dk<__half, 64>(p, maps, sum, sms, st) : launch_tc_dk<__half, 128>(p, maps, sum, sms, st);
+  return p.dk == 64 ? launch_tc_dk<__nv_bfloat16, 64>(p, maps, sum, sms, st)
+                    : launch_tc_dk<__nv_bfloat16, 128>(p, maps, sum, sms, st);
 }
 
 template <typename T, int ROWS>
@@ -133,7 +243,7 @@ int check_args(const gtr_hla_args* a, bool step, hla::Params* p, bool* empty) {
   }
   if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->outgate, 16) ||
       !aligned(a->out, 16) || !aligned(a->state_in, 16) || !aligned(a->state_out, 16) ||
-      !aligned(a->workspace, 16) || !aligned(a->g, 4) || !aligned(a->rms_w, 4) || !aligned(a->slots, 4) ||
+      !aligned(a->workspace, 16) || !aligned(a->rms_w, 16) || !aligned(a->g, 4) || !aligned(a->slots, 4) ||
       !aligned(a->seen, 4) || !aligned(a->cu_seqlens, 4))
     return GTR_ERR_ALIGNMENT;
   if (a->state_in && a->state_out && a->state_in != a->state_out) {
@@ -142,7 +252,7 @@ int check_args(const gtr_hla_args* a, bool step, hla::Params* p, bool* empty) {
     if (x < y + n && y < x + n) return GTR_ERR_INVALID_ARG;
   }
   *p = hla::Params{a->q, a->k, a->v, a->g, a->outgate, a->rms_w, a->out, a->state_in, a->state_out, a->slots, a->seen,
-                   a->cu_seqlens, nullptr, nullptr, ld[0], ld[1], ld[2], ld[3], ld[4], a->nseq, a->T, a->Hk, a->H,
+                   a->cu_seqlens, nullptr, nullptr, nullptr, ld[0], ld[1], ld[2], ld[3], ld[4], a->nseq, a->T, a->Hk, a->H,
                    a->dk, a->dv, a->nslots, a->g_per_head != 0, a->scale, 0, 0};
   *empty = false;
   return GTR_OK;
@@ -170,10 +280,10 @@ GTR_API size_t gtr_hla_workspace_bytes(int nseq, int T, int H, int dk, int dv, i
   int sms;
   if (device_sms(&sms)) return (size_t)-1;
   Plan a;
-  make_plan(nseq, T, H, dk, dv, false, sms, &a);
+  make_plan(nseq, T, H, dk, dv, dtype, false, sms, &a);
   if (T % nseq != 0) return a.bytes;
   Plan b;
-  make_plan(nseq, T, H, dk, dv, true, sms, &b);
+  make_plan(nseq, T, H, dk, dv, dtype, true, sms, &b);
   return a.bytes > b.bytes ? a.bytes : b.bytes;
 }
 
@@ -185,21 +295,33 @@ GTR_API gtr_status_t gtr_hla_fwd(const gtr_hla_args* args, void* stream) {
   int sms;
   if (int rc = device_sms(&sms)) return (gtr_status_t)rc;
   Plan pl;
-  make_plan(p.nseq, p.T, p.H, p.dk, p.dv, !p.cu, sms, &pl);
+  make_plan(p.nseq, p.T, p.H, p.dk, p.dv, args->dtype, !p.cu, sms, &pl);
   if (pl.bytes > 0 && !args->workspace) return GTR_ERR_INVALID_ARG;
   if (args->workspace_bytes < pl.bytes) return GTR_ERR_NO_MEMORY;
   p.L = pl.L;
   p.nslot = pl.nslot;
   p.wsS = (float*)args->workspace;
+  p.ws0 = (float*)((char*)args->workspace + pl.off_0);
   p.wsA = (float*)((char*)args->workspace + pl.off_a);
   const cudaStream_t st = (cudaStream_t)stream;
+  // an empty call (T = 0) only copies states: no tensor to map
+  const bool tc = tc_shape(p.dk, p.dv, args->dtype) && p.T > 0;
+  hla::Maps maps;
+  if (tc && (map_rows(&maps.q, args->dtype, p.q, p.T, p.Hk, p.dk, p.ldq) ||
+             map_rows(&maps.k, args->dtype, p.k, p.T, p.Hk, p.dk, p.ldk) ||
+             map_rows(&maps.v, args->dtype, p.v, p.T, p.H, p.dv, p.ldv) ||
+             map_rows(&maps.z, args->dtype, p.z ? p.z : p.v, p.T, p.H, p.dv, p.z ? p.ldz : p.ldv)))
+    return GTR_ERR_CUDA;
+  const auto launch = [&](bool sum) {
+    return tc ? launch_tc(p, maps, args->dtype, sum, sms, st) : launch_prompt(p, args->dtype, sum, st);
+  };
   if (pl.entries > 0) {
-    if (launch_prompt(p, args->dtype, true, st)) return GTR_ERR_CUDA;
+    if (launch(true)) return GTR_ERR_CUDA;
     const unsigned eb = (unsigned)((p.dk * p.dv / 4 + hla::kScanThreads - 1) / hla::kScanThreads);
     if (launch_pdl(hla::hla_scan, dim3((unsigned)pl.entries, (unsigned)p.H, eb), dim3(hla::kScanThreads), 0, st, p))
       return GTR_ERR_CUDA;
   }
-  return launch_prompt(p, args->dtype, false, st) ? GTR_ERR_CUDA : GTR_OK;
+  return launch(false) ? GTR_ERR_CUDA : GTR_OK;
 }
 
 GTR_API gtr_status_t gtr_hla_step(const gtr_hla_args* args, void* stream) {

@@ -26,6 +26,7 @@ struct Params {
   const void* q; const void* k; const void* v; const float* g; const void* z; const float* w; void* out;
   const float* state_in; float* state_out; const int* slots; const int* seen; const int* cu;
   float* wsS; float* wsA;          // segment summaries [entry][H][dk][dv], summed log2-decays [entry][H]
+  float* ws0;                      // initial states of sequences of several segments [first entry][H][dk][dv]
   long long ldq, ldk, ldv, ldz, ldo;
   int nseq, T, Hk, H, dk, dv, nslots, g_per_head;
   float scale;
@@ -106,6 +107,17 @@ __device__ __forceinline__ bool find_segment(const Params& p, int s, Segment& g)
   return g.slot >= 0;
 }
 
+// The state a segment starts from, or null for zero.  A sequence of several
+// segments has the scan's copy of its initial state: in place, its last
+// segment may write the state before its first one has read it.
+__device__ __forceinline__ const float* start_state(const Params& p, const Segment& g, int h) {
+  const size_t hs = (size_t)p.dk * p.dv;
+  if (g.i > 0) return p.wsS + ((size_t)(g.ws + g.i - 1) * p.H + h) * hs;
+  if (!g.start) return nullptr;
+  if (g.m > 1) return p.ws0 + ((size_t)g.ws * p.H + h) * hs;
+  return p.state_in + ((size_t)g.slot * p.H + h) * hs;
+}
+
 // log2 of a decay: at most zero; below e^-110 nothing is left.  A NaN stays.
 __device__ __forceinline__ float log2_decay(float g) {
   g = g > 0.f ? 0.f : g;
@@ -159,8 +171,10 @@ __global__ void __launch_bounds__(kScanThreads) hla_scan(const Params p) {
   const int e = (blockIdx.z * kScanThreads + threadIdx.x) * 4;
   if (e >= per_state) return;
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.state_in && (!p.seen || __ldg(p.seen + n) > 0))
+  if (p.state_in && (!p.seen || __ldg(p.seen + n) > 0)) {
     S = *reinterpret_cast<const float4*>(p.state_in + ((size_t)slot * p.H + h) * per_state + e);
+    *reinterpret_cast<float4*>(p.ws0 + ((size_t)entry * p.H + h) * per_state + e) = S;
+  }
   const size_t step = (size_t)p.H * per_state;
   float* ws = p.wsS + ((size_t)entry * p.H + h) * per_state + e;
   const float* wa = p.wsA + (size_t)entry * p.H + h;

@@ -9,6 +9,7 @@ namespace hla {
 
 constexpr int kSimtThreads = 256;
 constexpr int kSimtBatch = 16;     // tokens staged in shared memory per pass
+constexpr float kLn2 = 0.6931471805599453f;
 
 __host__ __device__ inline int simt_smem_floats(int dk, int dv, bool sum) {
   return kSimtBatch * (1 + (sum ? 1 : 2) * dk + dv + (sum ? 0 : kSimtThreads));
@@ -25,7 +26,7 @@ template <typename T, int ROWS, bool kSum>
 __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
   extern __shared__ float sm[];
   const int dk = p.dk, dv = p.dv;
-  float* as = sm;                            // [batch] decays
+  float* as = sm;                            // [batch] log-decays
   float* ks = as + kSimtBatch;               // [batch][dk]
   float* qs = ks + kSimtBatch * dk;          // [batch][dk], outputs only
   float* vs = qs + (kSum ? 0 : kSimtBatch * dk);   // [batch][dv]
@@ -41,9 +42,7 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
   const size_t hs = (size_t)dk * dv;
   float S[ROWS];
   {
-    const float* src = nullptr;
-    if (!kSum && g.i > 0) src = p.wsS + ((size_t)(g.ws + g.i - 1) * p.H + h) * hs;
-    else if (!kSum && g.start) src = p.state_in + ((size_t)g.slot * p.H + h) * hs;
+    const float* src = kSum ? nullptr : start_state(p, g, h);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) S[r] = src ? src[(size_t)(r0 + r) * dv + j] : 0.f;
   }
@@ -64,14 +63,19 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
     }
     __syncthreads();
     for (int t = 0; t < n; ++t) {
-      const float l = as[t], a = exp2f(l), v = vs[t * dv + j];
+      // S <- a S + k v as S + (a - 1) S + k v for a near one: rounding a itself
+      // would be the same relative error at every token, 2^-25 a token for as
+      // long as the state remembers
+      const float l = as[t], v = vs[t * dv + j];
+      const bool near_one = l > -1.f;
+      const float a = near_one ? expm1f(l * kLn2) : exp2f(l);
       total += l;
       const float* k = ks + t * dk + r0;
       const float* q = qs + t * dk + r0;
       float o = 0.f;
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
-        S[r] = fmaf(a, S[r], k[r] * v);
+        S[r] = fmaf(a, S[r], near_one ? fmaf(k[r], v, S[r]) : k[r] * v);
         if (!kSum) o = fmaf(q[r], S[r], o);
       }
       if (!kSum) part[t * kSimtThreads + tid] = o;

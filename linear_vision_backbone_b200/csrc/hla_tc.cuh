@@ -1,0 +1,855 @@
+// hla_tc.cuh -- the tensor-core (tcgen05) kernels of the head-decay linear
+// attention for prompts: 16-bit q, k, v, dk and dv of 64 or 128.
+//
+// Blocks of C = 128 tokens.  With l_t the log-decay of token t of a block, G_i
+// the inclusive sum of l up to token i, S the state before the block,
+//
+//   o_i = e^{G_i} q_i S + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j
+//   S  <- e^{G_C} S + sum_j k_j^T (e^{G_C - G_j} v_j)
+//
+// every factor at most one, so nothing overflows whatever the decays: the
+// sums G_C - G_j come from a suffix sum of their own, and e^{G_i - G_j} is a
+// product e^{G_i - G_b} e^{G_b - G_j} through the end b of j's 32 tokens where
+// i is past it (one exponential per row and 32 columns), and a single
+// exponential only in the 32 x 32 squares on the diagonal.
+//
+// Four matrix products per block, accumulated in fp32 in tensor memory, with
+// q, k and v as they are and every computed operand in 16-bit terms (x = hi +
+// lo [+ lo2], each the rounding of what is left):
+//   scores  = q k^T             M 128 tokens, N 128 tokens, K dk
+//   qs      = q [S hi | S lo]   M 128, N 64 + 64, K dk
+//   kv      = k^T [wv hi | wv lo (+ lo2)]  M dk, N 64 + 64, K 128 tokens
+//   pv      = P hi v + P lo v   M 128, N 64, K 128, P in tensor memory
+// Two bf16 terms carry 16 significant bits, so an output is off by about 2^-17
+// of its terms before its own rounding (one term would cost as much as that
+// rounding again); the state, which is returned in fp32, takes three.  fp16
+// terms are scaled by a power of two (per row of P, per block of wv, per S),
+// undone on the fp32 result, which keeps them in fp16's range: two are 22 bits.
+//
+// One block of threads per SM and 64 value columns of a head (dv = 128: two
+// blocks share a head, as a cluster when the norm needs the sum over both),
+// walking the blocks of 128 tokens of its segments.  18 warps, each group one
+// step of the pipeline, joined by mbarriers:
+//   0-3   scores -> decayed, masked P (a thread has a row)
+//   4-7   the decay sums; wv terms; zeros behind the last token
+//   8-11  the state: fp32 in registers (a thread has a row of 64 columns, or a
+//         half row), S <- a S + kv, and its terms for the next block's qs
+//   12-15 outputs: qs and pv joined, norm, gate, stores
+//   16    loads (TMA, 128-byte swizzled tiles of 128 rows x 64 columns)
+//   17    issues the products
+// The products of a block are issued scores, qs, kv, pv: while the P warps turn
+// block c's scores around, the tensor cores do its qs and kv.
+#pragma once
+#include "hla_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace gtr {
+namespace hla {
+
+using tc::saddr;
+
+constexpr int kTile = kC * 128;          // 128 rows x 64 16-bit columns: 16 KB
+constexpr int kTcThreads = 18 * 32;
+constexpr int kSumThreads = 10 * 32;
+
+struct Maps {
+  CUtensorMap q, k, v, z;
+};
+
+// mbarriers of a block of threads, in 8-byte units
+enum Bars {
+  kQF = 0, kQE = 2, kKF = 4, kKE = 7, kVF = 10, kVE = 13, kZF = 16, kZE = 18, kScF = 20, kPF = 21, kPvF = 22, kOE = 23,
+  kSF = 24, kSE = 25, kWF = 26, kWE = 27, kKvF = 28, kKvE = 29, kGF = 30, kGE = 32, kXF = 34, kXE = 35, kNumBars = 36
+};
+
+template <typename T, int DK, bool kSum> struct Layout {
+  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr int kTerms = kBf16 ? 3 : 2;       // of wv
+  static constexpr int kQTile = DK / 64 * kTile;
+  static constexpr int kNQ = kSum ? 0 : DK == 64 ? 2 : 1;   // stages: q of the next block comes from L2 for dk = 128
+  static constexpr int kNK = kSum ? 3 : 2;
+  static constexpr int kNV = kSum ? 3 : 2;
+  static constexpr int kNZ = DK == 64 ? 2 : 1;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + kNQ * kQTile;
+  static constexpr int kV = kK + kNK * kQTile;
+  static constexpr int kW = kV + kNV * kTile;
+  static constexpr int kS = kW + kTerms * kTile;      // S hi, S lo: dk rows x 64 columns each
+  static constexpr int kSTile = DK * 128;
+  static constexpr int kZ = kS + (kSum ? 0 : 2 * kSTile);   // z, then the outputs over it
+  static constexpr int kG = kZ + (kSum ? 0 : kNZ * kTile);         // [2][128] G
+  static constexpr int kU = kG + 2 * kC * 4;          // [2][128] e^{G_b - G_j}
+  static constexpr int kX = kU + 2 * kC * 4;          // [128] the other half's sums of squares
+  static constexpr int kMisc = kX + kC * 4;
+  // misc: warp sums [2][4], maxima [2][4], exponents of wv [2] and S [2], tensor memory address, barriers
+  static constexpr int kBars = kMisc + 96;
+  static constexpr int kPExp = kBars + kNumBars * 8;  // fp16: exponents of P [2][128], one byte each
+  static constexpr int kSmem = kPExp + (kBf16 ? 0 : 2 * kC);
+  static_assert(kSmem <= 232448, "shared memory of one block");
+};
+
+// Tensor memory columns (512)
+constexpr uint32_t kTmSc = 0;      // scores, then P hi in [0, 64)
+constexpr uint32_t kTmPlo = 128;   // P lo
+constexpr uint32_t kTmQS = 192;    // q S hi | q S lo
+constexpr uint32_t kTmPV = 320;
+constexpr uint32_t kTmKV = 384;    // kv hi | kv lo
+
+// Instruction descriptor, kind::f16, fp32 accumulation
+__host__ __device__ constexpr uint32_t idesc(bool bf16, int a_mn, int b_mn, int m, int n) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(saddr(dst)), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(saddr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0), "r"(c1),
+               "r"(c2)
+               : "memory");
+}
+
+// 32 lanes x 32 bit, N columns (thread t of warp w <- lane 32 (w % 4) + t); use after ld_wait
+__device__ __forceinline__ void tm_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// 16 lanes x 32 bit in two halves of 16 columns (the M = 64 accumulator: row r in lane 32 (r / 16) + r % 16)
+__device__ __forceinline__ void tm_ld16x2(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Waits for this thread's loads; the registers are operands, so that no use of them is scheduled before it.
+template <int N> __device__ __forceinline__ void tm_wait(uint32_t (&r)[N]) {
+  static_assert(N == 16 || N == 32, "");
+  if constexpr (N == 16)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])
+                 :
+                 : "memory");
+  else
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+template <typename T> struct T2;
+template <> struct T2<__half> {
+  using t = __half2;
+  static __device__ __forceinline__ t from(float a, float b) { return __floats2half2_rn(a, b); }
+  static __device__ __forceinline__ float2 to(t x) { return __half22float2(x); }
+};
+template <> struct T2<__nv_bfloat16> {
+  using t = __nv_bfloat162;
+  static __device__ __forceinline__ t from(float a, float b) { return __floats2bfloat162_rn(a, b); }
+  static __device__ __forceinline__ float2 to(t x) { return __bfloat1622float2(x); }
+};
+template <typename T> __device__ __forceinline__ uint32_t word(typename T2<T>::t x) {
+  uint32_t u;
+  memcpy(&u, &x, 4);
+  return u;
+}
+template <typename T> __device__ __forceinline__ float2 widen(uint32_t u) {
+  typename T2<T>::t x;
+  memcpy(&x, &u, 4);
+  return T2<T>::to(x);
+}
+// hi = T(x), lo = T(x - hi); a, b become what is left.
+template <typename T> __device__ __forceinline__ uint32_t term(float& a, float& b) {
+  const typename T2<T>::t h = T2<T>::from(a, b);
+  const float2 f = T2<T>::to(h);
+  a -= f.x;
+  b -= f.y;
+  return word<T>(h);
+}
+
+__device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void peer_store(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Bounded wait that acquires what the other block of the cluster released.
+__device__ __forceinline__ bool cluster_wait(uint64_t* b, uint32_t parity) {
+  const unsigned long long t0 = tc::globaltimer();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(saddr(b)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if (tc::globaltimer() - t0 > tc::kWaitNs) return false;
+  }
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One thread's columns of a state tile of dk rows x 64: M = 128 accumulators
+// give a thread a whole row, M = 64 ones two runs of 16 columns (32 apart).
+template <int DK> struct StateCols {
+  static constexpr int kN = DK == 128 ? 64 : 32;
+  // row, and first column of the 16-column run e
+  static __device__ __forceinline__ int row(int warp4, int lane) {
+    return DK == 128 ? warp4 * 32 + lane : warp4 * 16 + (lane & 15);
+  }
+  static __device__ __forceinline__ int col(int run, int lane) {
+    return DK == 128 ? run * 16 : run * 32 + (lane >> 4) * 16;
+  }
+};
+
+// kPair: the two halves of dv = 128 with a norm, as a cluster of two.
+template <typename T, int DK, bool kSum, bool kPair>
+__global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(const Params p,
+                                                                             const __grid_constant__ Maps maps,
+                                                                             const int halves) {
+  using L = Layout<T, DK, kSum>;
+  constexpr bool kBf16 = L::kBf16;
+  extern __shared__ __align__(1024) uint8_t tiles[];
+  uint8_t* sm = tiles;
+  float* Gs = reinterpret_cast<float*>(sm + L::kG);
+  float* Us = reinterpret_cast<float*>(sm + L::kU);
+  float* Xs = reinterpret_cast<float*>(sm + L::kX);
+  float* wsum = reinterpret_cast<float*>(sm + L::kMisc);           // [2][4]
+  float* wmax = wsum + 8;                                           // [4] builders, [4] state
+  int* ew = reinterpret_cast<int*>(wmax + 8);                       // [2] exponent of wv
+  int* es = ew + 2;                                                 // [2] exponent of S
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(es + 2);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBars);
+  int8_t* pexp = reinterpret_cast<int8_t*>(sm + L::kPExp);          // [2][128], fp16 only
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // roles: the summary has no score and output warps
+  const int role = kSum ? (warp < 4 ? 1 : warp < 8 ? 2 : warp - 4) : (warp < 16 ? warp >> 2 : warp - 12);
+  enum { kP = 0, kBuild = 1, kState = 2, kOut = 3, kLoad = 4, kMma = 5 };
+  if ((saddr(sm) & 1023u) != 0u) {
+    if (tid == 0) gtr_flag(kStatusBadShape);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) {
+      if (i < 2) { tc::mbar_init(bar + kQF + i, 1); tc::mbar_init(bar + kQE + i, 1); }
+      if (i < 2) { tc::mbar_init(bar + kZF + i, 1); tc::mbar_init(bar + kZE + i, kC); }
+      tc::mbar_init(bar + kKF + i, 1); tc::mbar_init(bar + kKE + i, 1);
+      tc::mbar_init(bar + kVF + i, 1); tc::mbar_init(bar + kVE + i, 1);
+    }
+    for (int b : {kScF, kPvF, kSE, kWE, kKvF}) tc::mbar_init(bar + b, 1);
+    for (int b : {kPF, kOE, kSF, kWF, kKvE}) tc::mbar_init(bar + b, 4);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar + kGF + i, 4);
+      tc::mbar_init(bar + kGE + i, kSum ? 4 : 12);
+    }
+    tc::mbar_init(bar + kXF, kC);
+    tc::mbar_init(bar + kXE, kC);
+    tc::mbar_fence_init();
+  }
+  if (role == kMma) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_before_sync();
+  __syncthreads();
+  tc::tc_after_sync();
+  if constexpr (kPair) cluster_sync();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tm = *tmem_slot;
+  const int half = (int)blockIdx.x % halves;
+  const int w4 = warp & 3, row = w4 * 32 + lane;               // a token row, or a lane of an accumulator
+  const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
+  const int group = p.H / p.Hk;
+  const bool gated = p.z != nullptr;
+  const long long units = (long long)p.nslot * p.H;
+  uint32_t it = 0;                                             // blocks of tokens since the start
+  bool ok = true;
+  auto wait = [&](int b, uint32_t parity) { return tc::mbar_wait(bar + b, parity); };
+  // one arrival for a warp, after all its lanes
+  auto warp_arrive = [&](int b) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive_one(bar + b);
+  };
+
+  for (long long unit = (int)blockIdx.x / halves; unit < units && ok; unit += (int)gridDim.x / halves) {
+    Segment g;
+    const int h = (int)(unit % p.H), hk = h / group;
+    if (!find_segment(p, (int)(unit / p.H), g)) continue;
+    const bool last = g.i >= g.m - 1;
+    if (kSum && last) continue;
+    const int nb = (g.len + kC - 1) / kC;
+    const bool want_end = kSum || (last && p.state_out);       // the state after the segment is needed
+
+    if (role == kLoad) {
+      if (lane == 0) {
+        for (int c = 0; c < nb && ok; ++c) {
+          const uint32_t i = it + c;
+          const int t = g.t0 + c * kC;
+          const int sk = i % L::kNK, sv = i % L::kNV;
+          ok = wait(kKE + sk, (i / L::kNK & 1) ^ 1);
+          if (!ok) break;
+          tc::mbar_arrive_tx(bar + kKF + sk, L::kQTile);
+          for (int x = 0; x < DK / 64; ++x)
+            tma_load_3d(sm + L::kK + sk * L::kQTile + x * kTile, &maps.k, x * 64, hk, t, bar + kKF + sk);
+          if constexpr (!kSum) {
+            if (L::kNQ == 1)
+              for (int x = 0; x < DK / 64; ++x) tma_prefetch_3d(&maps.q, x * 64, hk, t);
+          }
+          ok = wait(kVE + sv, (i / L::kNV & 1) ^ 1);
+          if (!ok) break;
+          tc::mbar_arrive_tx(bar + kVF + sv, kTile);
+          tma_load_3d(sm + L::kV + sv * kTile, &maps.v, half * 64, h, t, bar + kVF + sv);
+          if constexpr (!kSum) {
+            if (gated) {
+              const int sz = i % L::kNZ;
+              ok = wait(kZE + sz, (i / L::kNZ & 1) ^ 1);
+              if (!ok) break;
+              tc::mbar_arrive_tx(bar + kZF + sz, kTile);
+              tma_load_3d(sm + L::kZ + sz * kTile, &maps.z, half * 64, h, t, bar + kZF + sz);
+            }
+            const int sq = i % L::kNQ;
+            ok = wait(kQE + sq, (i / L::kNQ & 1) ^ 1);
+            if (!ok) break;
+            tc::mbar_arrive_tx(bar + kQF + sq, L::kQTile);
+            for (int x = 0; x < DK / 64; ++x)
+              tma_load_3d(sm + L::kQ + sq * L::kQTile + x * kTile, &maps.q, x * 64, hk, t, bar + kQF + sq);
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    } else if (role == kMma) {
+      if (lane == 0) {
+        constexpr uint32_t kIdSc = idesc(kBf16, 0, 0, 128, 128), kIdQS = idesc(kBf16, 0, 1, 128, 128);
+        constexpr uint32_t kIdKV = idesc(kBf16, 1, 1, DK, 128), kIdKV3 = idesc(kBf16, 1, 1, DK, 64);
+        constexpr uint32_t kIdPV = idesc(kBf16, 0, 1, 128, 64);
+        for (int c = 0; c < nb && ok; ++c) {
+          const uint32_t i = it + c, par = i & 1;
+          const int sk = i % L::kNK, sv = i % L::kNV;
+          const uint8_t* K = sm + L::kK + sk * L::kQTile;
+          const uint8_t* V = sm + L::kV + sv * kTile;
+          const uint8_t* W = sm + L::kW;
+          ok = wait(kKF + sk, i / L::kNK & 1);
+          if constexpr (!kSum) {
+            const int sq = i % L::kNQ;
+            const uint8_t* Q = sm + L::kQ + sq * L::kQTile;
+            ok = ok && wait(kQF + sq, i / L::kNQ & 1);
+            if (!ok) break;
+            tc::tc_after_sync();
+            const uint64_t aq = tc::sdesc(saddr(Q), 16, 1024), bk = tc::sdesc(saddr(K), 16, 1024);
+#pragma unroll
+            for (int s = 0; s < DK / 16; ++s) {
+              const uint64_t o = (uint64_t)((s >> 2) * (kTile >> 4) + (s & 3) * tc::kStepK);
+              tc::mma_f16(tm + kTmSc, aq + o, bk + o, kIdSc, s > 0);
+            }
+            tc::mma_commit(bar + kScF);
+            ok = wait(kSF, par) && wait(kOE, par ^ 1);          // S terms; qs and pv of the block before are read
+            if (!ok) break;
+            tc::tc_after_sync();
+            const uint64_t bs = tc::sdesc(saddr(sm + L::kS), L::kSTile, 1024);
+#pragma unroll
+            for (int s = 0; s < DK / 16; ++s) {
+              const uint64_t o = (uint64_t)((s >> 2) * (kTile >> 4) + (s & 3) * tc::kStepK);
+              tc::mma_f16(tm + kTmQS, aq + o, bs + s * tc::kStepMN, kIdQS, s > 0);
+            }
+            tc::mma_commit(bar + kQE + sq);
+            tc::mma_commit(bar + kSE);
+          }
+          ok = ok && wait(kWF, par) && wait(kKvE, par ^ 1);
+          if (!ok) break;
+          tc::tc_after_sync();
+          if (c + 1 < nb || want_end) {
+            const uint64_t ak = tc::sdesc(saddr(K), kTile, 1024), bw = tc::sdesc(saddr(W), kTile, 1024);
+#pragma unroll
+            for (int s = 0; s < kC / 16; ++s)
+              tc::mma_f16(tm + kTmKV, ak + s * tc::kStepMN, bw + s * tc::kStepMN, kIdKV, s > 0);
+            if (L::kTerms == 3) {
+              const uint64_t bw3 = tc::sdesc(saddr(W + 2 * kTile), kTile, 1024);
+#pragma unroll
+              for (int s = 0; s < kC / 16; ++s)
+                tc::mma_f16(tm + kTmKV + 64, ak + s * tc::kStepMN, bw3 + s * tc::kStepMN, kIdKV3, 1u);
+            }
+          }
+          tc::mma_commit(bar + kKvF);
+          tc::mma_commit(bar + kWE);
+          tc::mma_commit(bar + kKE + sk);
+          if constexpr (!kSum) {
+            ok = wait(kPF, par);
+            if (!ok) break;
+            tc::tc_after_sync();
+            const uint64_t bv = tc::sdesc(saddr(V), kTile, 1024);
+#pragma unroll
+            for (int s = 0; s < kC / 16; ++s)
+              tc::mma_f16_ts(tm + kTmPV, tm + kTmSc + 8 * s, bv + s * tc::kStepMN, kIdPV, s > 0);
+#pragma unroll
+            for (int s = 0; s < kC / 16; ++s)
+              tc::mma_f16_ts(tm + kTmPV, tm + kTmPlo + 8 * s, bv + s * tc::kStepMN, kIdPV, 1u);
+            tc::mma_commit(bar + kPvF);
+          }
+          tc::mma_commit(bar + kVE + sv);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    } else if (role == kBuild) {
+      float l = row < g.len ? load_decay(p, g.t0 + row, h) : 0.f;
+      for (int c = 0; c < nb && ok; ++c) {
+        const uint32_t i = it + c, par = i & 1;
+        const int nv = min(kC, g.len - c * kC);                  // tokens of this block
+        const float lc = l;
+        if (c + 1 < nb) {
+          const int r = (c + 1) * kC + row;
+          l = r < g.len ? load_decay(p, g.t0 + r, h) : 0.f;
+        }
+        // inclusive sums from the front, exclusive ones from the back
+        float pre = lc, suf = lc;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const float a = __shfl_up_sync(0xffffffffu, pre, d), b = __shfl_down_sync(0xffffffffu, suf, d);
+          if (lane >= d) pre += a;
+          if (lane + d < 32) suf += b;
+        }
+        if (lane == 31) wsum[(i & 1) * 4 + w4] = pre;
+        const float in_warp = __shfl_down_sync(0xffffffffu, suf, 1);
+        suf = lane == 31 ? 0.f : in_warp;
+        tc::named_barrier(1, 128);
+        const float* ws = wsum + (i & 1) * 4;
+        float G = pre, R = suf;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (x < w4) G += ws[x];
+          if (x > w4) R += ws[x];
+        }
+        ok = wait(kGE + (i & 1), (i >> 1 & 1) ^ 1);
+        if (!ok) break;
+        Gs[(i & 1) * kC + row] = G;
+        Us[(i & 1) * kC + row] = tc::ex2(suf);
+        warp_arrive(kGF + (i & 1));
+        const int sv = i % L::kNV, sk = i % L::kNK;
+        ok = wait(kVF + sv, i / L::kNV & 1);
+        if (!ok) break;
+        uint8_t* V = sm + L::kV + sv * kTile + row * 128;
+        const bool build = c + 1 < nb || want_end;
+        const bool live = row < nv;
+        const float w = tc::ex2(R);
+        uint4 v[8];
+        if (build) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const uint4*>(V + ((u ^ (row & 7)) << 4));
+        }
+        float up = 1.f;
+        int exp_w = 0;
+        if (!kBf16 && build) {
+          // a power of two that brings the block's largest |w v| under 2^15
+          float m = 0.f;
+          if (live) {
+            uint32_t mx = 0;                                     // |fp16| orders as its bits; a NaN or infinity on top
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx = __vmaxu2(mx, x[e] & 0x7fff7fffu);
+            }
+            const float2 f = widen<T>(mx);
+            m = fmaxf(f.x, f.y) * w;
+          }
+          m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+          if (lane == 0) wmax[w4] = m;
+          tc::named_barrier(1, 128);
+          const int e = tc::scale_exp(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])));
+          up = tc::pow2i(e);
+          exp_w = e;
+        }
+        ok = wait(kWE, par ^ 1);
+        if (!ok) break;
+        if (build) {
+          // the kv of the block before is done, so the one before that, with this slot's exponent, is read
+          if (!kBf16 && row == 0) ew[i & 1] = exp_w;
+          uint8_t* W = sm + L::kW + row * 128;
+          const float f = w * up;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            uint32_t t[L::kTerms][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float2 y = widen<T>(x[e]);
+              y.x = live ? y.x * f : 0.f;
+              y.y = live ? y.y * f : 0.f;
+#pragma unroll
+              for (int n = 0; n < L::kTerms; ++n) t[n][e] = term<T>(y.x, y.y);
+            }
+            const int off = (u ^ (row & 7)) << 4;
+#pragma unroll
+            for (int n = 0; n < L::kTerms; ++n)
+              *reinterpret_cast<uint4*>(W + n * kTile + off) = make_uint4(t[n][0], t[n][1], t[n][2], t[n][3]);
+          }
+        }
+        if (nv < kC) {
+          // rows behind the sequence's last token hold others' data: zeros, so
+          // that nothing of them (a NaN times a zero weight) enters a product
+          ok = wait(kKF + sk, i / L::kNK & 1);
+          if (!ok) break;
+          if (!live) {
+            uint8_t* K = sm + L::kK + sk * L::kQTile + row * 128;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              *reinterpret_cast<uint4*>(V + (u << 4)) = zero;
+#pragma unroll
+              for (int x = 0; x < DK / 64; ++x) *reinterpret_cast<uint4*>(K + x * kTile + (u << 4)) = zero;
+            }
+          }
+        }
+        tc::fence_async_smem();
+        warp_arrive(kWF);
+      }
+    } else if (role == kState) {
+      using SC = StateCols<DK>;
+      constexpr int kRuns = SC::kN / 16;
+      const int r = SC::row(w4, lane);
+      const size_t hs = (size_t)DK * p.dv;
+      float S[SC::kN];
+      {
+        const float* src = nullptr;
+        if (!kSum) src = start_state(p, g, h);
+#pragma unroll
+        for (int x = 0; x < kRuns; ++x) {
+          const size_t at = (size_t)r * p.dv + half * 64 + SC::col(x, lane);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 f = src ? *reinterpret_cast<const float4*>(src + at + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[16 * x + 4 * e] = f.x; S[16 * x + 4 * e + 1] = f.y;
+            S[16 * x + 4 * e + 2] = f.z; S[16 * x + 4 * e + 3] = f.w;
+          }
+        }
+      }
+      // S in two terms as the operand of block `i`'s qs
+      auto put = [&](uint32_t i) {
+        float up = 1.f;
+        if (!kBf16) {
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < SC::kN; ++e) m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(S[e]) & 0x7fffffffu));
+          m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+          if (lane == 0) wmax[4 + w4] = m;
+          tc::named_barrier(2, 128);
+          m = fmaxf(fmaxf(wmax[4], wmax[5]), fmaxf(wmax[6], wmax[7]));
+          tc::named_barrier(2, 128);                             // read before the next block's are written
+          const int e = tc::scale_exp(m);
+          up = tc::pow2i(e);
+          if (w4 == 0 && lane == 0) es[i & 1] = e;
+        }
+        if (!wait(kSE, (i & 1) ^ 1)) return false;
+        uint8_t* D = sm + L::kS + r * 128;
+#pragma unroll
+        for (int x = 0; x < kRuns; ++x) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float a0 = S[16 * x + 8 * b + 2 * e] * up, a1 = S[16 * x + 8 * b + 2 * e + 1] * up;
+              hi[e] = term<T>(a0, a1);
+              lo[e] = term<T>(a0, a1);
+            }
+            const int off = ((SC::col(x, lane) / 8 + b) ^ (r & 7)) << 4;
+            *reinterpret_cast<uint4*>(D + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(D + L::kSTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        tc::fence_async_smem();
+        warp_arrive(kSF);
+        return true;
+      };
+      if (!kSum && nb > 0) ok = put(it);
+      float total = 0.f;
+      for (int c = 0; c < nb && ok; ++c) {
+        const uint32_t i = it + c, par = i & 1;
+        ok = wait(kGF + (i & 1), i >> 1 & 1);
+        if (!ok) break;
+        const float la = Gs[(i & 1) * kC + kC - 1];
+        warp_arrive(kGE + (i & 1));
+        ok = wait(kKvF, par);
+        if (!ok) break;
+        tc::tc_after_sync();
+        if (c + 1 < nb || want_end) {
+          total += la;
+          const float a = tc::ex2(la);
+          const float down = kBf16 ? 1.f : tc::pow2i(-ew[i & 1]);
+#pragma unroll
+          for (int x = 0; x < kRuns; ++x) {
+            uint32_t hi[16], lo[16];
+            if constexpr (DK == 128) {
+              tm_ld16(tm + lane_base + kTmKV + 16 * x, hi);
+              tm_ld16(tm + lane_base + kTmKV + 64 + 16 * x, lo);
+            } else {
+              tm_ld16x2(tm + lane_base + kTmKV + 32 * x, hi);
+              tm_ld16x2(tm + lane_base + kTmKV + 64 + 32 * x, lo);
+            }
+            tm_wait(hi);
+            tm_wait(lo);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              S[16 * x + e] = fmaf(a, S[16 * x + e], (__uint_as_float(hi[e]) + __uint_as_float(lo[e])) * down);
+          }
+        }
+        tc::tc_before_sync();
+        warp_arrive(kKvE);
+        if (!kSum && c + 1 < nb) ok = put(i + 1);
+      }
+      if (ok && want_end) {
+        float* dst = kSum ? p.wsS + ((size_t)(g.ws + g.i) * p.H + h) * hs : p.state_out + ((size_t)g.slot * p.H + h) * hs;
+#pragma unroll
+        for (int x = 0; x < kRuns; ++x) {
+          float4* d4 = reinterpret_cast<float4*>(dst + (size_t)r * p.dv + half * 64 + SC::col(x, lane));
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            d4[e] = make_float4(S[16 * x + 4 * e], S[16 * x + 4 * e + 1], S[16 * x + 4 * e + 2], S[16 * x + 4 * e + 3]);
+        }
+        if (kSum && half == 0 && w4 == 0 && lane == 0) p.wsA[(size_t)(g.ws + g.i) * p.H + h] = total;
+      }
+    } else if (!kSum && role == kP) {
+      for (int c = 0; c < nb && ok; ++c) {
+        const uint32_t i = it + c, par = i & 1;
+        ok = wait(kGF + (i & 1), i >> 1 & 1) && wait(kScF, par);
+        if (!ok) break;
+        tc::tc_after_sync();
+        const float* G = Gs + (i & 1) * kC;
+        const float* U = Us + (i & 1) * kC;
+        const float Gi = G[row];
+        float up = 1.f;
+        if (!kBf16) {
+          // a power of two that brings the row's largest |score| under 2^15
+          uint32_t mx = 0;
+#pragma unroll 1
+          for (int b = 0; b <= w4; ++b) {
+            uint32_t s[32];
+            tm_ld32(tm + lane_base + kTmSc + 32 * b, s);
+            tm_wait(s);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx = max(mx, b < w4 || e <= lane ? s[e] & 0x7fffffffu : 0u);
+          }
+          const int e = tc::scale_exp(__uint_as_float(mx));
+          up = tc::pow2i(e);
+          pexp[(i & 1) * kC + row] = (int8_t)e;
+        }
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          uint32_t hi[16], lo[16];
+          if (b > w4) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0u;
+          } else {
+            uint32_t s[32];
+            tm_ld32(tm + lane_base + kTmSc + 32 * b, s);
+            tm_wait(s);
+            if (b == w4) {
+              const float4* g4 = reinterpret_cast<const float4*>(G + 32 * b);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 gj = g4[e];
+                const float d[4] = {gj.x, gj.y, gj.z, gj.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const float y = __uint_as_float(s[4 * e + x]) * (tc::ex2(Gi - d[x]) * up);
+                  s[4 * e + x] = 4 * e + x <= lane ? __float_as_uint(y) : 0u;
+                }
+              }
+            } else {
+              const float f = tc::ex2(Gi - G[32 * b + 31]) * up;
+              const float4* u4 = reinterpret_cast<const float4*>(U + 32 * b);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 uj = u4[e];
+                s[4 * e] = __float_as_uint(__uint_as_float(s[4 * e]) * (uj.x * f));
+                s[4 * e + 1] = __float_as_uint(__uint_as_float(s[4 * e + 1]) * (uj.y * f));
+                s[4 * e + 2] = __float_as_uint(__uint_as_float(s[4 * e + 2]) * (uj.z * f));
+                s[4 * e + 3] = __float_as_uint(__uint_as_float(s[4 * e + 3]) * (uj.w * f));
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float a0 = __uint_as_float(s[2 * e]), a1 = __uint_as_float(s[2 * e + 1]);
+              hi[e] = term<T>(a0, a1);
+              lo[e] = term<T>(a0, a1);
+            }
+          }
+          // hi over scores already read (columns [16 b, 16 b + 16) of block b / 2)
+          tm_st16(tm + lane_base + kTmSc + 16 * b, hi);
+          tm_st16(tm + lane_base + kTmPlo + 16 * b, lo);
+        }
+        tc::tmem_st_wait();
+        tc::tc_before_sync();
+        warp_arrive(kPF);
+        warp_arrive(kGE + (i & 1));
+      }
+    } else if (!kSum && role == kOut) {
+      const uint32_t rank = kPair ? blockIdx.x & 1u : 0u;
+      for (int c = 0; c < nb && ok; ++c) {
+        const uint32_t i = it + c, par = i & 1;
+        const int nv = min(kC, g.len - c * kC);
+        ok = wait(kGF + (i & 1), i >> 1 & 1);
+        if (!ok) break;
+        const float Gi = Gs[(i & 1) * kC + row];
+        warp_arrive(kGE + (i & 1));
+        ok = wait(kPvF, par);
+        if (!ok) break;
+        tc::tc_after_sync();
+        float f1 = p.scale * tc::ex2(Gi), f2 = p.scale;
+        if (!kBf16) {
+          f1 *= tc::pow2i(-es[i & 1]);
+          f2 *= tc::pow2i(-(int)pexp[(i & 1) * kC + row]);
+        }
+        float o[64];
+        float ss = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t a[16], b[16], d[16];
+          tm_ld16(tm + lane_base + kTmQS + 16 * x, a);
+          tm_ld16(tm + lane_base + kTmQS + 64 + 16 * x, b);
+          tm_ld16(tm + lane_base + kTmPV + 16 * x, d);
+          tm_wait(a);
+          tm_wait(b);
+          tm_wait(d);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float y = fmaf(f1, __uint_as_float(a[e]) + __uint_as_float(b[e]), f2 * __uint_as_float(d[e]));
+            o[16 * x + e] = y;
+            ss = fmaf(y, y, ss);
+          }
+        }
+        tc::tc_before_sync();
+        warp_arrive(kOE);
+        const int sz = i % L::kNZ;
+        uint8_t* Z = sm + L::kZ + sz * kTile;
+        float inv = 1.f;
+        if (gated) {
+          if constexpr (kPair) {
+            // the other half's sum of this row; its copy of ours is free once it has read the block before
+            ok = cluster_wait(bar + kXE, par ^ 1);
+            if (!ok) break;
+            peer_store(peer_addr(saddr(Xs + row), rank ^ 1u), ss);
+            peer_arrive(peer_addr(saddr(bar + kXF), rank ^ 1u));
+            ok = cluster_wait(bar + kXF, par);
+            if (!ok) break;
+            ss += *reinterpret_cast<volatile float*>(Xs + row);
+            peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));
+          }
+          inv = rsqrtf(ss / (float)p.dv + kRmsEps);
+          ok = wait(kZF + sz, i / L::kNZ & 1);
+          if (!ok) break;
+        } else {
+          // the copies of the block that used this buffer before are done
+          tc::named_barrier(3, 128);
+        }
+        const float4* w4p = reinterpret_cast<const float4*>(p.w + half * 64);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          uint4* unit16 = reinterpret_cast<uint4*>(Z + row * 128 + ((u ^ (row & 7)) << 4));
+          if (gated) {
+            const uint4 zu = *unit16;
+            const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
+            float wt[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+            if (p.w) {
+              const float4 wa = __ldg(w4p + 2 * u), wb = __ldg(w4p + 2 * u + 1);
+              wt[0] = wa.x; wt[1] = wa.y; wt[2] = wa.z; wt[3] = wa.w;
+              wt[4] = wb.x; wt[5] = wb.y; wt[6] = wb.z; wt[7] = wb.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 z = widen<T>(zw[e]);
+              o[8 * u + 2 * e] *= inv * wt[2 * e] * __fdividef(z.x, 1.0f + __expf(-z.x));
+              o[8 * u + 2 * e + 1] *= inv * wt[2 * e + 1] * __fdividef(z.y, 1.0f + __expf(-z.y));
+            }
+          }
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = word<T>(T2<T>::from(o[8 * u + 2 * e], o[8 * u + 2 * e + 1]));
+          *unit16 = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        tc::named_barrier(3, 128);
+        {
+          const int u = row & 7;
+          T* dst = (T*)p.out + (long long)(g.t0 + c * kC) * p.ldo + (long long)h * p.dv + half * 64 + u * 8;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = (row >> 3) + 16 * e;
+            if (r < nv)
+              *reinterpret_cast<uint4*>(dst + r * p.ldo) =
+                  *reinterpret_cast<const uint4*>(Z + r * 128 + ((u ^ (r & 7)) << 4));
+          }
+        }
+        if (gated) {
+          tc::fence_async_smem();                               // the next z is written by the async proxy
+          tc::mbar_arrive_one(bar + kZE + sz);
+        }
+      }
+    }
+    it += nb;
+  }
+  // a bounded wait that ran out ends every warp's walk the same way; loads and
+  // products in flight are waited for (bounded) before the memory is given up
+  if (!ok && lane == 0) gtr_flag(kStatusMbarTimeout);
+  __syncwarp();
+  if (role == kMma && ok && it > 0) {
+    // the last arrival a product makes on this memory
+    const uint32_t i = it - 1;
+    ok = wait(kVE + i % L::kNV, i / L::kNV & 1);
+    if (!ok && lane == 0) gtr_flag(kStatusMbarTimeout);
+  }
+  if (role == kLoad && !ok && lane == 0) {
+    const unsigned long long t0 = tc::globaltimer();
+    while (tc::globaltimer() - t0 < 2000000ull) {}
+  }
+  tc::tc_before_sync();
+  __syncthreads();
+  if constexpr (kPair) cluster_sync();
+  if (role == kMma) tc::tmem_dealloc(tm, 512);
+}
+
+}  // namespace hla
+}  // namespace gtr

@@ -135,6 +135,20 @@ def test_long_sequence_over_many_segments(dtype, dk, dv):
     check(d, 1, dtype, "long")
 
 
+@pytest.mark.parametrize("dtype,dk,dv", [("f16", 64, 64), ("bf16", 128, 128), ("f32", 32, 16)])
+def test_states_in_place_over_many_segments(dtype, dk, dv):
+    # a sequence's last segment may finish before its first one starts
+    d = make([12000, 50, 7000], 1, 1, dk, dv, dtype, seed=30, div=64.0, states=True)
+    c = dev(d)
+    ref, S = reference(d)
+    for _ in range(5):
+        pool = c["S"].clone()
+        out = binding.hla_fwd(c["q"], c["k"], c["v"], c["g"], c["z"], c["w"], cu_seqlens=c["cu"], scale=d["scale"],
+                              state_in=pool, state_out=pool)
+        assert_close(out, ref, DT[dtype], "in place")
+        check_states(pool, S)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("size", [1e-3, 300.0])
 def test_small_and_large_values(dtype, size):
