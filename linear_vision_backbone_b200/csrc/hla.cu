@@ -38,64 +38,38 @@ int device_sms(int* sms) {
 // 16-bit types and head dims the tensor-core kernels take
 bool tc_shape(int dk, int dv, int dtype) { return dtype != GTR_F32 && dk >= 64 && dv >= 64; }
 
-// Tokens per segment and what follows from it.
+// How the work is split (hla_common.cuh) and the workspace that takes.
 struct Plan {
-  int L;                      // tokens per segment
-  int nslot;                  // segment slots (work items of a head)
-  long long entries;          // summaries
+  int J, cut;
   size_t off_0, off_a, bytes; // workspace: summaries, initial states, log-decays
 };
 
-// Shorter segments spread a long sequence over more SMs; each costs the
-// summary of its tokens, k and v read a second time.  `units`: blocks of
-// threads a segment slot takes, `slots`: resident blocks of threads.
-//
-// Lengths known (equal ones, or one sequence): the number m of segments that
-// minimises rounds x (blocks of 128 tokens of a segment + kStart), half as
-// much again for the summaries of m > 1, and kExtra for their two launches,
-// in units of one block of tokens.  The constants are fitted to measurements
-// of the tensor-core kernels: an item's first block costs about two more, the
-// two launches about four.
-// Only the sum of the lengths known: about half the tokens an SM gets, so the
-// longest segment adds at most a third to the time of an even spread.
-int segment_blocks(long long nseq, long long T, long long units, long long slots, bool known) {
-  const long long len = known ? (T + nseq - 1) / nseq : T;
-  const long long nb = (len + hla::kC - 1) / hla::kC;
-  if (nb <= 1) return 1;
-  if (!known) {
-    const long long share = ((T / hla::kC + nseq) * units / slots + 1) / 2;
-    return (int)(share < 1 ? 1 : share < nb ? share : nb);
-  }
-  constexpr double kStart = 2.0, kExtra = 4.0;
-  double best = 0;
-  long long best_b = nb;
-  for (long long m = 1; m <= nb && m <= 4096; ++m) {
-    const long long b = (nb + m - 1) / m;
-    const long long items = nseq * units * ((nb + b - 1) / b);
-    const double rounds = (double)((items + slots - 1) / slots);
-    double cost = rounds * ((double)b + kStart);
-    if (m > 1) cost = 1.5 * cost + kExtra;
-    if (m == 1 || cost < best) { best = cost; best_b = b; }
-  }
-  return (int)best_b;
-}
-
+// `slots` groups can run at once.  Cutting spreads a long sequence evenly over
+// them, and costs the summaries (k and v before the cuts are read a second
+// time) and two more launches; whole (sequence, head)s need neither, but the
+// longest one bounds the time.  In units of one block of tokens of the outputs
+// kernel, a summary's block costs about kSum and the two launches kExtra.
+// With cu_seqlens the longest sequence may have all the tokens.
 void make_plan(int nseq, int T, int H, int dk, int dv, int dtype, bool equal, int sms, Plan* p) {
+  constexpr double kSum = 0.35, kExtra = 4.0;
   const bool tc = tc_shape(dk, dv, dtype);
-  const long long units = (long long)H * (tc ? dv / 64 : 1), slots = (long long)sms * (tc ? 1 : 4);
-  const long long L = (long long)segment_blocks(nseq, T, units, slots, equal || nseq == 1) * hla::kC;
-  p->L = (int)(L < (1ll << 30) ? L : (1ll << 30));
-  if (equal) {
-    const long long m = ((long long)(T / nseq) + p->L - 1) / p->L;
-    p->nslot = (int)(nseq * (m > 1 ? m : 1));
-    p->entries = m > 1 ? nseq * (m - 1) : 0;
-  } else {
-    p->nslot = T / p->L + nseq;
-    p->entries = T > p->L ? T / p->L + 1 : 0;
-  }
-  p->off_0 = (size_t)p->entries * H * dk * dv * sizeof(float);
+  const long long C = tc ? hla::kC : hla::kSimtBatch;
+  const long long slots = tc ? sms / (dv / 64) : (long long)sms * 4;
+  const long long len = equal ? T / nseq : T, longest = len > C ? (len + C - 1) / C : 1;
+  const long long B = H * (equal ? nseq * longest : T / C + nseq);      // at most, with cu_seqlens
+  const long long items = (long long)nseq * H;
+  const long long share = (B + slots - 1) / slots;
+  const double whole = equal ? (double)((items + slots - 1) / slots) * (double)longest
+                             : (double)(share > longest ? share : longest);
+  p->cut = longest > 1 && whole > share * (1.0 + kSum) + kExtra;
+  long long J;
+  if (p->cut) J = (B + share - 1) / share;                               // even shares
+  else J = items < slots ? items : slots;
+  p->J = (int)J;
+  const size_t state = (size_t)dk * dv * sizeof(float);
+  p->off_0 = p->cut ? J * state : 0;
   p->off_a = 2 * p->off_0;
-  p->bytes = p->off_a + (size_t)p->entries * H * sizeof(float);
+  p->bytes = p->off_a + (p->cut ? J * sizeof(float) : 0);
 }
 
 // ---- tensor-core launches
@@ -135,7 +109,7 @@ int map_rows(CUtensorMap* map, int dtype, const void* base, int T, int heads, in
 }
 
 template <typename T, int DK, bool kSum, bool kPair>
-int launch_tc_kernel(const hla::Params& p, const hla::Maps& maps, int halves, int sms, cudaStream_t st) {
+int launch_tc_kernel(const hla::Params& p, const hla::Maps& maps, int halves, cudaStream_t st) {
   constexpr int smem = hla::Layout<T, DK, kSum>::kSmem;
   const auto kern = hla::hla_tc<T, DK, kSum, kPair>;
   static std::atomic<bool> done[kMaxDevices];
@@ -145,10 +119,8 @@ int launch_tc_kernel(const hla::Params& p, const hla::Maps& maps, int halves, in
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return GTR_ERR_CUDA;
     done[dev].store(true, std::memory_order_relaxed);
   }
-  const long long items = (long long)p.nslot * p.H * halves;
-  const long long most = sms / halves * halves;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items < most ? items : most));
+  cfg.gridDim = dim3((unsigned)(p.J * halves));
   cfg.blockDim = dim3(kSum ? hla::kSumThreads : hla::kTcThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -163,22 +135,22 @@ int launch_tc_kernel(const hla::Params& p, const hla::Maps& maps, int halves, in
   return cudaLaunchKernelEx(&cfg, kern, p, maps, halves) == cudaSuccess ? GTR_OK : GTR_ERR_CUDA;
 }
 template <typename T, int DK>
-int launch_tc_dk(const hla::Params& p, const hla::Maps& maps, bool sum, int sms, cudaStream_t st) {
+int launch_tc_dk(const hla::Params& p, const hla::Maps& maps, bool sum, cudaStream_t st) {
   const int halves = p.dv / 64;
-  if (sum) return launch_tc_kernel<T, DK, true, false>(p, maps, halves, sms, st);
-  if (halves == 2 && p.z) return launch_tc_kernel<T, DK, false, true>(p, maps, halves, sms, st);
-  return launch_tc_kernel<T, DK, false, false>(p, maps, halves, sms, st);
+  if (sum) return launch_tc_kernel<T, DK, true, false>(p, maps, halves, st);
+  if (halves == 2 && p.z) return launch_tc_kernel<T, DK, false, true>(p, maps, halves, st);
+  return launch_tc_kernel<T, DK, false, false>(p, maps, halves, st);
 }
-int launch_tc(const hla::Params& p, const hla::Maps& maps, int dtype, bool sum, int sms, cudaStream_t st) {
+int launch_tc(const hla::Params& p, const hla::Maps& maps, int dtype, bool sum, cudaStream_t st) {
   if (dtype == GTR_F16)
-    return p.dk == 64 ? launch_tc_dk<__half, 64>(p, maps, sum, sms, st) : launch_tc_dk<__half, 128>(p, maps, sum, sms, st);
-  return p.dk == 64 ? launch_tc_dk<__nv_bfloat16, 64>(p, maps, sum, sms, st)
-                    : launch_tc_dk<__nv_bfloat16, 128>(p, maps, sum, sms, st);
+    return p.dk == 64 ? launch_tc_dk<__half, 64>(p, maps, sum, st) : launch_tc_dk<__half, 128>(p, maps, sum, st);
+  return p.dk == 64 ? launch_tc_dk<__nv_bfloat16, 64>(p, maps, sum, st)
+                    : launch_tc_dk<__nv_bfloat16, 128>(p, maps, sum, st);
 }
 
 template <typename T, int ROWS>
 int launch_simt_rows(const hla::Params& p, bool sum, cudaStream_t st) {
-  const dim3 grid((unsigned)p.nslot, (unsigned)p.H);
+  const dim3 grid((unsigned)p.J);
   const size_t smem = (size_t)hla::simt_smem_floats(p.dk, p.dv, sum) * sizeof(float);   // below 48 KB
   if (sum) return launch_pdl(hla::hla_simt<T, ROWS, true>, grid, dim3(hla::kSimtThreads), smem, st, p);
   return launch_pdl(hla::hla_simt<T, ROWS, false>, grid, dim3(hla::kSimtThreads), smem, st, p);
@@ -298,8 +270,8 @@ GTR_API gtr_status_t gtr_hla_fwd(const gtr_hla_args* args, void* stream) {
   make_plan(p.nseq, p.T, p.H, p.dk, p.dv, args->dtype, !p.cu, sms, &pl);
   if (pl.bytes > 0 && !args->workspace) return GTR_ERR_INVALID_ARG;
   if (args->workspace_bytes < pl.bytes) return GTR_ERR_NO_MEMORY;
-  p.L = pl.L;
-  p.nslot = pl.nslot;
+  p.J = pl.J;
+  p.cut = pl.cut;
   p.wsS = (float*)args->workspace;
   p.ws0 = (float*)((char*)args->workspace + pl.off_0);
   p.wsA = (float*)((char*)args->workspace + pl.off_a);
@@ -313,13 +285,13 @@ GTR_API gtr_status_t gtr_hla_fwd(const gtr_hla_args* args, void* stream) {
              map_rows(&maps.z, args->dtype, p.z ? p.z : p.v, p.T, p.H, p.dv, p.z ? p.ldz : p.ldv)))
     return GTR_ERR_CUDA;
   const auto launch = [&](bool sum) {
-    return tc ? launch_tc(p, maps, args->dtype, sum, sms, st) : launch_prompt(p, args->dtype, sum, st);
+    return tc ? launch_tc(p, maps, args->dtype, sum, st) : launch_prompt(p, args->dtype, sum, st);
   };
-  if (pl.entries > 0) {
+  if (pl.cut) {
     if (launch(true)) return GTR_ERR_CUDA;
-    const unsigned eb = (unsigned)((p.dk * p.dv / 4 + hla::kScanThreads - 1) / hla::kScanThreads);
-    if (launch_pdl(hla::hla_scan, dim3((unsigned)pl.entries, (unsigned)p.H, eb), dim3(hla::kScanThreads), 0, st, p))
-      return GTR_ERR_CUDA;
+    const dim3 grid((unsigned)p.J, (unsigned)((p.dk * p.dv / 4 + hla::kScanThreads - 1) / hla::kScanThreads));
+    const auto scan = tc ? hla::hla_scan<hla::kC> : hla::hla_scan<hla::kSimtBatch>;
+    if (launch_pdl(scan, grid, dim3(hla::kScanThreads), 0, st, p)) return GTR_ERR_CUDA;
   }
   return launch(false) ? GTR_ERR_CUDA : GTR_OK;
 }

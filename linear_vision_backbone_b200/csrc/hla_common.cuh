@@ -1,53 +1,44 @@
 // hla_common.cuh -- what the kernels of the head-decay linear attention share:
-// their parameters, the split of packed sequences into segments and blocks of
-// tokens, and the decay.
+// their parameters, the split of the work, the scan over its cuts, and the
+// decay.
 //
-// A segment is a run of at most L consecutive tokens of one sequence (L a
-// multiple of the block of kHlaC tokens).  Sequence n of start a and length
-// len has ceil(len / L) segments, in slots a / L + n onwards; since
-// floor((a + len) / L) + 1 >= floor(a / L) + ceil(len / L), the slots of
-// different sequences are distinct and below T / L + nseq, so the grid is
-// known without the lengths, which only the device has.  All but a sequence's
-// last segment have a summary (the state the segment makes from zero, and its
-// decay) in workspace entry a / L + i, distinct by the same argument and at
-// most T / L.  Offsets that are not those of a valid cu_seqlens are clamped
-// to [0, T], so no access leaves the tensors whatever it holds.
+// The split.  Sequence n has nb_n = max(1, ceil(len_n / C)) blocks of C tokens
+// in each of its H heads (one, empty, for a length of zero: its state still
+// moves).  All blocks stand in one line, sequence by sequence, head by head,
+// and group j of J takes the blocks [j B / J, (j + 1) B / J) of the B = H sum
+// nb_n.  Only the device knows the lengths, so every kernel finds its range
+// from cu_seqlens by itself.  With `cut` a range may end inside a (sequence,
+// head): the part before the cut then has a summary (the state it makes from
+// zero, and its decay) in workspace entry j, which the scan turns into the state
+// the next group starts from; there are J entries whatever the sizes.  Without,
+// a group takes the (sequence, head)s whose first block is in its range, whole.
+// Offsets that are not those of a valid cu_seqlens are clamped to [0, T], so no
+// access leaves the tensors whatever it holds.
 #pragma once
 #include "common.cuh"
 
 namespace gtr {
 namespace hla {
 
-constexpr int kC = 128;            // tokens per block of the tensor-core kernels; segments are multiples of it
+constexpr int kC = 128;            // tokens per block of the tensor-core kernels
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLog = -110.0f; // e^-110 is zero in fp32
 
 struct Params {
   const void* q; const void* k; const void* v; const float* g; const void* z; const float* w; void* out;
   const float* state_in; float* state_out; const int* slots; const int* seen; const int* cu;
-  float* wsS; float* wsA;          // segment summaries [entry][H][dk][dv], summed log2-decays [entry][H]
-  float* ws0;                      // initial states of sequences of several segments [first entry][H][dk][dv]
+  float* wsS;                      // [J][dk][dv]: summaries, then start states of the next group
+  float* ws0;                      // [J][dk][dv]: initial states of cut (sequence, head)s, by their first group
+  float* wsA;                      // [J]: the summaries' log2-decays
   long long ldq, ldk, ldv, ldz, ldo;
   int nseq, T, Hk, H, dk, dv, nslots, g_per_head;
   float scale;
-  int L;                           // tokens per segment
-  int nslot;                       // segment slots, empty ones among them
+  int J, cut;
 };
 
-// Segments sequence n of length len has.
-__device__ __forceinline__ int n_segments(int len, int L) { return (int)(((long long)len + L - 1) / L); }
-
-struct Segment {
-  int n;          // sequence
-  int t0, len;    // first token row, tokens
-  int i, m;       // this segment of m
-  int ws;         // workspace entry of the sequence's first segment
-  long long slot; // state row, or -1: the sequence is skipped
-  bool start;     // the sequence starts from state_in
-};
-
-// Rows of sequence n.
-__device__ __forceinline__ void seq_rows(const Params& p, int n, int& a, int& b) {
+// Rows of sequence n, and its blocks of C tokens.
+template <int C> __device__ __forceinline__ int seq_rows(const Params& p, int n, int& a) {
+  int b;
   if (p.cu) {
     a = min(max(__ldg(p.cu + n), 0), p.T);
     b = min(max(__ldg(p.cu + n + 1), a), p.T);
@@ -56,66 +47,158 @@ __device__ __forceinline__ void seq_rows(const Params& p, int n, int& a, int& b)
     a = n * len;
     b = a + len;
   }
+  return b - a;
 }
+__device__ __forceinline__ int n_blocks(int len, int C) { return max(1, (int)(((long long)len + C - 1) / C)); }
 
-// Segment slot s, by a whole warp; false for a slot that holds none.  Sequence
-// n is the last one whose first slot a_n / L + n is <= s: these grow with n,
-// so it is a count, 32 sequences a step.
-__device__ __forceinline__ bool find_segment(const Params& p, int s, Segment& g) {
-  const int lane = threadIdx.x & 31;
+// A place in the line of blocks: block `off` of the H nb_n of sequence n.
+struct Place {
   int n;
-  if (p.cu) {
-    int count = 0;
-    for (int n0 = 0; n0 < p.nseq; n0 += 32) {
-      const int j = n0 + lane;
-      bool le = false;
-      if (j < p.nseq) le = min(max(__ldg(p.cu + j), 0), p.T) / p.L + j <= s;
-      const int c = __popc(__ballot_sync(0xffffffffu, le));
-      count += c;
-      if (c < 32) break;
-    }
-    if (count == 0) return false;
-    n = count - 1;
-    int a, b;
-    seq_rows(p, n, a, b);
-    g.i = s - (a / p.L + n);
-    g.ws = a / p.L;
-    g.t0 = a;
-    g.len = b - a;
-    g.m = n_segments(g.len, p.L);
-    if (g.i < 0 || g.i >= max(g.m, 1)) return false;   // a sequence of length zero has a slot for its state
-  } else {
-    const int len = p.T / p.nseq;
-    g.m = max(1, n_segments(len, p.L));
-    n = s / g.m;
-    if (n >= p.nseq) return false;
-    g.i = s - n * g.m;
-    g.ws = n * (g.m - 1);
-    g.t0 = n * len;
-    g.len = len;
+  long long off;
+};
+
+// Group j's range: the line's B blocks, the groups J that have any (at most
+// one per block, so that none between two others is empty), the places x0 and
+// x1 it lies between and the sequences they fall into (nseq for x = B).
+struct Range {
+  long long B, x0, x1;
+  int J;
+  Place a, b;
+  __device__ __forceinline__ void set(long long blocks, int groups, int j) {
+    B = blocks;
+    J = (int)min((long long)groups, blocks);
+    x0 = B * min(j, J) / J;
+    x1 = B * min(j + 1, J) / J;
   }
-  g.n = n;
-  const int off = g.i * p.L;
-  g.t0 += off;
-  g.len = min(p.L, g.len - off);
-  g.slot = p.slots ? __ldg(p.slots + n) : n;
-  if (g.slot >= p.nslots && (p.state_in || p.state_out)) {
-    if (lane == 0) gtr_flag(kStatusBadSlot);
-    g.slot = -1;
+};
+
+// By the whole block of threads.  `scratch`: 40 long longs of shared memory,
+// free again after the caller's next barrier.
+template <int C> __device__ __forceinline__ void locate(const Params& p, int j, long long* scratch, Range& g) {
+  if (!p.cu) {
+    const long long per = (long long)n_blocks(p.T / p.nseq, C) * p.H;
+    g.set(per * p.nseq, p.J, j);
+    g.a.n = (int)(g.x0 / per); g.a.off = g.x0 - g.a.n * per;
+    g.b.n = (int)(g.x1 / per); g.b.off = g.x1 - g.b.n * per;
+    return;
   }
-  g.start = p.state_in && (!p.seen || __ldg(p.seen + n) > 0);
-  return g.slot >= 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  const int per = (p.nseq + blockDim.x - 1) / (int)blockDim.x;   // sequences per thread, consecutive ones
+  const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
+  long long mine = 0;
+  int r;
+  for (int n = n0; n < n1; ++n) mine += n_blocks(seq_rows<C>(p, n, r), C);
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  if (tid == 0) {
+    scratch[32] = p.nseq; scratch[33] = 0;
+    scratch[34] = p.nseq; scratch[35] = 0;
+  }
+  __syncthreads();
+  long long before = inc - mine, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  g.set(total * p.H, p.J, j);
+  for (int n = n0; n < n1; ++n) {
+    const long long nb = n_blocks(seq_rows<C>(p, n, r), C);
+    const long long s = before * p.H, e = (before + nb) * p.H;
+    if (s <= g.x0 && g.x0 < e) { scratch[32] = n; scratch[33] = g.x0 - s; }
+    if (s <= g.x1 && g.x1 < e) { scratch[34] = n; scratch[35] = g.x1 - s; }
+    before += nb;
+  }
+  __syncthreads();
+  g.a.n = (int)scratch[32]; g.a.off = scratch[33];
+  g.b.n = (int)scratch[34]; g.b.off = scratch[35];
 }
 
-// The state a segment starts from, or null for zero.  A sequence of several
-// segments has the scan's copy of its initial state: in place, its last
-// segment may write the state before its first one has read it.
-__device__ __forceinline__ const float* start_state(const Params& p, const Segment& g, int h) {
+// A group's part of one (sequence, head).
+struct Part {
+  int n, h;
+  int t0, len;        // its first token row, its tokens
+  int nb;             // its blocks of C tokens (0: an empty sequence)
+  bool first, last;   // it has the first / the last block of the (sequence, head)
+  long long slot;     // state row, or -1: the sequence is skipped
+  bool start;         // the sequence starts from state_in
+};
+
+// Steps through a range of the line; every thread (or warp) of a group can
+// walk it by itself and sees the same parts.
+struct Walk {
+  Place at;
+  long long left;
+};
+template <int C> __device__ __forceinline__ bool next_part(const Params& p, Walk& w, Part& g) {
+  while (w.left > 0 && w.at.n < p.nseq) {
+    int a;
+    const int len = seq_rows<C>(p, w.at.n, a);
+    const int nb = n_blocks(len, C);
+    const int h = (int)(w.at.off / nb), b0 = (int)(w.at.off - (long long)h * nb);
+    int take = (int)min((long long)(nb - b0), w.left);
+    const int n = w.at.n;
+    w.left -= take;
+    w.at.off += take;
+    if (w.at.off >= (long long)nb * p.H) { w.at.n++; w.at.off = 0; }
+    if (!p.cut) {
+      if (b0 > 0) continue;                    // another group has it whole
+      take = nb;
+    }
+    g.n = n;
+    g.h = h;
+    g.first = b0 == 0;
+    g.last = b0 + take == nb;
+    g.t0 = a + b0 * C;
+    g.len = min(len - b0 * C, take * C);
+    g.nb = len > 0 ? take : 0;
+    g.slot = p.slots ? __ldg(p.slots + n) : n;
+    if (g.slot >= p.nslots && (p.state_in || p.state_out)) {
+      gtr_flag(kStatusBadSlot);
+      g.slot = -1;
+    }
+    g.start = p.state_in && (!p.seen || __ldg(p.seen + n) > 0);
+    if (g.slot >= 0) return true;
+  }
+  return false;
+}
+
+// The state a part of group j starts from, or null for zero.  A cut (sequence,
+// head) has the scan's copy of its initial state: in place, the group of its
+// end may write the state before the group of its start has read it.
+__device__ __forceinline__ const float* start_state(const Params& p, const Part& g, int j) {
   const size_t hs = (size_t)p.dk * p.dv;
-  if (g.i > 0) return p.wsS + ((size_t)(g.ws + g.i - 1) * p.H + h) * hs;
+  if (!g.first) return p.wsS + (size_t)(j - 1) * hs;
   if (!g.start) return nullptr;
-  if (g.m > 1) return p.ws0 + ((size_t)g.ws * p.H + h) * hs;
-  return p.state_in + ((size_t)g.slot * p.H + h) * hs;
+  if (!g.last) return p.ws0 + (size_t)j * hs;
+  return p.state_in + ((size_t)g.slot * p.H + g.h) * hs;
+}
+
+// The part of a group before the cut at the end of its range; false when it
+// ends with a (sequence, head).
+template <int C> __device__ __forceinline__ bool cut_part(const Params& p, const Range& rg, Part& g) {
+  const Place& b = rg.b;
+  if (rg.x0 >= rg.x1 || b.n >= p.nseq) return false;
+  int a;
+  const int len = seq_rows<C>(p, b.n, a), nb = n_blocks(len, C);
+  const int h = (int)(b.off / nb), e = (int)(b.off - (long long)h * nb);   // blocks before the cut
+  if (e == 0) return false;
+  const int b0 = (long long)e <= rg.x1 - rg.x0 ? 0 : (int)(e - (rg.x1 - rg.x0));
+  g.n = b.n;
+  g.h = h;
+  g.first = b0 == 0;
+  g.last = false;
+  g.t0 = a + b0 * C;
+  g.len = (e - b0) * C;                        // whole blocks: the sequence goes on behind the cut
+  g.nb = e - b0;
+  g.slot = p.slots ? __ldg(p.slots + b.n) : b.n;
+  if (g.slot >= p.nslots && (p.state_in || p.state_out)) g.slot = -1;
+  g.start = p.state_in && (!p.seen || __ldg(p.seen + b.n) > 0);
+  return g.slot >= 0;
 }
 
 // log2 of a decay: at most zero; below e^-110 nothing is left.  A NaN stays.
@@ -129,63 +212,46 @@ __device__ __forceinline__ float load_decay(const Params& p, int t, int h) {
 }
 
 // ---------------------------------------------------------------------------
-// The states segments start from: for each sequence of several segments,
-// S = its initial state, then entry i (the summary of segment i) is replaced by
-// S = e^{decay of segment i} S + summary, the state segment i + 1 starts from.
-// One thread per four state elements; grid (entries, H, dk dv / 4 / 128), a
-// block whose entry is not the first of a sequence ends at once.
+// The states groups start from.  The group with the first block of a cut
+// (sequence, head) walks its cuts: S = the initial state (copied to ws0), then
+// entry i becomes S = e^{decay of part i} S + summary of part i.  One thread
+// per four state elements; grid (J, dk dv / 4 / 128), most blocks have no such
+// cut and end at once.
 constexpr int kScanThreads = 128;
-constexpr int kScanAhead = 8;      // segments whose loads are in flight together
+constexpr int kScanAhead = 12;     // parts whose loads are in flight together
 
-__global__ void __launch_bounds__(kScanThreads) hla_scan(const Params p) {
+template <int C> __global__ void __launch_bounds__(kScanThreads) hla_scan(const Params p) {
+  __shared__ long long scratch[40];
   pdl_wait();
   pdl_trigger();
-  const int entry = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
-  int n, a, b;
-  if (p.cu) {
-    // the last sequence with a_n / L <= entry
-    int count = 0;
-    for (int n0 = 0; n0 < p.nseq; n0 += 32) {
-      const int j = n0 + lane;
-      bool le = false;
-      if (j < p.nseq) le = min(max(__ldg(p.cu + j), 0), p.T) / p.L <= entry;
-      const int c = __popc(__ballot_sync(0xffffffffu, le));
-      count += c;
-      if (c < 32) break;
-    }
-    if (count == 0) return;
-    n = count - 1;
-    seq_rows(p, n, a, b);
-    if (a / p.L != entry) return;
-  } else {
-    const int per = n_segments(p.T / p.nseq, p.L) - 1;
-    if (per < 1 || entry % per != 0) return;
-    n = entry / per;
-    if (n >= p.nseq) return;
-    seq_rows(p, n, a, b);
-  }
-  const int m = n_segments(b - a, p.L) - 1;      // summaries
-  const long long slot = p.slots ? __ldg(p.slots + n) : n;
-  if (m < 1 || slot < 0 || (slot >= p.nslots && (p.state_in || p.state_out))) return;
+  const int j = blockIdx.x;
+  Range rg;
+  locate<C>(p, j, scratch, rg);
+  Part g;
+  if (!cut_part<C>(p, rg, g) || !g.first) return;
+  // the summaries of this (sequence, head): of the groups that end before it does
+  int r;
+  const long long end = rg.x1 - g.nb + n_blocks(seq_rows<C>(p, g.n, r), C);
+  int m = 1;
+  while (j + m < rg.J && rg.B * (j + m + 1) / rg.J < end) ++m;
   const int per_state = p.dk * p.dv;
-  const int e = (blockIdx.z * kScanThreads + threadIdx.x) * 4;
+  const int e = (blockIdx.y * kScanThreads + threadIdx.x) * 4;
   if (e >= per_state) return;
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.state_in && (!p.seen || __ldg(p.seen + n) > 0)) {
-    S = *reinterpret_cast<const float4*>(p.state_in + ((size_t)slot * p.H + h) * per_state + e);
-    *reinterpret_cast<float4*>(p.ws0 + ((size_t)entry * p.H + h) * per_state + e) = S;
+  if (g.start) {
+    S = *reinterpret_cast<const float4*>(p.state_in + ((size_t)g.slot * p.H + g.h) * per_state + e);
+    *reinterpret_cast<float4*>(p.ws0 + (size_t)j * per_state + e) = S;
   }
-  const size_t step = (size_t)p.H * per_state;
-  float* ws = p.wsS + ((size_t)entry * p.H + h) * per_state + e;
-  const float* wa = p.wsA + (size_t)entry * p.H + h;
+  float* ws = p.wsS + (size_t)j * per_state + e;
+  const float* wa = p.wsA + j;
   for (int i0 = 0; i0 < m; i0 += kScanAhead) {
     float4 d[kScanAhead];
     float l[kScanAhead];
 #pragma unroll
     for (int u = 0; u < kScanAhead; ++u)
       if (i0 + u < m) {
-        d[u] = *reinterpret_cast<const float4*>(ws + (i0 + u) * step);
-        l[u] = wa[(size_t)(i0 + u) * p.H];
+        d[u] = *reinterpret_cast<const float4*>(ws + (size_t)(i0 + u) * per_state);
+        l[u] = wa[i0 + u];
       }
 #pragma unroll
     for (int u = 0; u < kScanAhead; ++u)
@@ -193,7 +259,7 @@ __global__ void __launch_bounds__(kScanThreads) hla_scan(const Params p) {
         const float f = exp2f(l[u]);
         S.x = fmaf(f, S.x, d[u].x); S.y = fmaf(f, S.y, d[u].y);
         S.z = fmaf(f, S.z, d[u].z); S.w = fmaf(f, S.w, d[u].w);
-        *reinterpret_cast<float4*>(ws + (i0 + u) * step) = S;
+        *reinterpret_cast<float4*>(ws + (size_t)(i0 + u) * per_state) = S;
       }
   }
 }

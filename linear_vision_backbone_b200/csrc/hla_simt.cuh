@@ -15,110 +15,112 @@ __host__ __device__ inline int simt_smem_floats(int dk, int dv, bool sum) {
   return kSimtBatch * (1 + (sum ? 1 : 2) * dk + dv + (sum ? 0 : kSimtThreads));
 }
 
-// One segment of one head by the recurrence itself, the state spread over the
-// block: thread tid has column tid % dv and the ROWS rows from (tid / dv) ROWS,
-// so a warp reads a token's k and q values as broadcasts.  kSum: the state a
-// segment makes from zero and its decay (skipped for a sequence's last
-// segment); else its outputs from the state it starts from, and the
-// sequence's final state after its last segment.  Bound by the serial chain of
-// its tokens (two products and a sum per state element and token in fp32).
+// A group's parts by the recurrence itself, the state spread over the block:
+// thread tid has column tid % dv and the ROWS rows from (tid / dv) ROWS, so a
+// warp reads a token's k and q values as broadcasts.  kSum: the summary of the
+// part before the group's cut; else the outputs, and final states.  Bound by the
+// serial chain of its tokens (two products and a sum per state element and
+// token in fp32).
 template <typename T, int ROWS, bool kSum>
 __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   const int dk = p.dk, dv = p.dv;
   float* as = sm;                            // [batch] log-decays
   float* ks = as + kSimtBatch;               // [batch][dk]
   float* qs = ks + kSimtBatch * dk;          // [batch][dk], outputs only
   float* vs = qs + (kSum ? 0 : kSimtBatch * dk);   // [batch][dv]
   float* part = vs + kSimtBatch * dv;        // [batch][threads]: partial o, outputs only
+  __shared__ long long scratch[40];
   pdl_wait();
   pdl_trigger();
-  const int h = blockIdx.y, hk = h / (p.H / p.Hk);
-  Segment g;
-  if (!find_segment(p, blockIdx.x, g)) return;
-  const bool last = g.i >= g.m - 1;
-  if (kSum && last) return;
+  Range rg;
+  locate<kSimtBatch>(p, blockIdx.x, scratch, rg);
+  Walk walk{rg.a, rg.x1 - rg.x0};
+  Part g;
   const int tid = threadIdx.x, j = tid % dv, r0 = tid / dv * ROWS;
   const size_t hs = (size_t)dk * dv;
-  float S[ROWS];
-  {
-    const float* src = kSum ? nullptr : start_state(p, g, h);
+  while (kSum ? cut_part<kSimtBatch>(p, rg, g) : next_part<kSimtBatch>(p, walk, g)) {
+    const int h = g.h, hk = h / (p.H / p.Hk);
+    float S[ROWS];
+    const float* src = kSum ? nullptr : start_state(p, g, blockIdx.x);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) S[r] = src ? src[(size_t)(r0 + r) * dv + j] : 0.f;
-  }
-  float total = 0.f;                         // thread 0: the segment's summed log2-decay
-  for (int b0 = 0; b0 < g.len; b0 += kSimtBatch) {
-    const int n = min(kSimtBatch, g.len - b0);
-    const long long t0 = (long long)g.t0 + b0;
-    __syncthreads();
-    if (tid < n) as[tid] = load_decay(p, (int)(t0 + tid), h);
-    for (int e = tid; e < n * dk; e += kSimtThreads) {
-      const int t = e / dk, i = e - t * dk;
-      ks[e] = ld_f((const T*)p.k + (t0 + t) * p.ldk + (long long)hk * dk + i);
-      if (!kSum) qs[e] = ld_f((const T*)p.q + (t0 + t) * p.ldq + (long long)hk * dk + i) * p.scale;
-    }
-    for (int e = tid; e < n * dv; e += kSimtThreads) {
-      const int t = e / dv, i = e - t * dv;
-      vs[e] = ld_f((const T*)p.v + (t0 + t) * p.ldv + (long long)h * dv + i);
-    }
-    __syncthreads();
-    for (int t = 0; t < n; ++t) {
-      // S <- a S + k v as S + (a - 1) S + k v for a near one: rounding a itself
-      // would be the same relative error at every token, 2^-25 a token for as
-      // long as the state remembers
-      const float l = as[t], v = vs[t * dv + j];
-      const bool near_one = l > -1.f;
-      const float a = near_one ? expm1f(l * kLn2) : exp2f(l);
-      total += l;
-      const float* k = ks + t * dk + r0;
-      const float* q = qs + t * dk + r0;
-      float o = 0.f;
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        S[r] = fmaf(a, S[r], near_one ? fmaf(k[r], v, S[r]) : k[r] * v);
-        if (!kSum) o = fmaf(q[r], S[r], o);
-      }
-      if (!kSum) part[t * kSimtThreads + tid] = o;
-    }
-    if (!kSum) {
+    float total = 0.f;                       // the part's summed log2-decay
+    for (int b0 = 0; b0 < g.len; b0 += kSimtBatch) {
+      const int n = min(kSimtBatch, g.len - b0);
+      const long long t0 = (long long)g.t0 + b0;
       __syncthreads();
-      // one warp per token: the rows' partial sums, then the norm and the gate
-      const int lane = tid & 31;
-      for (int t = tid >> 5; t < n; t += kSimtThreads / 32) {
-        float o[4];
-        float ss = 0.f;
+      if (tid < n) as[tid] = load_decay(p, (int)(t0 + tid), h);
+      for (int e = tid; e < n * dk; e += kSimtThreads) {
+        const int t = e / dk, i = e - t * dk;
+        ks[e] = ld_f((const T*)p.k + (t0 + t) * p.ldk + (long long)hk * dk + i);
+        if (!kSum) qs[e] = ld_f((const T*)p.q + (t0 + t) * p.ldq + (long long)hk * dk + i) * p.scale;
+      }
+      for (int e = tid; e < n * dv; e += kSimtThreads) {
+        const int t = e / dv, i = e - t * dv;
+        vs[e] = ld_f((const T*)p.v + (t0 + t) * p.ldv + (long long)h * dv + i);
+      }
+      __syncthreads();
+      for (int t = 0; t < n; ++t) {
+        // S <- a S + k v as S + (a - 1) S + k v for a near one: rounding a itself
+        // would be the same relative error at every token, 2^-25 a token for as
+        // long as the state remembers
+        const float l = as[t], v = vs[t * dv + j];
+        const bool near_one = l > -1.f;
+        const float a = near_one ? expm1f(l * kLn2) : exp2f(l);
+        total += l;
+        const float* k = ks + t * dk + r0;
+        const float* q = qs + t * dk + r0;
+        float o = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = lane + 32 * c;
-          o[c] = 0.f;
-          if (col < dv)
-            for (int r = 0; r < kSimtThreads / dv; ++r) o[c] += part[t * kSimtThreads + r * dv + col];
-          ss = fmaf(o[c], o[c], ss);
+        for (int r = 0; r < ROWS; ++r) {
+          S[r] = fmaf(a, S[r], near_one ? fmaf(k[r], v, S[r]) : k[r] * v);
+          if (!kSum) o = fmaf(q[r], S[r], o);
         }
-        float inv = 1.f;
-        if (p.z) inv = rsqrtf(warp_sum(ss) / (float)dv + kRmsEps);
-        T* orow = (T*)p.out + (t0 + t) * p.ldo + (long long)h * dv;
-        const T* zrow = p.z ? (const T*)p.z + (t0 + t) * p.ldz + (long long)h * dv : nullptr;
+        if (!kSum) part[t * kSimtThreads + tid] = o;
+      }
+      if (!kSum) {
+        __syncthreads();
+        // one warp per token: the rows' partial sums, then the norm and the gate
+        const int lane = tid & 31;
+        for (int t = tid >> 5; t < n; t += kSimtThreads / 32) {
+          float o[4];
+          float ss = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = lane + 32 * c;
-          if (col >= dv) continue;
-          float y = o[c];
-          if (zrow) y = y * inv * (p.w ? p.w[col] : 1.f) * silu_f(ld_f(zrow + col));
-          orow[col] = Elem<T>::from_f(y);
+          for (int c = 0; c < 4; ++c) {
+            const int col = lane + 32 * c;
+            o[c] = 0.f;
+            if (col < dv)
+              for (int r = 0; r < kSimtThreads / dv; ++r) o[c] += part[t * kSimtThreads + r * dv + col];
+            ss = fmaf(o[c], o[c], ss);
+          }
+          float inv = 1.f;
+          if (p.z) inv = rsqrtf(warp_sum(ss) / (float)dv + kRmsEps);
+          T* orow = (T*)p.out + (t0 + t) * p.ldo + (long long)h * dv;
+          const T* zrow = p.z ? (const T*)p.z + (t0 + t) * p.ldz + (long long)h * dv : nullptr;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int col = lane + 32 * c;
+            if (col >= dv) continue;
+            float y = o[c];
+            if (zrow) y = y * inv * (p.w ? p.w[col] : 1.f) * silu_f(ld_f(zrow + col));
+            orow[col] = Elem<T>::from_f(y);
+          }
         }
       }
     }
-  }
-  if (kSum) {
-    float* dst = p.wsS + ((size_t)(g.ws + g.i) * p.H + h) * hs;
+    if (kSum) {
+      float* dst = p.wsS + (size_t)blockIdx.x * hs;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) dst[(size_t)(r0 + r) * dv + j] = S[r];
-    if (tid == 0) p.wsA[(size_t)(g.ws + g.i) * p.H + h] = total;
-  } else if (last && p.state_out) {
-    float* dst = p.state_out + ((size_t)g.slot * p.H + h) * hs;
+      for (int r = 0; r < ROWS; ++r) dst[(size_t)(r0 + r) * dv + j] = S[r];
+      if (tid == 0) p.wsA[blockIdx.x] = total;
+      return;
+    }
+    if (g.last && p.state_out) {
+      float* dst = p.state_out + ((size_t)g.slot * p.H + h) * hs;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) dst[(size_t)(r0 + r) * dv + j] = S[r];
+      for (int r = 0; r < ROWS; ++r) dst[(size_t)(r0 + r) * dv + j] = S[r];
+    }
   }
 }
 

@@ -28,15 +28,16 @@
 //
 // One block of threads per SM and 64 value columns of a head (dv = 128: two
 // blocks share a head, as a cluster when the norm needs the sum over both),
-// walking the blocks of 128 tokens of its segments.  18 warps, each group one
+// walking the blocks of 128 tokens of its segments.  20 warps, each group one
 // step of the pipeline, joined by mbarriers:
 //   0-3   scores -> decayed, masked P (a thread has a row)
 //   4-7   the decay sums; wv terms; zeros behind the last token
 //   8-11  the state: fp32 in registers (a thread has a row of 64 columns, or a
 //         half row), S <- a S + kv, and its terms for the next block's qs
 //   12-15 outputs: qs and pv joined, norm, gate, stores
-//   16    loads (TMA, 128-byte swizzled tiles of 128 rows x 64 columns)
+//   16    loads of k and v (TMA, 128-byte swizzled tiles of 128 rows x 64 columns)
 //   17    issues the products
+//   18,19 loads of q and of z, each waiting for its own buffers only
 // The products of a block are issued scores, qs, kv, pv: while the P warps turn
 // block c's scores around, the tensor cores do its qs and kv.
 #pragma once
@@ -49,7 +50,7 @@ namespace hla {
 using tc::saddr;
 
 constexpr int kTile = kC * 128;          // 128 rows x 64 16-bit columns: 16 KB
-constexpr int kTcThreads = 18 * 32;
+constexpr int kTcThreads = 20 * 32;
 constexpr int kSumThreads = 10 * 32;
 
 struct Maps {
@@ -172,6 +173,31 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16])
       : "memory");
 }
 
+// Two fp32 in one 64-bit register (add / mul / fma .f32x2: one issue for two)
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float a) { return tc::f2pack(a, a); }
+
+template <int N> __device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void tm_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 template <typename T> struct T2;
 template <> struct T2<__half> {
   using t = __half2;
@@ -188,20 +214,35 @@ template <typename T> __device__ __forceinline__ uint32_t word(typename T2<T>::t
   memcpy(&u, &x, 4);
   return u;
 }
-template <typename T> __device__ __forceinline__ float2 widen(uint32_t u) {
+// two 16-bit values as two fp32
+template <typename T> __device__ __forceinline__ uint64_t widen(uint32_t u) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return pack2(u << 16, u & 0xffff0000u);
   typename T2<T>::t x;
   memcpy(&x, &u, 4);
-  return T2<T>::to(x);
+  const float2 f = T2<T>::to(x);
+  return tc::f2pack(f.x, f.y);
 }
-// hi = T(x), lo = T(x - hi); a, b become what is left.
-template <typename T> __device__ __forceinline__ uint32_t term(float& a, float& b) {
-  const typename T2<T>::t h = T2<T>::from(a, b);
-  const float2 f = T2<T>::to(h);
-  a -= f.x;
-  b -= f.y;
-  return word<T>(h);
+template <typename T> __device__ __forceinline__ uint32_t narrow(uint64_t x) {
+  const float2 f = tc::f2unpack(x);
+  return word<T>(T2<T>::from(f.x, f.y));
+}
+// The rounding of x to T; x becomes what is left.
+template <typename T> __device__ __forceinline__ uint32_t term(uint64_t& x) {
+  const uint32_t h = narrow<T>(x);
+  x = tc::ffma2(widen<T>(h), both(-1.f), x);
+  return h;
 }
 
+// One lane of the (whole) warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
@@ -268,7 +309,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // roles: the summary has no score and output warps
   const int role = kSum ? (warp < 4 ? 1 : warp < 8 ? 2 : warp - 4) : (warp < 16 ? warp >> 2 : warp - 12);
-  enum { kP = 0, kBuild = 1, kState = 2, kOut = 3, kLoad = 4, kMma = 5 };
+  enum { kP = 0, kBuild = 1, kState = 2, kOut = 3, kLoad = 4, kMma = 5, kLoadQ = 6, kLoadZ = 7 };
   if ((saddr(sm) & 1023u) != 0u) {
     if (tid == 0) gtr_flag(kStatusBadShape);
     return;
@@ -301,13 +342,16 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   pdl_wait();
   pdl_trigger();
   const uint32_t tm = *tmem_slot;
-  const int half = (int)blockIdx.x % halves;
+  const int half = (int)blockIdx.x % halves, group_j = (int)blockIdx.x / halves;
+  Range rg;
+  locate<kC>(p, group_j, reinterpret_cast<long long*>(Gs), rg);
+  __syncthreads();                                             // the scratch becomes the decay sums
   const int w4 = warp & 3, row = w4 * 32 + lane;               // a token row, or a lane of an accumulator
   const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
-  const int group = p.H / p.Hk;
+  const int share = p.H / p.Hk;                                // heads of a key head
   const bool gated = p.z != nullptr;
-  const long long units = (long long)p.nslot * p.H;
   uint32_t it = 0;                                             // blocks of tokens since the start
+  uint32_t is = 0;                                             // those that had a state before them
   bool ok = true;
   auto wait = [&](int b, uint32_t parity) { return tc::mbar_wait(bar + b, parity); };
   // one arrival for a warp, after all its lanes
@@ -315,19 +359,25 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     __syncwarp();
     if (lane == 0) tc::mbar_arrive_one(bar + b);
   };
+  auto for_parts = [&](auto&& body) {
+    Part g;
+    if constexpr (kSum) {
+      if (cut_part<kC>(p, rg, g)) body(g);
+    } else {
+      Walk walk{rg.a, rg.x1 - rg.x0};
+      while (ok && next_part<kC>(p, walk, g)) body(g);
+    }
+  };
+  // the state after the part is needed / there is one before it
+  auto wants_end = [&](const Part& g) { return kSum || (g.last && p.state_out); };
+  auto has_start = [&](const Part& g) { return !kSum && (!g.first || g.start); };
 
-  for (long long unit = (int)blockIdx.x / halves; unit < units && ok; unit += (int)gridDim.x / halves) {
-    Segment g;
-    const int h = (int)(unit % p.H), hk = h / group;
-    if (!find_segment(p, (int)(unit / p.H), g)) continue;
-    const bool last = g.i >= g.m - 1;
-    if (kSum && last) continue;
-    const int nb = (g.len + kC - 1) / kC;
-    const bool want_end = kSum || (last && p.state_out);       // the state after the segment is needed
-
-    if (role == kLoad) {
+  if (role == kLoad) {
+    if constexpr (!kSum) fewer_registers<48>();
+    for_parts([&](const Part& g) {
+      const int hk = g.h / share;
       if (lane == 0) {
-        for (int c = 0; c < nb && ok; ++c) {
+        for (int c = 0; c < g.nb && ok; ++c) {
           const uint32_t i = it + c;
           const int t = g.t0 + c * kC;
           const int sk = i % L::kNK, sv = i % L::kNV;
@@ -336,92 +386,95 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           tc::mbar_arrive_tx(bar + kKF + sk, L::kQTile);
           for (int x = 0; x < DK / 64; ++x)
             tma_load_3d(sm + L::kK + sk * L::kQTile + x * kTile, &maps.k, x * 64, hk, t, bar + kKF + sk);
-          if constexpr (!kSum) {
-            if (L::kNQ == 1)
-              for (int x = 0; x < DK / 64; ++x) tma_prefetch_3d(&maps.q, x * 64, hk, t);
-          }
           ok = wait(kVE + sv, (i / L::kNV & 1) ^ 1);
           if (!ok) break;
           tc::mbar_arrive_tx(bar + kVF + sv, kTile);
-          tma_load_3d(sm + L::kV + sv * kTile, &maps.v, half * 64, h, t, bar + kVF + sv);
-          if constexpr (!kSum) {
-            if (gated) {
-              const int sz = i % L::kNZ;
-              ok = wait(kZE + sz, (i / L::kNZ & 1) ^ 1);
-              if (!ok) break;
-              tc::mbar_arrive_tx(bar + kZF + sz, kTile);
-              tma_load_3d(sm + L::kZ + sz * kTile, &maps.z, half * 64, h, t, bar + kZF + sz);
-            }
-            const int sq = i % L::kNQ;
-            ok = wait(kQE + sq, (i / L::kNQ & 1) ^ 1);
-            if (!ok) break;
-            tc::mbar_arrive_tx(bar + kQF + sq, L::kQTile);
-            for (int x = 0; x < DK / 64; ++x)
-              tma_load_3d(sm + L::kQ + sq * L::kQTile + x * kTile, &maps.q, x * 64, hk, t, bar + kQF + sq);
-          }
+          tma_load_3d(sm + L::kV + sv * kTile, &maps.v, half * 64, g.h, t, bar + kVF + sv);
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
-    } else if (role == kMma) {
-      if (lane == 0) {
-        constexpr uint32_t kIdSc = idesc(kBf16, 0, 0, 128, 128), kIdQS = idesc(kBf16, 0, 1, 128, 128);
-        constexpr uint32_t kIdKV = idesc(kBf16, 1, 1, DK, 128), kIdKV3 = idesc(kBf16, 1, 1, DK, 64);
-        constexpr uint32_t kIdPV = idesc(kBf16, 0, 1, 128, 64);
-        for (int c = 0; c < nb && ok; ++c) {
-          const uint32_t i = it + c, par = i & 1;
-          const int sk = i % L::kNK, sv = i % L::kNV;
-          const uint8_t* K = sm + L::kK + sk * L::kQTile;
-          const uint8_t* V = sm + L::kV + sv * kTile;
-          const uint8_t* W = sm + L::kW;
-          ok = wait(kKF + sk, i / L::kNK & 1);
-          if constexpr (!kSum) {
-            const int sq = i % L::kNQ;
-            const uint8_t* Q = sm + L::kQ + sq * L::kQTile;
-            ok = ok && wait(kQF + sq, i / L::kNQ & 1);
-            if (!ok) break;
-            tc::tc_after_sync();
-            const uint64_t aq = tc::sdesc(saddr(Q), 16, 1024), bk = tc::sdesc(saddr(K), 16, 1024);
+      it += g.nb;
+    });
+  } else if (role == kMma) {
+    if constexpr (!kSum) fewer_registers<48>();
+    const bool lead = elect_one();
+    for_parts([&](const Part& g) {
+      constexpr uint32_t kIdSc = idesc(kBf16, 0, 0, 128, 128), kIdQS = idesc(kBf16, 0, 1, 128, 128);
+      constexpr uint32_t kIdKV = idesc(kBf16, 1, 1, DK, 128), kIdKV3 = idesc(kBf16, 1, 1, DK, 64);
+      constexpr uint32_t kIdPV = idesc(kBf16, 0, 1, 128, 64);
+      // the same in every lane; the reduction says so to the compiler
+      const int nb = (int)__reduce_max_sync(0xffffffffu, (unsigned)g.nb);
+      const bool want_end = wants_end(g);
+      for (int c = 0; c < nb && ok; ++c) {
+        const uint32_t i = it + c, par = i & 1;
+        const int sk = i % L::kNK, sv = i % L::kNV;
+        const uint8_t* K = sm + L::kK + sk * L::kQTile;
+        const uint8_t* V = sm + L::kV + sv * kTile;
+        const uint8_t* W = sm + L::kW;
+        ok = wait(kKF + sk, i / L::kNK & 1);
+        if constexpr (!kSum) {
+          const int sq = i % L::kNQ;
+          const uint8_t* Q = sm + L::kQ + sq * L::kQTile;
+          ok = ok && wait(kQF + sq, i / L::kNQ & 1);
+          if (!ok) break;
+          tc::tc_after_sync();
+          const uint64_t aq = tc::sdesc(saddr(Q), 16, 1024), bk = tc::sdesc(saddr(K), 16, 1024);
+          if (lead) {
 #pragma unroll
             for (int s = 0; s < DK / 16; ++s) {
               const uint64_t o = (uint64_t)((s >> 2) * (kTile >> 4) + (s & 3) * tc::kStepK);
               tc::mma_f16(tm + kTmSc, aq + o, bk + o, kIdSc, s > 0);
             }
             tc::mma_commit(bar + kScF);
-            ok = wait(kSF, par) && wait(kOE, par ^ 1);          // S terms; qs and pv of the block before are read
+          }
+          __syncwarp();
+          ok = wait(kOE, par ^ 1);                               // qs and pv of the block before are read
+          if (!ok) break;
+          if (c > 0 || has_start(g)) {
+            ok = wait(kSF, is & 1);
             if (!ok) break;
             tc::tc_after_sync();
             const uint64_t bs = tc::sdesc(saddr(sm + L::kS), L::kSTile, 1024);
+            if (lead) {
 #pragma unroll
-            for (int s = 0; s < DK / 16; ++s) {
-              const uint64_t o = (uint64_t)((s >> 2) * (kTile >> 4) + (s & 3) * tc::kStepK);
-              tc::mma_f16(tm + kTmQS, aq + o, bs + s * tc::kStepMN, kIdQS, s > 0);
+              for (int s = 0; s < DK / 16; ++s) {
+                const uint64_t o = (uint64_t)((s >> 2) * (kTile >> 4) + (s & 3) * tc::kStepK);
+                tc::mma_f16(tm + kTmQS, aq + o, bs + s * tc::kStepMN, kIdQS, s > 0);
+              }
+              tc::mma_commit(bar + kSE);
             }
-            tc::mma_commit(bar + kQE + sq);
-            tc::mma_commit(bar + kSE);
+            ++is;
           }
-          ok = ok && wait(kWF, par) && wait(kKvE, par ^ 1);
-          if (!ok) break;
-          tc::tc_after_sync();
-          if (c + 1 < nb || want_end) {
-            const uint64_t ak = tc::sdesc(saddr(K), kTile, 1024), bw = tc::sdesc(saddr(W), kTile, 1024);
+          if (lead) tc::mma_commit(bar + kQE + sq);
+          __syncwarp();
+        }
+        ok = ok && wait(kWF, par) && wait(kKvE, par ^ 1);
+        if (!ok) break;
+        tc::tc_after_sync();
+        if ((c + 1 < nb || want_end) && lead) {
+          const uint64_t ak = tc::sdesc(saddr(K), kTile, 1024), bw = tc::sdesc(saddr(W), kTile, 1024);
+#pragma unroll
+          for (int s = 0; s < kC / 16; ++s)
+            tc::mma_f16(tm + kTmKV, ak + s * tc::kStepMN, bw + s * tc::kStepMN, kIdKV, s > 0);
+          if (L::kTerms == 3) {
+            const uint64_t bw3 = tc::sdesc(saddr(W + 2 * kTile), kTile, 1024);
 #pragma unroll
             for (int s = 0; s < kC / 16; ++s)
-              tc::mma_f16(tm + kTmKV, ak + s * tc::kStepMN, bw + s * tc::kStepMN, kIdKV, s > 0);
-            if (L::kTerms == 3) {
-              const uint64_t bw3 = tc::sdesc(saddr(W + 2 * kTile), kTile, 1024);
-#pragma unroll
-              for (int s = 0; s < kC / 16; ++s)
-                tc::mma_f16(tm + kTmKV + 64, ak + s * tc::kStepMN, bw3 + s * tc::kStepMN, kIdKV3, 1u);
-            }
+              tc::mma_f16(tm + kTmKV + 64, ak + s * tc::kStepMN, bw3 + s * tc::kStepMN, kIdKV3, 1u);
           }
+        }
+        if (lead) {
           tc::mma_commit(bar + kKvF);
           tc::mma_commit(bar + kWE);
           tc::mma_commit(bar + kKE + sk);
-          if constexpr (!kSum) {
-            ok = wait(kPF, par);
-            if (!ok) break;
-            tc::tc_after_sync();
-            const uint64_t bv = tc::sdesc(saddr(V), kTile, 1024);
+        }
+        __syncwarp();
+        if constexpr (!kSum) {
+          ok = wait(kPF, par);
+          if (!ok) break;
+          tc::tc_after_sync();
+          const uint64_t bv = tc::sdesc(saddr(V), kTile, 1024);
+          if (lead) {
 #pragma unroll
             for (int s = 0; s < kC / 16; ++s)
               tc::mma_f16_ts(tm + kTmPV, tm + kTmSc + 8 * s, bv + s * tc::kStepMN, kIdPV, s > 0);
@@ -430,19 +483,28 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
               tc::mma_f16_ts(tm + kTmPV, tm + kTmPlo + 8 * s, bv + s * tc::kStepMN, kIdPV, 1u);
             tc::mma_commit(bar + kPvF);
           }
-          tc::mma_commit(bar + kVE + sv);
         }
+        if (lead) tc::mma_commit(bar + kVE + sv);
+        __syncwarp();
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    } else if (role == kBuild) {
-      float l = row < g.len ? load_decay(p, g.t0 + row, h) : 0.f;
-      for (int c = 0; c < nb && ok; ++c) {
+      it += nb;
+    });
+    if (ok && it > 0) {
+      // the last arrival a product makes on this memory
+      const uint32_t i = it - 1;
+      ok = wait(kVE + i % L::kNV, i / L::kNV & 1);
+    }
+  } else if (role == kBuild) {
+    for_parts([&](const Part& g) {
+      const bool want_end = wants_end(g);
+      float l = row < g.len ? load_decay(p, g.t0 + row, g.h) : 0.f;
+      for (int c = 0; c < g.nb && ok; ++c) {
         const uint32_t i = it + c, par = i & 1;
         const int nv = min(kC, g.len - c * kC);                  // tokens of this block
         const float lc = l;
-        if (c + 1 < nb) {
+        if (c + 1 < g.nb) {
           const int r = (c + 1) * kC + row;
-          l = r < g.len ? load_decay(p, g.t0 + r, h) : 0.f;
+          l = r < g.len ? load_decay(p, g.t0 + r, g.h) : 0.f;
         }
         // inclusive sums from the front, exclusive ones from the back
         float pre = lc, suf = lc;
@@ -472,36 +534,34 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         ok = wait(kVF + sv, i / L::kNV & 1);
         if (!ok) break;
         uint8_t* V = sm + L::kV + sv * kTile + row * 128;
-        const bool build = c + 1 < nb || want_end;
+        const bool build = c + 1 < g.nb || want_end;
         const bool live = row < nv;
         const float w = tc::ex2(R);
         uint4 v[8];
         if (build) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const uint4*>(V + ((u ^ (row & 7)) << 4));
+          for (int u = 0; u < 8; ++u) {
+            v[u] = *reinterpret_cast<const uint4*>(V + ((u ^ (row & 7)) << 4));
+            if (!live) v[u] = make_uint4(0, 0, 0, 0);            // others' data, maybe NaN
+          }
         }
         float up = 1.f;
         int exp_w = 0;
         if (!kBf16 && build) {
           // a power of two that brings the block's largest |w v| under 2^15
-          float m = 0.f;
-          if (live) {
-            uint32_t mx = 0;                                     // |fp16| orders as its bits; a NaN or infinity on top
+          uint32_t mx = 0;                                       // |fp16| orders as its bits, NaN on top
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          for (int u = 0; u < 8; ++u) {
+            const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mx = __vmaxu2(mx, x[e] & 0x7fff7fffu);
-            }
-            const float2 f = widen<T>(mx);
-            m = fmaxf(f.x, f.y) * w;
+            for (int e = 0; e < 4; ++e) mx = __vmaxu2(mx, x[e] & 0x7fff7fffu);
           }
-          m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+          const float2 f = tc::f2unpack(widen<T>(mx));
+          const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(f.x, f.y) * w)));
           if (lane == 0) wmax[w4] = m;
           tc::named_barrier(1, 128);
-          const int e = tc::scale_exp(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])));
-          up = tc::pow2i(e);
-          exp_w = e;
+          exp_w = tc::scale_exp(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])));
+          up = tc::pow2i(exp_w);
         }
         ok = wait(kWE, par ^ 1);
         if (!ok) break;
@@ -509,18 +569,17 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           // the kv of the block before is done, so the one before that, with this slot's exponent, is read
           if (!kBf16 && row == 0) ew[i & 1] = exp_w;
           uint8_t* W = sm + L::kW + row * 128;
-          const float f = w * up;
+          const uint64_t f = both(w * up);
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
             uint32_t t[L::kTerms][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float2 y = widen<T>(x[e]);
-              y.x = live ? y.x * f : 0.f;
-              y.y = live ? y.y * f : 0.f;
+              uint64_t y = tc::fmul2(widen<T>(x[e]), f);
 #pragma unroll
-              for (int n = 0; n < L::kTerms; ++n) t[n][e] = term<T>(y.x, y.y);
+              for (int n = 0; n + 1 < L::kTerms; ++n) t[n][e] = term<T>(y);
+              t[L::kTerms - 1][e] = narrow<T>(y);
             }
             const int off = (u ^ (row & 7)) << 4;
 #pragma unroll
@@ -547,67 +606,72 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         tc::fence_async_smem();
         warp_arrive(kWF);
       }
-    } else if (role == kState) {
-      using SC = StateCols<DK>;
-      constexpr int kRuns = SC::kN / 16;
-      const int r = SC::row(w4, lane);
-      const size_t hs = (size_t)DK * p.dv;
-      float S[SC::kN];
-      {
-        const float* src = nullptr;
-        if (!kSum) src = start_state(p, g, h);
+      it += g.nb;
+    });
+  } else if (role == kState) {
+    if constexpr (!kSum) more_registers<112>();
+    using SC = StateCols<DK>;
+    constexpr int kRuns = SC::kN / 16;
+    const int r = SC::row(w4, lane);
+    uint64_t S[SC::kN / 2];                                       // two columns each
+    // S in two terms as the operand of the next block's qs
+    auto put = [&]() {
+      uint64_t up = both(1.f);
+      if (!kBf16) {
+        uint32_t mx = 0;
 #pragma unroll
-        for (int x = 0; x < kRuns; ++x) {
-          const size_t at = (size_t)r * p.dv + half * 64 + SC::col(x, lane);
+        for (int e = 0; e < SC::kN / 2; ++e) {
+          const float2 f = tc::f2unpack(S[e]);
+          mx = max(mx, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+        }
+        const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, mx));
+        if (lane == 0) wmax[4 + w4] = m;
+        tc::named_barrier(2, 128);
+        const int e = tc::scale_exp(fmaxf(fmaxf(wmax[4], wmax[5]), fmaxf(wmax[6], wmax[7])));
+        tc::named_barrier(2, 128);                               // read before the next block's are written
+        up = both(tc::pow2i(e));
+        if (w4 == 0 && lane == 0) es[is & 1] = e;
+      }
+      if (!wait(kSE, (is & 1) ^ 1)) return false;
+      ++is;
+      uint8_t* D = sm + L::kS + r * 128;
+#pragma unroll
+      for (int x = 0; x < kRuns; ++x) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float4 f = src ? *reinterpret_cast<const float4*>(src + at + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[16 * x + 4 * e] = f.x; S[16 * x + 4 * e + 1] = f.y;
-            S[16 * x + 4 * e + 2] = f.z; S[16 * x + 4 * e + 3] = f.w;
+            uint64_t a = S[8 * x + 4 * b + e];
+            if (!kBf16) a = tc::fmul2(a, up);
+            hi[e] = term<T>(a);
+            lo[e] = narrow<T>(a);
           }
+          const int off = ((SC::col(x, lane) / 8 + b) ^ (r & 7)) << 4;
+          *reinterpret_cast<uint4*>(D + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(D + L::kSTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
-      // S in two terms as the operand of block `i`'s qs
-      auto put = [&](uint32_t i) {
-        float up = 1.f;
-        if (!kBf16) {
-          float m = 0.f;
+      tc::fence_async_smem();
+      warp_arrive(kSF);
+      return true;
+    };
+    for_parts([&](const Part& g) {
+      const bool want_end = wants_end(g);
+      const size_t hs = (size_t)DK * p.dv, at = (size_t)r * p.dv + half * 64;
+      const float* src = kSum ? nullptr : start_state(p, g, group_j);
 #pragma unroll
-          for (int e = 0; e < SC::kN; ++e) m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(S[e]) & 0x7fffffffu));
-          m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-          if (lane == 0) wmax[4 + w4] = m;
-          tc::named_barrier(2, 128);
-          m = fmaxf(fmaxf(wmax[4], wmax[5]), fmaxf(wmax[6], wmax[7]));
-          tc::named_barrier(2, 128);                             // read before the next block's are written
-          const int e = tc::scale_exp(m);
-          up = tc::pow2i(e);
-          if (w4 == 0 && lane == 0) es[i & 1] = e;
+      for (int x = 0; x < kRuns; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 f = src ? *reinterpret_cast<const float4*>(src + at + SC::col(x, lane) + 4 * e)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+          S[8 * x + 2 * e] = tc::f2pack(f.x, f.y);
+          S[8 * x + 2 * e + 1] = tc::f2pack(f.z, f.w);
         }
-        if (!wait(kSE, (i & 1) ^ 1)) return false;
-        uint8_t* D = sm + L::kS + r * 128;
-#pragma unroll
-        for (int x = 0; x < kRuns; ++x) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float a0 = S[16 * x + 8 * b + 2 * e] * up, a1 = S[16 * x + 8 * b + 2 * e + 1] * up;
-              hi[e] = term<T>(a0, a1);
-              lo[e] = term<T>(a0, a1);
-            }
-            const int off = ((SC::col(x, lane) / 8 + b) ^ (r & 7)) << 4;
-            *reinterpret_cast<uint4*>(D + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(D + L::kSTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        }
-        tc::fence_async_smem();
-        warp_arrive(kSF);
-        return true;
-      };
-      if (!kSum && nb > 0) ok = put(it);
+      if (g.nb > 0 && has_start(g)) ok = put();
       float total = 0.f;
-      for (int c = 0; c < nb && ok; ++c) {
+      for (int c = 0; c < g.nb && ok; ++c) {
         const uint32_t i = it + c, par = i & 1;
         ok = wait(kGF + (i & 1), i >> 1 & 1);
         if (!ok) break;
@@ -616,10 +680,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         ok = wait(kKvF, par);
         if (!ok) break;
         tc::tc_after_sync();
-        if (c + 1 < nb || want_end) {
+        if (c + 1 < g.nb || want_end) {
           total += la;
-          const float a = tc::ex2(la);
-          const float down = kBf16 ? 1.f : tc::pow2i(-ew[i & 1]);
+          const uint64_t a = both(tc::ex2(la));
+          const uint64_t down = both(kBf16 ? 1.f : tc::pow2i(-ew[i & 1]));
 #pragma unroll
           for (int x = 0; x < kRuns; ++x) {
             uint32_t hi[16], lo[16];
@@ -633,218 +697,287 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             tm_wait(hi);
             tm_wait(lo);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              S[16 * x + e] = fmaf(a, S[16 * x + e], (__uint_as_float(hi[e]) + __uint_as_float(lo[e])) * down);
+            for (int e = 0; e < 8; ++e) {
+              uint64_t d = add2(pack2(hi[2 * e], hi[2 * e + 1]), pack2(lo[2 * e], lo[2 * e + 1]));
+              if (!kBf16) d = tc::fmul2(d, down);
+              S[8 * x + e] = tc::ffma2(a, S[8 * x + e], d);
+            }
           }
         }
         tc::tc_before_sync();
         warp_arrive(kKvE);
-        if (!kSum && c + 1 < nb) ok = put(i + 1);
+        if (!kSum && c + 1 < g.nb) ok = put();
       }
+      it += g.nb;
       if (ok && want_end) {
-        float* dst = kSum ? p.wsS + ((size_t)(g.ws + g.i) * p.H + h) * hs : p.state_out + ((size_t)g.slot * p.H + h) * hs;
+        float* dst = kSum ? p.wsS + (size_t)group_j * hs : p.state_out + ((size_t)g.slot * p.H + g.h) * hs;
 #pragma unroll
-        for (int x = 0; x < kRuns; ++x) {
-          float4* d4 = reinterpret_cast<float4*>(dst + (size_t)r * p.dv + half * 64 + SC::col(x, lane));
+        for (int x = 0; x < kRuns; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            d4[e] = make_float4(S[16 * x + 4 * e], S[16 * x + 4 * e + 1], S[16 * x + 4 * e + 2], S[16 * x + 4 * e + 3]);
-        }
-        if (kSum && half == 0 && w4 == 0 && lane == 0) p.wsA[(size_t)(g.ws + g.i) * p.H + h] = total;
-      }
-    } else if (!kSum && role == kP) {
-      for (int c = 0; c < nb && ok; ++c) {
-        const uint32_t i = it + c, par = i & 1;
-        ok = wait(kGF + (i & 1), i >> 1 & 1) && wait(kScF, par);
-        if (!ok) break;
-        tc::tc_after_sync();
-        const float* G = Gs + (i & 1) * kC;
-        const float* U = Us + (i & 1) * kC;
-        const float Gi = G[row];
-        float up = 1.f;
-        if (!kBf16) {
-          // a power of two that brings the row's largest |score| under 2^15
-          uint32_t mx = 0;
-#pragma unroll 1
-          for (int b = 0; b <= w4; ++b) {
-            uint32_t s[32];
-            tm_ld32(tm + lane_base + kTmSc + 32 * b, s);
-            tm_wait(s);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx = max(mx, b < w4 || e <= lane ? s[e] & 0x7fffffffu : 0u);
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = tc::f2unpack(S[8 * x + 2 * e]), b = tc::f2unpack(S[8 * x + 2 * e + 1]);
+            *reinterpret_cast<float4*>(dst + at + SC::col(x, lane) + 4 * e) = make_float4(a.x, a.y, b.x, b.y);
           }
-          const int e = tc::scale_exp(__uint_as_float(mx));
-          up = tc::pow2i(e);
-          pexp[(i & 1) * kC + row] = (int8_t)e;
-        }
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          uint32_t hi[16], lo[16];
-          if (b > w4) {
+        if (kSum && half == 0 && w4 == 0 && lane == 0) p.wsA[group_j] = total;
+      }
+    });
+  } else if constexpr (!kSum) {
+    if (role == kP) {
+      {
+        // P lo right of the diagonal is zero for good
+        uint32_t zero[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0u;
-          } else {
-            uint32_t s[32];
-            tm_ld32(tm + lane_base + kTmSc + 32 * b, s);
-            tm_wait(s);
-            if (b == w4) {
-              const float4* g4 = reinterpret_cast<const float4*>(G + 32 * b);
+        for (int e = 0; e < 16; ++e) zero[e] = 0u;
+        for (int b = w4 + 1; b < 4; ++b) tm_st16(tm + lane_base + kTmPlo + 16 * b, zero);
+      }
+      for_parts([&](const Part& g) {
+        for (int c = 0; c < g.nb && ok; ++c) {
+          const uint32_t i = it + c, par = i & 1;
+          ok = wait(kGF + (i & 1), i >> 1 & 1) && wait(kScF, par);
+          if (!ok) break;
+          tc::tc_after_sync();
+          const float* G = Gs + (i & 1) * kC;
+          const float* U = Us + (i & 1) * kC;
+          const float Gi = G[row];
+          const uint32_t sc = tm + lane_base + kTmSc;
+          float up = 1.f;
+          if (!kBf16) {
+            // a power of two that brings the row's largest |score| under 2^15
+            uint32_t mx = 0;
+#pragma unroll 2
+            for (int b = 0; b <= 2 * w4 + 1; ++b) {
+              uint32_t x[16];
+              tm_ld16(sc + 16 * b, x);
+              tm_wait(x);
+              const int diag = lane + 32 * w4 - 16 * b;          // the row's last column of this run
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
+              for (int e = 0; e < 16; ++e) mx = max(mx, e <= diag ? x[e] & 0x7fffffffu : 0u);
+            }
+            const int e = tc::scale_exp(__uint_as_float(mx));
+            up = tc::pow2i(e);
+            pexp[(i & 1) * kC + row] = (int8_t)e;
+          }
+          // 16 columns at a time, the next ones loading; P hi goes over scores
+          // already read (columns [8 b, 8 b + 8) of 16-column run b / 2)
+          uint32_t s[2][16];
+          tm_ld16(sc, s[0]);
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            uint32_t hi[8], lo[8];
+            if (b >> 1 > w4) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) hi[e] = 0u;
+              tm_st8(sc + 8 * b, hi);
+              continue;
+            }
+            uint32_t(&x)[16] = s[b & 1];
+            tm_wait(x);
+            if (b < 7 && (b + 1) >> 1 <= w4) tm_ld16(sc + 16 * (b + 1), s[(b + 1) & 1]);
+            if (b >> 1 == w4) {
+              const float4* g4 = reinterpret_cast<const float4*>(G + 16 * b);
+              const int diag = lane - 16 * (b & 1);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
                 const float4 gj = g4[e];
                 const float d[4] = {gj.x, gj.y, gj.z, gj.w};
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  const float y = __uint_as_float(s[4 * e + x]) * (tc::ex2(Gi - d[x]) * up);
-                  s[4 * e + x] = 4 * e + x <= lane ? __float_as_uint(y) : 0u;
+                for (int y = 0; y < 4; ++y) {
+                  const float m = __uint_as_float(x[4 * e + y]) * (tc::ex2(Gi - d[y]) * up);
+                  x[4 * e + y] = 4 * e + y <= diag ? __float_as_uint(m) : 0u;
                 }
               }
-            } else {
-              const float f = tc::ex2(Gi - G[32 * b + 31]) * up;
-              const float4* u4 = reinterpret_cast<const float4*>(U + 32 * b);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float4 uj = u4[e];
-                s[4 * e] = __float_as_uint(__uint_as_float(s[4 * e]) * (uj.x * f));
-                s[4 * e + 1] = __float_as_uint(__uint_as_float(s[4 * e + 1]) * (uj.y * f));
-                s[4 * e + 2] = __float_as_uint(__uint_as_float(s[4 * e + 2]) * (uj.z * f));
-                s[4 * e + 3] = __float_as_uint(__uint_as_float(s[4 * e + 3]) * (uj.w * f));
+                uint64_t y = pack2(x[2 * e], x[2 * e + 1]);
+                hi[e] = term<T>(y);
+                lo[e] = narrow<T>(y);
+              }
+            } else {
+              const uint64_t f = both(tc::ex2(Gi - G[16 * (b | 1) + 15]) * up);
+              const ulonglong2* u2 = reinterpret_cast<const ulonglong2*>(U + 16 * b);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const ulonglong2 uj = u2[e];
+                uint64_t y = tc::fmul2(pack2(x[4 * e], x[4 * e + 1]), tc::fmul2(uj.x, f));
+                hi[2 * e] = term<T>(y);
+                lo[2 * e] = narrow<T>(y);
+                y = tc::fmul2(pack2(x[4 * e + 2], x[4 * e + 3]), tc::fmul2(uj.y, f));
+                hi[2 * e + 1] = term<T>(y);
+                lo[2 * e + 1] = narrow<T>(y);
               }
             }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float a0 = __uint_as_float(s[2 * e]), a1 = __uint_as_float(s[2 * e + 1]);
-              hi[e] = term<T>(a0, a1);
-              lo[e] = term<T>(a0, a1);
-            }
+            tm_st8(sc + 8 * b, hi);
+            tm_st8(tm + lane_base + kTmPlo + 8 * b, lo);
           }
-          // hi over scores already read (columns [16 b, 16 b + 16) of block b / 2)
-          tm_st16(tm + lane_base + kTmSc + 16 * b, hi);
-          tm_st16(tm + lane_base + kTmPlo + 16 * b, lo);
+          tc::tmem_st_wait();
+          tc::tc_before_sync();
+          warp_arrive(kPF);
+          warp_arrive(kGE + (i & 1));
         }
-        tc::tmem_st_wait();
-        tc::tc_before_sync();
-        warp_arrive(kPF);
-        warp_arrive(kGE + (i & 1));
-      }
-    } else if (!kSum && role == kOut) {
+        it += g.nb;
+      });
+    } else if (role == kOut) {
+      more_registers<128>();
       const uint32_t rank = kPair ? blockIdx.x & 1u : 0u;
-      for (int c = 0; c < nb && ok; ++c) {
-        const uint32_t i = it + c, par = i & 1;
-        const int nv = min(kC, g.len - c * kC);
-        ok = wait(kGF + (i & 1), i >> 1 & 1);
-        if (!ok) break;
-        const float Gi = Gs[(i & 1) * kC + row];
-        warp_arrive(kGE + (i & 1));
-        ok = wait(kPvF, par);
-        if (!ok) break;
-        tc::tc_after_sync();
-        float f1 = p.scale * tc::ex2(Gi), f2 = p.scale;
-        if (!kBf16) {
-          f1 *= tc::pow2i(-es[i & 1]);
-          f2 *= tc::pow2i(-(int)pexp[(i & 1) * kC + row]);
-        }
-        float o[64];
-        float ss = 0.f;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t a[16], b[16], d[16];
-          tm_ld16(tm + lane_base + kTmQS + 16 * x, a);
-          tm_ld16(tm + lane_base + kTmQS + 64 + 16 * x, b);
-          tm_ld16(tm + lane_base + kTmPV + 16 * x, d);
-          tm_wait(a);
-          tm_wait(b);
-          tm_wait(d);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float y = fmaf(f1, __uint_as_float(a[e]) + __uint_as_float(b[e]), f2 * __uint_as_float(d[e]));
-            o[16 * x + e] = y;
-            ss = fmaf(y, y, ss);
-          }
-        }
-        tc::tc_before_sync();
-        warp_arrive(kOE);
-        const int sz = i % L::kNZ;
-        uint8_t* Z = sm + L::kZ + sz * kTile;
-        float inv = 1.f;
-        if (gated) {
-          if constexpr (kPair) {
-            // the other half's sum of this row; its copy of ours is free once it has read the block before
-            ok = cluster_wait(bar + kXE, par ^ 1);
-            if (!ok) break;
-            peer_store(peer_addr(saddr(Xs + row), rank ^ 1u), ss);
-            peer_arrive(peer_addr(saddr(bar + kXF), rank ^ 1u));
-            ok = cluster_wait(bar + kXF, par);
-            if (!ok) break;
-            ss += *reinterpret_cast<volatile float*>(Xs + row);
-            peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));
-          }
-          inv = rsqrtf(ss / (float)p.dv + kRmsEps);
-          ok = wait(kZF + sz, i / L::kNZ & 1);
+      for_parts([&](const Part& g) {
+        for (int c = 0; c < g.nb && ok; ++c) {
+          const uint32_t i = it + c, par = i & 1;
+          const int nv = min(kC, g.len - c * kC);
+          ok = wait(kGF + (i & 1), i >> 1 & 1);
           if (!ok) break;
-        } else {
-          // the copies of the block that used this buffer before are done
-          tc::named_barrier(3, 128);
-        }
-        const float4* w4p = reinterpret_cast<const float4*>(p.w + half * 64);
+          const float Gi = Gs[(i & 1) * kC + row];
+          warp_arrive(kGE + (i & 1));
+          ok = wait(kPvF, par);
+          if (!ok) break;
+          tc::tc_after_sync();
+          const bool state = c > 0 || has_start(g);
+          float f1 = p.scale * tc::ex2(Gi), f2 = p.scale;
+          if (!kBf16) {
+            f1 *= tc::pow2i(-es[is & 1]);
+            f2 *= tc::pow2i(-(int)pexp[(i & 1) * kC + row]);
+          }
+          const uint64_t f11 = both(f1), f22 = both(f2);
+          uint64_t o[32];
+          uint64_t ss2 = both(0.f);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint4* unit16 = reinterpret_cast<uint4*>(Z + row * 128 + ((u ^ (row & 7)) << 4));
+          for (int x = 0; x < 4; ++x) {
+            uint32_t a[16], b[16], d[16];
+            tm_ld16(tm + lane_base + kTmPV + 16 * x, d);
+            if (state) {
+              tm_ld16(tm + lane_base + kTmQS + 16 * x, a);
+              tm_ld16(tm + lane_base + kTmQS + 64 + 16 * x, b);
+              tm_wait(a);
+              tm_wait(b);
+            }
+            tm_wait(d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              uint64_t y = tc::fmul2(f22, pack2(d[2 * e], d[2 * e + 1]));
+              if (state)
+                y = tc::ffma2(f11, add2(pack2(a[2 * e], a[2 * e + 1]), pack2(b[2 * e], b[2 * e + 1])), y);
+              o[8 * x + e] = y;
+              ss2 = tc::ffma2(y, y, ss2);
+            }
+          }
+          if (state) ++is;
+          tc::tc_before_sync();
+          warp_arrive(kOE);
+          const int sz = i % L::kNZ;
+          uint8_t* Z = sm + L::kZ + sz * kTile;
+          uint64_t inv2 = both(1.f);
           if (gated) {
-            const uint4 zu = *unit16;
-            const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
-            float wt[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-            if (p.w) {
-              const float4 wa = __ldg(w4p + 2 * u), wb = __ldg(w4p + 2 * u + 1);
-              wt[0] = wa.x; wt[1] = wa.y; wt[2] = wa.z; wt[3] = wa.w;
-              wt[4] = wb.x; wt[5] = wb.y; wt[6] = wb.z; wt[7] = wb.w;
+            const float2 sf = tc::f2unpack(ss2);
+            float ss = sf.x + sf.y;
+            if constexpr (kPair) {
+              // the other half's sum of this row; its copy of ours is free once it has read the block before
+              ok = cluster_wait(bar + kXE, par ^ 1);
+              if (!ok) break;
+              peer_store(peer_addr(saddr(Xs + row), rank ^ 1u), ss);
+              peer_arrive(peer_addr(saddr(bar + kXF), rank ^ 1u));
+              ok = cluster_wait(bar + kXF, par);
+              if (!ok) break;
+              ss += *reinterpret_cast<volatile float*>(Xs + row);
+              peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));
             }
+            inv2 = both(rsqrtf(ss / (float)p.dv + kRmsEps));
+            ok = wait(kZF + sz, i / L::kNZ & 1);
+            if (!ok) break;
+          } else {
+            // the copies of the block that used this buffer before are done
+            tc::named_barrier(3, 128);
+          }
+          const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(p.w + half * 64);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 z = widen<T>(zw[e]);
-              o[8 * u + 2 * e] *= inv * wt[2 * e] * __fdividef(z.x, 1.0f + __expf(-z.x));
-              o[8 * u + 2 * e + 1] *= inv * wt[2 * e + 1] * __fdividef(z.y, 1.0f + __expf(-z.y));
+          for (int u = 0; u < 8; ++u) {
+            uint4* unit16 = reinterpret_cast<uint4*>(Z + row * 128 + ((u ^ (row & 7)) << 4));
+            uint64_t y[4] = {o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]};
+            if (gated) {
+              const uint4 zu = *unit16;
+              const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
+              uint64_t wt[4] = {inv2, inv2, inv2, inv2};
+              if (p.w) {
+                const ulonglong2 wa = __ldg(wp + 2 * u), wb = __ldg(wp + 2 * u + 1);
+                wt[0] = tc::fmul2(wa.x, inv2); wt[1] = tc::fmul2(wa.y, inv2);
+                wt[2] = tc::fmul2(wb.x, inv2); wt[3] = tc::fmul2(wb.y, inv2);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // z sigmoid(z) = z / (1 + 2^(-z log2 e))
+                const uint64_t z = widen<T>(zw[e]);
+                const float2 m = tc::f2unpack(tc::fmul2(z, both(-kLog2e)));
+                const float2 q = tc::f2unpack(add2(tc::f2pack(tc::ex2(m.x), tc::ex2(m.y)), both(1.f)));
+                const float2 zf = tc::f2unpack(z);
+                y[e] = tc::fmul2(tc::fmul2(y[e], wt[e]), tc::f2pack(__fdividef(zf.x, q.x), __fdividef(zf.y, q.y)));
+              }
+            }
+            *unit16 = make_uint4(narrow<T>(y[0]), narrow<T>(y[1]), narrow<T>(y[2]), narrow<T>(y[3]));
+          }
+          tc::named_barrier(3, 128);
+          {
+            const int u = row & 7;
+            T* dst = (T*)p.out + (long long)(g.t0 + c * kC) * p.ldo + (long long)g.h * p.dv + half * 64 + u * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int r = (row >> 3) + 16 * e;
+              if (r < nv)
+                *reinterpret_cast<uint4*>(dst + r * p.ldo) =
+                    *reinterpret_cast<const uint4*>(Z + r * 128 + ((u ^ (r & 7)) << 4));
             }
           }
-          uint32_t y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = word<T>(T2<T>::from(o[8 * u + 2 * e], o[8 * u + 2 * e + 1]));
-          *unit16 = make_uint4(y[0], y[1], y[2], y[3]);
-        }
-        tc::named_barrier(3, 128);
-        {
-          const int u = row & 7;
-          T* dst = (T*)p.out + (long long)(g.t0 + c * kC) * p.ldo + (long long)h * p.dv + half * 64 + u * 8;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = (row >> 3) + 16 * e;
-            if (r < nv)
-              *reinterpret_cast<uint4*>(dst + r * p.ldo) =
-                  *reinterpret_cast<const uint4*>(Z + r * 128 + ((u ^ (r & 7)) << 4));
+          if (gated) {
+            tc::fence_async_smem();                             // the next z is written by the async proxy
+            tc::mbar_arrive_one(bar + kZE + sz);
           }
         }
-        if (gated) {
-          tc::fence_async_smem();                               // the next z is written by the async proxy
-          tc::mbar_arrive_one(bar + kZE + sz);
+        it += g.nb;
+      });
+    } else if (role == kLoadQ) {
+      fewer_registers<48>();
+      for_parts([&](const Part& g) {
+        const int hk = g.h / share;
+        if (lane == 0) {
+          for (int c = 0; c < g.nb && ok; ++c) {
+            const uint32_t i = it + c;
+            const int t = g.t0 + c * kC, sq = i % L::kNQ;
+            if (L::kNQ == 1)                                     // one buffer: at least from memory into L2
+              for (int x = 0; x < DK / 64; ++x) tma_prefetch_3d(&maps.q, x * 64, hk, t);
+            ok = wait(kQE + sq, (i / L::kNQ & 1) ^ 1);
+            if (!ok) break;
+            tc::mbar_arrive_tx(bar + kQF + sq, L::kQTile);
+            for (int x = 0; x < DK / 64; ++x)
+              tma_load_3d(sm + L::kQ + sq * L::kQTile + x * kTile, &maps.q, x * 64, hk, t, bar + kQF + sq);
+          }
         }
-      }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        it += g.nb;
+      });
+    } else if (role == kLoadZ) {
+      fewer_registers<48>();
+      if (gated)
+        for_parts([&](const Part& g) {
+          if (lane == 0) {
+            for (int c = 0; c < g.nb && ok; ++c) {
+              const uint32_t i = it + c;
+              const int sz = i % L::kNZ;
+              ok = wait(kZE + sz, (i / L::kNZ & 1) ^ 1);
+              if (!ok) break;
+              tc::mbar_arrive_tx(bar + kZF + sz, kTile);
+              tma_load_3d(sm + L::kZ + sz * kTile, &maps.z, half * 64, g.h, g.t0 + c * kC, bar + kZF + sz);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          it += g.nb;
+        });
     }
-    it += nb;
   }
   // a bounded wait that ran out ends every warp's walk the same way; loads and
-  // products in flight are waited for (bounded) before the memory is given up
-  if (!ok && lane == 0) gtr_flag(kStatusMbarTimeout);
-  __syncwarp();
-  if (role == kMma && ok && it > 0) {
-    // the last arrival a product makes on this memory
-    const uint32_t i = it - 1;
-    ok = wait(kVE + i % L::kNV, i / L::kNV & 1);
-    if (!ok && lane == 0) gtr_flag(kStatusMbarTimeout);
-  }
-  if (role == kLoad && !ok && lane == 0) {
+  // products in flight get time to land before the memory is given up
+  if (!ok && lane == 0) {
+    gtr_flag(kStatusMbarTimeout);
     const unsigned long long t0 = tc::globaltimer();
     while (tc::globaltimer() - t0 < 2000000ull) {}
   }
+  __syncwarp();
   tc::tc_before_sync();
   __syncthreads();
   if constexpr (kPair) cluster_sync();

@@ -177,53 +177,64 @@ def test_argument_struct_has_the_headers_size(tmp_path):
     assert nseq == 13 * 8 + 8 + 5 * 8
 
 
-# ------------------------------------------------------- segment arithmetic
-def _segments(cu, T, L):
-    """The kernels' slot and workspace arithmetic (hla_common.cuh), for one cu_seqlens."""
-    nseq = len(cu) - 1
-    a = [min(max(c, 0), T) for c in cu[:-1]]
-    b = [min(max(c, x), T) for c, x in zip(cu[1:], a)]
-    found = []
-    for s in range(T // L + nseq):
-        count = sum(x // L + j <= s for j, x in enumerate(a))
-        if count == 0:
-            continue
-        n = count - 1
-        m = -(-(b[n] - a[n]) // L)
-        i = s - (a[n] // L + n)
-        if 0 <= i < max(m, 1):
-            found.append((n, i, m, a[n] // L + i))
-    return a, b, found
+# --------------------------------------------------- the split of the work
+def _ranges(lens, H, C, groups):
+    """The kernels' arithmetic (hla_common.cuh): the parts of every group and the cuts."""
+    nb = [max(1, -(-n // C)) for n in lens]
+    B = H * sum(nb)
+    J = min(groups, B)
+    starts = []                                     # first place of each sequence
+    x = 0
+    for n in nb:
+        starts.append(x)
+        x += n * H
+    parts, cuts = [], []
+    for j in range(groups):
+        x0, x1 = B * min(j, J) // J, B * min(j + 1, J) // J
+        mine, x = [], x0
+        while x < x1:
+            n = max(i for i, s in enumerate(starts) if s <= x)
+            h, b0 = divmod(x - starts[n], nb[n])
+            take = min(nb[n] - b0, x1 - x)
+            mine.append((n, h, b0, take))
+            x += take
+        parts.append(mine)
+        if x1 < B and x1 > x0:
+            n = max(i for i, s in enumerate(starts) if s <= x1)
+            h, e = divmod(x1 - starts[n], nb[n])
+            if e:
+                b0 = 0 if e <= x1 - x0 else e - (x1 - x0)
+                m = 0
+                if b0 == 0:                          # the scan's walk from here
+                    end, m = x1 - e + nb[n], 1
+                    while j + m < J and B * (j + m + 1) // J < end:
+                        m += 1
+                cuts.append((j, n, h, b0, e - b0, m))
+    return nb, J, parts, cuts
 
 
-def test_segment_slots_and_summaries_are_distinct_and_in_range():
+def test_every_block_is_in_one_part_and_every_cut_is_scanned():
     rng = random.Random(3)
-    for _ in range(400):
-        L = rng.choice([128, 256, 1280])
-        lens = [rng.choice([0, 1, L - 1, L, L + 1, rng.randrange(5 * L)]) for _ in range(rng.randrange(1, 9))]
-        cu = [rng.randrange(3)]
-        for n in lens:
-            cu.append(cu[-1] + n)
-        T = cu[-1] + rng.randrange(3)
-        a, b, found = _segments(cu, T, L)
-        want = {(n, i) for n in range(len(lens)) for i in range(max(1, -(-lens[n] // L)))}
-        assert {(n, i) for n, i, _, _ in found} == want and len(found) == len(want)
-        entries = [w for _, i, m, w in found if i < m - 1]
-        assert len(set(entries)) == len(entries) and all(0 <= w < T // L + 1 for w in entries)
-        # the scan finds each sequence of several segments from its first entry
-        for n in range(len(lens)):
-            if -(-lens[n] // L) > 1:
-                last = sum(x // L <= a[n] // L for x in a) - 1
-                assert last == n
-
-
-def test_malformed_offsets_stay_in_range():
-    rng = random.Random(4)
     for _ in range(300):
-        L, T = 128, rng.randrange(1, 2000)
-        cu = [rng.randrange(-3000, 5000) for _ in range(rng.randrange(2, 8))]
-        a, b, found = _segments(cu, T, L)
-        for n, i, m, w in found:
-            assert 0 <= a[n] + i * L <= T and 0 <= a[n] <= b[n] <= T
-            if i < m - 1:
-                assert 0 <= w < T // L + 1
+        C = rng.choice([16, 128])
+        lens = [rng.choice([0, 1, C - 1, C, C + 1, rng.randrange(9 * C)]) for _ in range(rng.randrange(1, 9))]
+        H, groups = rng.choice([1, 3, 8]), rng.choice([1, 5, 74, 148])
+        nb, J, parts, cuts = _ranges(lens, H, C, groups)
+        seen = [(n, h, b) for mine in parts for n, h, b0, take in mine for b in range(b0, b0 + take)]
+        assert seen == [(n, h, b) for n in range(len(lens)) for h in range(H) for b in range(nb[n])]
+        assert all(parts[j] for j in range(J)) and not any(parts[J:])     # no empty group between two others
+        # a part that does not start its (sequence, head) starts its group, and the group before has its summary
+        entry = {j: (n, h, b0 + k) for j, n, h, b0, k, _ in cuts}
+        for j, mine in enumerate(parts):
+            for x, (n, h, b0, take) in enumerate(mine):
+                if b0:
+                    assert x == 0 and entry[j - 1] == (n, h, b0)
+            n, h, b0, take = mine[-1] if mine else (0, 0, 0, 0)
+            if mine and b0 + take < nb[n]:
+                assert [(c[3], c[4]) for c in cuts if c[0] == j] == [(b0, take)]
+        # each cut is walked by exactly one scan, from its (sequence, head)'s first group on
+        walked = [j + u for j, *_, m in cuts for u in range(m)]
+        assert sorted(walked) == sorted(c[0] for c in cuts)
+        for j, n, h, b0, k, m in cuts:
+            for u in range(m):
+                assert entry[j + u][:2] == (n, h)
