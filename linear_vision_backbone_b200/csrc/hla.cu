@@ -198,6 +198,8 @@ int check_args(const gtr_hla_args* a, bool step, hla::Params* p, bool* empty) {
   if (a->nseq == 0 || a->H == 0 || (a->T == 0 && !a->state_out)) return GTR_OK;
   if (a->Hk == 0 || a->H % a->Hk != 0) return GTR_ERR_INVALID_ARG;
   if (a->H > 65535) return GTR_ERR_UNSUPPORTED;
+  // blocks of at least 16 tokens of all sequences and heads are counted in 31 bits
+  if (!step && ((long long)a->T / hla::kSimtBatch + a->nseq) * a->H >= (1ll << 31)) return GTR_ERR_UNSUPPORTED;
   if (step ? (a->T != a->nseq || a->cu_seqlens || a->seen) : (!a->cu_seqlens && a->T % a->nseq != 0))
     return GTR_ERR_INVALID_ARG;
   if (a->T > 0 && (!a->q || !a->k || !a->v || !a->g || !a->out)) return GTR_ERR_INVALID_ARG;

@@ -49,73 +49,78 @@ template <int C> __device__ __forceinline__ int seq_rows(const Params& p, int n,
   }
   return b - a;
 }
-__device__ __forceinline__ int n_blocks(int len, int C) { return max(1, (int)(((long long)len + C - 1) / C)); }
+__device__ __forceinline__ int n_blocks(int len, int C) { return len <= C ? 1 : (len - 1) / C + 1; }
 
-// A place in the line of blocks: block `off` of the H nb_n of sequence n.
+// A place in the line of blocks: block b of head h of sequence n.
 struct Place {
-  int n;
-  long long off;
+  int n, h, b;
+  // the place `off` blocks into sequence n of nb blocks a head
+  __device__ __forceinline__ void set(int seq, int off, int nb) {
+    n = seq;
+    h = off / nb;
+    b = off - h * nb;
+  }
 };
 
 // Group j's range: the line's B blocks, the groups J that have any (at most
 // one per block, so that none between two others is empty), the places x0 and
 // x1 it lies between and the sequences they fall into (nseq for x = B).
 struct Range {
-  long long B, x0, x1;
-  int J;
+  int B, x0, x1, J;                // B < 2^31: the host refuses more
   Place a, b;
-  __device__ __forceinline__ void set(long long blocks, int groups, int j) {
+  __device__ __forceinline__ int start(int j) const { return (int)((long long)B * min(j, J) / J); }
+  __device__ __forceinline__ void set(int blocks, int groups, int j) {
     B = blocks;
-    J = (int)min((long long)groups, blocks);
-    x0 = B * min(j, J) / J;
-    x1 = B * min(j + 1, J) / J;
+    J = min(groups, blocks);
+    x0 = start(j);
+    x1 = start(j + 1);
   }
 };
 
-// By the whole block of threads.  `scratch`: 40 long longs of shared memory,
-// free again after the caller's next barrier.
-template <int C> __device__ __forceinline__ void locate(const Params& p, int j, long long* scratch, Range& g) {
+// By the whole block of threads.  `scratch`: 40 ints of shared memory, free
+// again after the caller's next barrier.
+template <int C> __device__ __forceinline__ void locate(const Params& p, int j, int* scratch, Range& g) {
   if (!p.cu) {
-    const long long per = (long long)n_blocks(p.T / p.nseq, C) * p.H;
+    const int nb = n_blocks(p.T / p.nseq, C), per = nb * p.H;
     g.set(per * p.nseq, p.J, j);
-    g.a.n = (int)(g.x0 / per); g.a.off = g.x0 - g.a.n * per;
-    g.b.n = (int)(g.x1 / per); g.b.off = g.x1 - g.b.n * per;
+    const int n0 = g.x0 / per, n1 = g.x1 / per;
+    g.a.set(n0, g.x0 - n0 * per, nb);
+    g.b.set(n1, g.x1 - n1 * per, nb);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int per = (p.nseq + blockDim.x - 1) / (int)blockDim.x;   // sequences per thread, consecutive ones
   const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
-  long long mine = 0;
-  int r;
+  int mine = 0, r;
   for (int n = n0; n < n1; ++n) mine += n_blocks(seq_rows<C>(p, n, r), C);
-  long long inc = mine;
+  int inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+    const int o = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += o;
   }
   if (lane == 31) scratch[warp] = inc;
   if (tid == 0) {
-    scratch[32] = p.nseq; scratch[33] = 0;
-    scratch[34] = p.nseq; scratch[35] = 0;
+    scratch[32] = p.nseq; scratch[33] = 0; scratch[34] = 1;
+    scratch[35] = p.nseq; scratch[36] = 0; scratch[37] = 1;
   }
   __syncthreads();
-  long long before = inc - mine, total = 0;
+  int before = inc - mine, total = 0;
   for (int w = 0; w < nw; ++w) {
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
   g.set(total * p.H, p.J, j);
   for (int n = n0; n < n1; ++n) {
-    const long long nb = n_blocks(seq_rows<C>(p, n, r), C);
-    const long long s = before * p.H, e = (before + nb) * p.H;
-    if (s <= g.x0 && g.x0 < e) { scratch[32] = n; scratch[33] = g.x0 - s; }
-    if (s <= g.x1 && g.x1 < e) { scratch[34] = n; scratch[35] = g.x1 - s; }
+    const int nb = n_blocks(seq_rows<C>(p, n, r), C);
+    const int s = before * p.H, e = (before + nb) * p.H;
+    if (s <= g.x0 && g.x0 < e) { scratch[32] = n; scratch[33] = g.x0 - s; scratch[34] = nb; }
+    if (s <= g.x1 && g.x1 < e) { scratch[35] = n; scratch[36] = g.x1 - s; scratch[37] = nb; }
     before += nb;
   }
   __syncthreads();
-  g.a.n = (int)scratch[32]; g.a.off = scratch[33];
-  g.b.n = (int)scratch[34]; g.b.off = scratch[35];
+  g.a.set(scratch[32], scratch[33], scratch[34]);
+  g.b.set(scratch[35], scratch[36], scratch[37]);
 }
 
 // A group's part of one (sequence, head).
@@ -132,19 +137,18 @@ struct Part {
 // walk it by itself and sees the same parts.
 struct Walk {
   Place at;
-  long long left;
+  int left;
 };
 template <int C> __device__ __forceinline__ bool next_part(const Params& p, Walk& w, Part& g) {
   while (w.left > 0 && w.at.n < p.nseq) {
     int a;
     const int len = seq_rows<C>(p, w.at.n, a);
     const int nb = n_blocks(len, C);
-    const int h = (int)(w.at.off / nb), b0 = (int)(w.at.off - (long long)h * nb);
-    int take = (int)min((long long)(nb - b0), w.left);
-    const int n = w.at.n;
+    const int n = w.at.n, h = w.at.h, b0 = w.at.b;
+    int take = min(nb - b0, w.left);
     w.left -= take;
-    w.at.off += take;
-    if (w.at.off >= (long long)nb * p.H) { w.at.n++; w.at.off = 0; }
+    w.at.b = 0;                                // what is left of the range starts the next head
+    if (++w.at.h == p.H) { w.at.h = 0; w.at.n++; }
     if (!p.cut) {
       if (b0 > 0) continue;                    // another group has it whole
       take = nb;
@@ -184,10 +188,10 @@ template <int C> __device__ __forceinline__ bool cut_part(const Params& p, const
   const Place& b = rg.b;
   if (rg.x0 >= rg.x1 || b.n >= p.nseq) return false;
   int a;
-  const int len = seq_rows<C>(p, b.n, a), nb = n_blocks(len, C);
-  const int h = (int)(b.off / nb), e = (int)(b.off - (long long)h * nb);   // blocks before the cut
+  seq_rows<C>(p, b.n, a);
+  const int h = b.h, e = b.b;                  // e blocks before the cut
   if (e == 0) return false;
-  const int b0 = (long long)e <= rg.x1 - rg.x0 ? 0 : (int)(e - (rg.x1 - rg.x0));
+  const int b0 = max(0, e - (rg.x1 - rg.x0));
   g.n = b.n;
   g.h = h;
   g.first = b0 == 0;
@@ -221,7 +225,7 @@ constexpr int kScanThreads = 128;
 constexpr int kScanAhead = 12;     // parts whose loads are in flight together
 
 template <int C> __global__ void __launch_bounds__(kScanThreads) hla_scan(const Params p) {
-  __shared__ long long scratch[40];
+  __shared__ int scratch[40];
   pdl_wait();
   pdl_trigger();
   const int j = blockIdx.x;
@@ -231,9 +235,9 @@ template <int C> __global__ void __launch_bounds__(kScanThreads) hla_scan(const 
   if (!cut_part<C>(p, rg, g) || !g.first) return;
   // the summaries of this (sequence, head): of the groups that end before it does
   int r;
-  const long long end = rg.x1 - g.nb + n_blocks(seq_rows<C>(p, g.n, r), C);
+  const int end = rg.x1 - g.nb + n_blocks(seq_rows<C>(p, g.n, r), C);
   int m = 1;
-  while (j + m < rg.J && rg.B * (j + m + 1) / rg.J < end) ++m;
+  while (j + m < rg.J && rg.start(j + m + 1) < end) ++m;
   const int per_state = p.dk * p.dv;
   const int e = (blockIdx.y * kScanThreads + threadIdx.x) * 4;
   if (e >= per_state) return;

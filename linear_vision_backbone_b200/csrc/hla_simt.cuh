@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
   float* qs = ks + kSimtBatch * dk;          // [batch][dk], outputs only
   float* vs = qs + (kSum ? 0 : kSimtBatch * dk);   // [batch][dv]
   float* part = vs + kSimtBatch * dv;        // [batch][threads]: partial o, outputs only
-  __shared__ long long scratch[40];
+  __shared__ int scratch[40];
   pdl_wait();
   pdl_trigger();
   Range rg;

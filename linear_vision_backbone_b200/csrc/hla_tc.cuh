@@ -28,18 +28,21 @@
 //
 // One block of threads per SM and 64 value columns of a head (dv = 128: two
 // blocks share a head, as a cluster when the norm needs the sum over both),
-// walking the blocks of 128 tokens of its segments.  20 warps, each group one
-// step of the pipeline, joined by mbarriers:
+// walking its parts' blocks of 128 tokens.  20 warps, each group one step of the
+// pipeline, joined by mbarriers:
 //   0-3   scores -> decayed, masked P (a thread has a row)
 //   4-7   the decay sums; wv terms; zeros behind the last token
-//   8-11  the state: fp32 in registers (a thread has a row of 64 columns, or a
+//   8-11  outputs: qs and pv joined, norm, gate, stores
+//   12-15 the state: fp32 in registers (a thread has a row of 64 columns, or a
 //         half row), S <- a S + kv, and its terms for the next block's qs
-//   12-15 outputs: qs and pv joined, norm, gate, stores
 //   16    loads of k and v (TMA, 128-byte swizzled tiles of 128 rows x 64 columns)
 //   17    issues the products
 //   18,19 loads of q and of z, each waiting for its own buffers only
-// The products of a block are issued scores, qs, kv, pv: while the P warps turn
-// block c's scores around, the tensor cores do its qs and kv.
+// The products of a block are issued scores, kv, qs, pv: while the P warps turn
+// block c's scores around and the output warps still read block c - 1's qs and
+// pv, the tensor cores do its kv.
+// The loops are kept rolled where registers allow: unrolled, the instruction
+// streams of the groups outgrew the instruction caches (half of all stalls).
 #pragma once
 #include "hla_common.cuh"
 #include "tc_ptx.cuh"
@@ -82,7 +85,7 @@ template <typename T, int DK, bool kSum> struct Layout {
   static constexpr int kU = kG + 2 * kC * 4;          // [2][128] e^{G_b - G_j}
   static constexpr int kX = kU + 2 * kC * 4;          // [128] the other half's sums of squares
   static constexpr int kMisc = kX + kC * 4;
-  // misc: warp sums [2][4], maxima [2][4], exponents of wv [2] and S [2], tensor memory address, barriers
+  // misc: warp sums [2][4], maxima [4] + [4], exponents of wv [2] and S [2], tensor memory address; barriers
   static constexpr int kBars = kMisc + 96;
   static constexpr int kPExp = kBars + kNumBars * 8;  // fp16: exponents of P [2][128], one byte each
   static constexpr int kSmem = kPExp + (kBf16 ? 0 : 2 * kC);
@@ -135,6 +138,11 @@ __device__ __forceinline__ void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tm_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 // 16 lanes x 32 bit in two halves of 16 columns (the M = 64 accumulator: row r in lane 32 (r / 16) + r % 16)
 __device__ __forceinline__ void tm_ld16x2(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -146,8 +154,13 @@ __device__ __forceinline__ void tm_ld16x2(uint32_t taddr, uint32_t (&r)[16]) {
 }
 // Waits for this thread's loads; the registers are operands, so that no use of them is scheduled before it.
 template <int N> __device__ __forceinline__ void tm_wait(uint32_t (&r)[N]) {
-  static_assert(N == 16 || N == 32, "");
-  if constexpr (N == 16)
+  static_assert(N == 8 || N == 16 || N == 32, "");
+  if constexpr (N == 8)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+  else if constexpr (N == 16)
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
@@ -186,18 +199,26 @@ __device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint64_t both(float a) { return tc::f2pack(a, a); }
 
-template <int N> __device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+// The registers of a thread of a warp group, out of the 96 it was launched with.
+template <int N> __device__ __forceinline__ void set_registers() {
+  static_assert(N % 8 == 0 && N >= 24 && N <= 256, "");
+  if constexpr (N > 96) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N < 96) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-template <int N> __device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
+// Shares of the five warp groups: without spills as far as they go (the state
+// is 64 registers of a thread for dk = 128, 32 for dk = 64).
+template <int DK> struct Regs {
+  static constexpr int kP = DK == 128 ? 72 : 96, kBuild = kP, kOut = 96;
+  static constexpr int kState = DK == 128 ? 160 : 104, kMisc = DK == 128 ? 80 : 88;
+  static_assert(kP + kBuild + kOut + kState + kMisc <= 5 * 96, "no more than the block was launched with");
+};
 
 __device__ __forceinline__ void tm_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+
 template <typename T> struct T2;
 template <> struct T2<__half> {
   using t = __half2;
@@ -308,8 +329,8 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   int8_t* pexp = reinterpret_cast<int8_t*>(sm + L::kPExp);          // [2][128], fp16 only
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // roles: the summary has no score and output warps
-  const int role = kSum ? (warp < 4 ? 1 : warp < 8 ? 2 : warp - 4) : (warp < 16 ? warp >> 2 : warp - 12);
-  enum { kP = 0, kBuild = 1, kState = 2, kOut = 3, kLoad = 4, kMma = 5, kLoadQ = 6, kLoadZ = 7 };
+  enum { kP = 0, kBuild = 1, kOut = 2, kState = 3, kLoad = 4, kMma = 5, kLoadQ = 6, kLoadZ = 7 };
+  const int role = kSum ? (warp < 4 ? kBuild : warp < 8 ? kState : warp - 4) : (warp < 16 ? warp >> 2 : warp - 12);
   if ((saddr(sm) & 1023u) != 0u) {
     if (tid == 0) gtr_flag(kStatusBadShape);
     return;
@@ -322,7 +343,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       tc::mbar_init(bar + kVF + i, 1); tc::mbar_init(bar + kVE + i, 1);
     }
     for (int b : {kScF, kPvF, kSE, kWE, kKvF}) tc::mbar_init(bar + b, 1);
-    for (int b : {kPF, kOE, kSF, kWF, kKvE}) tc::mbar_init(bar + b, 4);
+    for (int b : {kPF, kOE, kWF, kSF, kKvE}) tc::mbar_init(bar + b, 4);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar + kGF + i, 4);
       tc::mbar_init(bar + kGE + i, kSum ? 4 : 12);
@@ -344,7 +365,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   const uint32_t tm = *tmem_slot;
   const int half = (int)blockIdx.x % halves, group_j = (int)blockIdx.x / halves;
   Range rg;
-  locate<kC>(p, group_j, reinterpret_cast<long long*>(Gs), rg);
+  locate<kC>(p, group_j, reinterpret_cast<int*>(Gs), rg);
   __syncthreads();                                             // the scratch becomes the decay sums
   const int w4 = warp & 3, row = w4 * 32 + lane;               // a token row, or a lane of an accumulator
   const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
@@ -373,7 +394,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   auto has_start = [&](const Part& g) { return !kSum && (!g.first || g.start); };
 
   if (role == kLoad) {
-    if constexpr (!kSum) fewer_registers<48>();
+    if constexpr (!kSum) set_registers<Regs<DK>::kMisc>();
     for_parts([&](const Part& g) {
       const int hk = g.h / share;
       if (lane == 0) {
@@ -396,7 +417,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       it += g.nb;
     });
   } else if (role == kMma) {
-    if constexpr (!kSum) fewer_registers<48>();
+    if constexpr (!kSum) set_registers<Regs<DK>::kMisc>();
     const bool lead = elect_one();
     for_parts([&](const Part& g) {
       constexpr uint32_t kIdSc = idesc(kBf16, 0, 0, 128, 128), kIdQS = idesc(kBf16, 0, 1, 128, 128);
@@ -428,25 +449,6 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             tc::mma_commit(bar + kScF);
           }
           __syncwarp();
-          ok = wait(kOE, par ^ 1);                               // qs and pv of the block before are read
-          if (!ok) break;
-          if (c > 0 || has_start(g)) {
-            ok = wait(kSF, is & 1);
-            if (!ok) break;
-            tc::tc_after_sync();
-            const uint64_t bs = tc::sdesc(saddr(sm + L::kS), L::kSTile, 1024);
-            if (lead) {
-#pragma unroll
-              for (int s = 0; s < DK / 16; ++s) {
-                const uint64_t o = (uint64_t)((s >> 2) * (kTile >> 4) + (s & 3) * tc::kStepK);
-                tc::mma_f16(tm + kTmQS, aq + o, bs + s * tc::kStepMN, kIdQS, s > 0);
-              }
-              tc::mma_commit(bar + kSE);
-            }
-            ++is;
-          }
-          if (lead) tc::mma_commit(bar + kQE + sq);
-          __syncwarp();
         }
         ok = ok && wait(kWF, par) && wait(kKvE, par ^ 1);
         if (!ok) break;
@@ -470,6 +472,27 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         }
         __syncwarp();
         if constexpr (!kSum) {
+          const int sq = i % L::kNQ;
+          const uint64_t aq = tc::sdesc(saddr(sm + L::kQ + sq * L::kQTile), 16, 1024);
+          ok = wait(kOE, par ^ 1);                               // qs and pv of the block before are read
+          if (!ok) break;
+          if (c > 0 || has_start(g)) {
+            ok = wait(kSF, is & 1);
+            if (!ok) break;
+            tc::tc_after_sync();
+            const uint64_t bs = tc::sdesc(saddr(sm + L::kS), L::kSTile, 1024);
+            if (lead) {
+#pragma unroll
+              for (int s = 0; s < DK / 16; ++s) {
+                const uint64_t o = (uint64_t)((s >> 2) * (kTile >> 4) + (s & 3) * tc::kStepK);
+                tc::mma_f16(tm + kTmQS, aq + o, bs + s * tc::kStepMN, kIdQS, s > 0);
+              }
+              tc::mma_commit(bar + kSE);
+            }
+            ++is;
+          }
+          if (lead) tc::mma_commit(bar + kQE + sq);
+          __syncwarp();
           ok = wait(kPF, par);
           if (!ok) break;
           tc::tc_after_sync();
@@ -495,6 +518,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       ok = wait(kVE + i % L::kNV, i / L::kNV & 1);
     }
   } else if (role == kBuild) {
+    if constexpr (!kSum) set_registers<Regs<DK>::kBuild>();
     for_parts([&](const Part& g) {
       const bool want_end = wants_end(g);
       float l = row < g.len ? load_decay(p, g.t0 + row, g.h) : 0.f;
@@ -537,22 +561,20 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         const bool build = c + 1 < g.nb || want_end;
         const bool live = row < nv;
         const float w = tc::ex2(R);
-        uint4 v[8];
-        if (build) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            v[u] = *reinterpret_cast<const uint4*>(V + ((u ^ (row & 7)) << 4));
-            if (!live) v[u] = make_uint4(0, 0, 0, 0);            // others' data, maybe NaN
-          }
-        }
+        // this row's unit u of v; nothing of others' data behind the last token (maybe NaN)
+        auto unit = [&](int u) {
+          const uint4 x = *reinterpret_cast<const uint4*>(V + ((u ^ (row & 7)) << 4));
+          return live ? x : make_uint4(0, 0, 0, 0);
+        };
         float up = 1.f;
         int exp_w = 0;
         if (!kBf16 && build) {
           // a power of two that brings the block's largest |w v| under 2^15
           uint32_t mx = 0;                                       // |fp16| orders as its bits, NaN on top
-#pragma unroll
+#pragma unroll 2
           for (int u = 0; u < 8; ++u) {
-            const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            const uint4 v = unit(u);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx = __vmaxu2(mx, x[e] & 0x7fff7fffu);
           }
@@ -570,9 +592,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           if (!kBf16 && row == 0) ew[i & 1] = exp_w;
           uint8_t* W = sm + L::kW + row * 128;
           const uint64_t f = both(w * up);
-#pragma unroll
+#pragma unroll 2
           for (int u = 0; u < 8; ++u) {
-            const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            const uint4 v = unit(u);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
             uint32_t t[L::kTerms][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -609,7 +632,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       it += g.nb;
     });
   } else if (role == kState) {
-    if constexpr (!kSum) more_registers<112>();
+    if constexpr (!kSum) set_registers<Regs<DK>::kState>();
     using SC = StateCols<DK>;
     constexpr int kRuns = SC::kN / 16;
     const int r = SC::row(w4, lane);
@@ -723,12 +746,11 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     });
   } else if constexpr (!kSum) {
     if (role == kP) {
+      set_registers<Regs<DK>::kP>();
       {
         // P lo right of the diagonal is zero for good
-        uint32_t zero[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) zero[e] = 0u;
-        for (int b = w4 + 1; b < 4; ++b) tm_st16(tm + lane_base + kTmPlo + 16 * b, zero);
+        uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int b = 2 * w4 + 2; b < 8; ++b) tm_st8(tm + lane_base + kTmPlo + 8 * b, zero);
       }
       for_parts([&](const Part& g) {
         for (int c = 0; c < g.nb && ok; ++c) {
@@ -739,17 +761,17 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           const float* G = Gs + (i & 1) * kC;
           const float* U = Us + (i & 1) * kC;
           const float Gi = G[row];
-          const uint32_t sc = tm + lane_base + kTmSc;
+          const uint32_t sc = tm + lane_base + kTmSc, plo = tm + lane_base + kTmPlo;
           float up = 1.f;
           if (!kBf16) {
             // a power of two that brings the row's largest |score| under 2^15
             uint32_t mx = 0;
-#pragma unroll 2
-            for (int b = 0; b <= 2 * w4 + 1; ++b) {
+#pragma unroll 1
+            for (int b = 0; b < 2 * w4 + 2; ++b) {
               uint32_t x[16];
               tm_ld16(sc + 16 * b, x);
               tm_wait(x);
-              const int diag = lane + 32 * w4 - 16 * b;          // the row's last column of this run
+              const int diag = 32 * w4 + lane - 16 * b;          // the row's last column of this run
 #pragma unroll
               for (int e = 0; e < 16; ++e) mx = max(mx, e <= diag ? x[e] & 0x7fffffffu : 0u);
             }
@@ -757,57 +779,59 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             up = tc::pow2i(e);
             pexp[(i & 1) * kC + row] = (int8_t)e;
           }
-          // 16 columns at a time, the next ones loading; P hi goes over scores
-          // already read (columns [8 b, 8 b + 8) of 16-column run b / 2)
-          uint32_t s[2][16];
-          tm_ld16(sc, s[0]);
-#pragma unroll
-          for (int b = 0; b < 8; ++b) {
-            uint32_t hi[8], lo[8];
-            if (b >> 1 > w4) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) hi[e] = 0u;
-              tm_st8(sc + 8 * b, hi);
-              continue;
-            }
-            uint32_t(&x)[16] = s[b & 1];
+          // runs of 16 columns; P hi goes over scores already read (columns
+          // [8 b, 8 b + 8) of run b / 2)
+#pragma unroll 2
+          for (int b = 0; b < 2 * w4; ++b) {
+            uint32_t x[16], hi[8], lo[8];
+            tm_ld16(sc + 16 * b, x);
+            const uint64_t f = both(tc::ex2(Gi - G[16 * (b | 1) + 15]) * up);
+            const ulonglong2* u2 = reinterpret_cast<const ulonglong2*>(U + 16 * b);
             tm_wait(x);
-            if (b < 7 && (b + 1) >> 1 <= w4) tm_ld16(sc + 16 * (b + 1), s[(b + 1) & 1]);
-            if (b >> 1 == w4) {
-              const float4* g4 = reinterpret_cast<const float4*>(G + 16 * b);
-              const int diag = lane - 16 * (b & 1);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 gj = g4[e];
-                const float d[4] = {gj.x, gj.y, gj.z, gj.w};
+            for (int e = 0; e < 4; ++e) {
+              const ulonglong2 uj = u2[e];
+              uint64_t y = tc::fmul2(pack2(x[4 * e], x[4 * e + 1]), tc::fmul2(uj.x, f));
+              hi[2 * e] = term<T>(y);
+              lo[2 * e] = narrow<T>(y);
+              y = tc::fmul2(pack2(x[4 * e + 2], x[4 * e + 3]), tc::fmul2(uj.y, f));
+              hi[2 * e + 1] = term<T>(y);
+              lo[2 * e + 1] = narrow<T>(y);
+            }
+            tm_st8(sc + 8 * b, hi);
+            tm_st8(plo + 8 * b, lo);
+          }
+          // the square on the diagonal
+#pragma unroll 1
+          for (int b = 2 * w4; b < 2 * w4 + 2; ++b) {
+            uint32_t x[16], hi[8], lo[8];
+            tm_ld16(sc + 16 * b, x);
+            const float4* g4 = reinterpret_cast<const float4*>(G + 16 * b);
+            const int diag = 32 * w4 + lane - 16 * b;
+            tm_wait(x);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const float m = __uint_as_float(x[4 * e + y]) * (tc::ex2(Gi - d[y]) * up);
-                  x[4 * e + y] = 4 * e + y <= diag ? __float_as_uint(m) : 0u;
-                }
+            for (int e = 0; e < 4; ++e) {
+              const float4 gj = g4[e];
+              const float d[4] = {gj.x, gj.y, gj.z, gj.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float m = __uint_as_float(x[4 * e + y]) * (tc::ex2(Gi - d[y]) * up);
+                x[4 * e + y] = 4 * e + y <= diag ? __float_as_uint(m) : 0u;
               }
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                uint64_t y = pack2(x[2 * e], x[2 * e + 1]);
-                hi[e] = term<T>(y);
-                lo[e] = narrow<T>(y);
-              }
-            } else {
-              const uint64_t f = both(tc::ex2(Gi - G[16 * (b | 1) + 15]) * up);
-              const ulonglong2* u2 = reinterpret_cast<const ulonglong2*>(U + 16 * b);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const ulonglong2 uj = u2[e];
-                uint64_t y = tc::fmul2(pack2(x[4 * e], x[4 * e + 1]), tc::fmul2(uj.x, f));
-                hi[2 * e] = term<T>(y);
-                lo[2 * e] = narrow<T>(y);
-                y = tc::fmul2(pack2(x[4 * e + 2], x[4 * e + 3]), tc::fmul2(uj.y, f));
-                hi[2 * e + 1] = term<T>(y);
-                lo[2 * e + 1] = narrow<T>(y);
+              for (int y = 0; y < 2; ++y) {
+                uint64_t z = pack2(x[4 * e + 2 * y], x[4 * e + 2 * y + 1]);
+                hi[2 * e + y] = term<T>(z);
+                lo[2 * e + y] = narrow<T>(z);
               }
             }
             tm_st8(sc + 8 * b, hi);
-            tm_st8(tm + lane_base + kTmPlo + 8 * b, lo);
+            tm_st8(plo + 8 * b, lo);
+          }
+          {
+            uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+            for (int b = 2 * w4 + 2; b < 8; ++b) tm_st8(sc + 8 * b, zero);
           }
           tc::tmem_st_wait();
           tc::tc_before_sync();
@@ -817,7 +841,6 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         it += g.nb;
       });
     } else if (role == kOut) {
-      more_registers<128>();
       const uint32_t rank = kPair ? blockIdx.x & 1u : 0u;
       for_parts([&](const Part& g) {
         for (int c = 0; c < g.nb && ok; ++c) {
@@ -837,35 +860,37 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             f2 *= tc::pow2i(-(int)pexp[(i & 1) * kC + row]);
           }
           const uint64_t f11 = both(f1), f22 = both(f2);
-          uint64_t o[32];
-          uint64_t ss2 = both(0.f);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t a[16], b[16], d[16];
-            tm_ld16(tm + lane_base + kTmPV + 16 * x, d);
+          if (state) ++is;
+          // 8 columns of o: qs (hi + lo) and pv joined
+          auto columns = [&](int u, uint64_t (&y)[4]) {
+            uint32_t a[8], b[8], d[8];
+            tm_ld8(tm + lane_base + kTmPV + 8 * u, d);
             if (state) {
-              tm_ld16(tm + lane_base + kTmQS + 16 * x, a);
-              tm_ld16(tm + lane_base + kTmQS + 64 + 16 * x, b);
+              tm_ld8(tm + lane_base + kTmQS + 8 * u, a);
+              tm_ld8(tm + lane_base + kTmQS + 64 + 8 * u, b);
               tm_wait(a);
               tm_wait(b);
             }
             tm_wait(d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              uint64_t y = tc::fmul2(f22, pack2(d[2 * e], d[2 * e + 1]));
+            for (int e = 0; e < 4; ++e) {
+              y[e] = tc::fmul2(f22, pack2(d[2 * e], d[2 * e + 1]));
               if (state)
-                y = tc::ffma2(f11, add2(pack2(a[2 * e], a[2 * e + 1]), pack2(b[2 * e], b[2 * e + 1])), y);
-              o[8 * x + e] = y;
-              ss2 = tc::ffma2(y, y, ss2);
+                y[e] = tc::ffma2(f11, add2(pack2(a[2 * e], a[2 * e + 1]), pack2(b[2 * e], b[2 * e + 1])), y[e]);
             }
-          }
-          if (state) ++is;
-          tc::tc_before_sync();
-          warp_arrive(kOE);
+          };
           const int sz = i % L::kNZ;
           uint8_t* Z = sm + L::kZ + sz * kTile;
           uint64_t inv2 = both(1.f);
           if (gated) {
+            uint64_t ss2 = both(0.f);
+#pragma unroll 2
+            for (int u = 0; u < 8; ++u) {
+              uint64_t y[4];
+              columns(u, y);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) ss2 = tc::ffma2(y[e], y[e], ss2);
+            }
             const float2 sf = tc::f2unpack(ss2);
             float ss = sf.x + sf.y;
             if constexpr (kPair) {
@@ -887,19 +912,19 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             tc::named_barrier(3, 128);
           }
           const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(p.w + half * 64);
-#pragma unroll
+#pragma unroll 1
           for (int u = 0; u < 8; ++u) {
             uint4* unit16 = reinterpret_cast<uint4*>(Z + row * 128 + ((u ^ (row & 7)) << 4));
-            uint64_t y[4] = {o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]};
+            uint64_t y[4];
             if (gated) {
-              const uint4 zu = *unit16;
-              const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
               uint64_t wt[4] = {inv2, inv2, inv2, inv2};
               if (p.w) {
                 const ulonglong2 wa = __ldg(wp + 2 * u), wb = __ldg(wp + 2 * u + 1);
                 wt[0] = tc::fmul2(wa.x, inv2); wt[1] = tc::fmul2(wa.y, inv2);
                 wt[2] = tc::fmul2(wb.x, inv2); wt[3] = tc::fmul2(wb.y, inv2);
               }
+              const uint4 zu = *unit16;
+              const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 // z sigmoid(z) = z / (1 + 2^(-z log2 e))
@@ -907,11 +932,18 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
                 const float2 m = tc::f2unpack(tc::fmul2(z, both(-kLog2e)));
                 const float2 q = tc::f2unpack(add2(tc::f2pack(tc::ex2(m.x), tc::ex2(m.y)), both(1.f)));
                 const float2 zf = tc::f2unpack(z);
-                y[e] = tc::fmul2(tc::fmul2(y[e], wt[e]), tc::f2pack(__fdividef(zf.x, q.x), __fdividef(zf.y, q.y)));
+                wt[e] = tc::fmul2(wt[e], tc::f2pack(__fdividef(zf.x, q.x), __fdividef(zf.y, q.y)));
               }
+              columns(u, y);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = tc::fmul2(y[e], wt[e]);
+            } else {
+              columns(u, y);
             }
             *unit16 = make_uint4(narrow<T>(y[0]), narrow<T>(y[1]), narrow<T>(y[2]), narrow<T>(y[3]));
           }
+          tc::tc_before_sync();
+          warp_arrive(kOE);
           tc::named_barrier(3, 128);
           {
             const int u = row & 7;
@@ -932,7 +964,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         it += g.nb;
       });
     } else if (role == kLoadQ) {
-      fewer_registers<48>();
+      set_registers<Regs<DK>::kMisc>();
       for_parts([&](const Part& g) {
         const int hk = g.h / share;
         if (lane == 0) {
@@ -952,7 +984,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         it += g.nb;
       });
     } else if (role == kLoadZ) {
-      fewer_registers<48>();
+      set_registers<Regs<DK>::kMisc>();
       if (gated)
         for_parts([&](const Part& g) {
           if (lane == 0) {
