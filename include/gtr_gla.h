@@ -464,11 +464,19 @@ GTR_API gtr_status_t gtr_hla_step(const gtr_hla_args *args, void *stream);
  *   than x_out = x (GTR_ERR_INVALID_ARG).  N = 0 is an empty problem.
  */
 typedef enum { GTR_GATE_MUL = 0, GTR_GATE_SIGMOID = 1, GTR_GATE_SILU = 2 } gtr_gate_act_t;
-GTR_API gtr_status_t gtr_residual_norm(const void *x, void *x_out, int x_dtype, const void *y, int post_norm,
-                                       const float *post_w, const void *gate, int gate_act,
-                                       long long gate_rows, const float *res_scale, float alpha,
-                                       const float *pre_w, void *out, long long N, int D, float eps,
-                                       int dtype, void *stream);
+typedef struct gtr_residual_norm_args {
+  const void *x;
+  void *x_out;
+  const void *y;
+  const float *post_w;
+  const void *gate;
+  const float *res_scale, *pre_w;
+  void *out;
+  long long N, gate_rows;
+  int D, x_dtype, dtype, post_norm, gate_act;
+  float alpha, eps;
+} gtr_residual_norm_args;
+GTR_API gtr_status_t gtr_residual_norm(const gtr_residual_norm_args *args, void *stream);
 
 /*
  * Chunk-boundary states, for testing the first two stages on their own: the

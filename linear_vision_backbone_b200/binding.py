@@ -97,8 +97,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "gtr_hla_workspace_bytes": ([I, I, I, I, I, I], Z),
             "gtr_hla_fwd": ([ctypes.c_char_p, P], I),
             "gtr_hla_step": ([ctypes.c_char_p, P], I),
-            "gtr_residual_norm": ([P, P, I, P, I, P, P, I, ctypes.c_longlong, P, F, P, P, ctypes.c_longlong, I, F,
-                                   I, P], I),
+            "gtr_residual_norm": ([ctypes.c_char_p, P], I),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -437,126 +436,138 @@ def gla_fwd_noalloc(q, k, v, g, z, w=None, *, grid_h: int, grid_w: int, directio
 
 
 # gtr_hla_args in the header's order: 13 pointers, the workspace size, five row
-# pitches, nine ints, the scale
+# pitches, nine ints, the scale; gtr_residual_norm_args: eight pointers, two
+# long longs, five ints, alpha and eps
 _HLA_ARGS = struct.Struct("@13PN5q9if")
+_NORM_ARGS = struct.Struct("@8P2q5i2f4x")
+_F32, _I32 = torch.float32, torch.int32
+_Tensor = torch.Tensor
 
 
-def _on(device: int, stream):
-    """The device's context where it is not the current one, and the raw stream to launch on."""
-    guard = None
-    if torch.cuda.current_device() != device:
-        guard = torch.cuda.device(device)
-    if stream is None:
-        return guard, torch._C._cuda_getCurrentRawStream(device)
-    if stream.device_index != device:
-        raise ValueError(f"the stream is on device {stream.device_index}, the tensors are on {device}")
-    return guard, stream.cuda_stream
+# The checks below are written for the host time of a small call: a kernel of a
+# few microseconds would otherwise wait for them.
+def _refuse(t, name, dtype, shape, device):
+    """The error for a tensor that failed a check."""
+    if not isinstance(t, _Tensor):
+        return ValueError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.get_device() != device or t.dtype != dtype:
+        return ValueError(f"{name} must be a {dtype} tensor on cuda:{device}, got {t.dtype} on {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        return ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return ValueError(f"{name} must be contiguous")
 
 
-@contextlib.contextmanager
-def _allocating(guard, stream):
-    """Allocations belong to the stream that uses them."""
-    with contextlib.ExitStack() as stack:
-        if guard is not None:
-            stack.enter_context(guard)
-        if stream is not None:
-            stack.enter_context(torch.cuda.stream(stream))
-        yield
+def _dense(t, name, dtype, shape, device):
+    """The address of a contiguous tensor of this type and shape."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != device or t.shape != shape \
+            or not t.is_contiguous():
+        raise _refuse(t, name, dtype, shape, device)
+    return t.data_ptr()
 
 
-@functools.lru_cache(maxsize=4096)
-def _hla_workspace(device: int, nseq: int, T: int, H: int, dk: int, dv: int, dtype: int) -> int:
-    with torch.cuda.device(device):
-        return int(load().gtr_hla_workspace_bytes(nseq, T, H, dk, dv, dtype))
-
-
-def _rows(t, name, lead, heads, d, dtype, device):
-    """Row pitch of a [*lead, heads, d] tensor whose tokens may be apart (0: dense)."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{device}")
-    if t.shape != (*lead, heads, d):
-        raise ValueError(f"{name} must have shape {(*lead, heads, d)}, got {tuple(t.shape)}")
+def _pitch(t, name, dtype, shape, device):
+    """Row pitch of a [..., heads, d] tensor whose tokens may be apart (0: dense)."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != device or t.shape != shape:
+        raise _refuse(t, name, dtype, shape, device)
     if t.is_contiguous():
         return 0
-    st = t.stride()
-    if st[-1] != 1 or (heads > 1 and st[-2] != d):
+    st, lead = t.stride(), shape[:-2]
+    if st[-1] != 1 or (shape[-2] > 1 and st[-2] != shape[-1]):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]:
         raise ValueError(f"{name}: sequences must follow each other at the tokens' pitch")
     return st[-3] if lead[-1] > 1 else (st[0] if len(lead) == 2 and lead[0] > 1 else 0)
 
 
-def _vector(t, name, n, dtype, device):
-    if t is None:
-        return 0
-    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != dtype or t.shape != (n,) \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} on cuda:{device}")
-    return t.data_ptr()
+@contextlib.contextmanager
+def _on(device: int, stream):
+    """The tensors' device as the current one, and allocations on the stream that uses them."""
+    with contextlib.ExitStack() as stack:
+        stack.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device_index != device:
+                raise ValueError(f"the stream is on device {stream.device_index}, the tensors are on {device}")
+            stack.enter_context(torch.cuda.stream(stream))
+        yield
 
 
-def _states(t, name, H, dk, dv, device):
-    if t is None:
-        return 0
-    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != torch.float32 or t.dim() != 4 \
-            or t.shape[1:] != (H, dk, dv) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor [n, {H}, {dk}, {dv}] on cuda:{device}")
-    return t.data_ptr()
+def _elsewhere(device: int, stream) -> bool:
+    """Whether a call needs _on: another device than the current one, or a stream of the caller's."""
+    return stream is not None or torch._C._cuda_getDevice() != device
+
+
+@functools.lru_cache(maxsize=4096)
+def _hla_workspace(device: int, nseq: int, T: int, H: int, dk: int, dv: int, dtype: int) -> int:
+    with torch.cuda.device(device):
+        need = int(load().gtr_hla_workspace_bytes(nseq, T, H, dk, dv, dtype))
+    return need if need < 1 << 62 else 0             # sizes it refuses: the call says so
 
 
 def _hla(fn, q, k, v, g, z, w, cu_seqlens, nseq, scale, state_in, state_out, slots, seen, out, stream):
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+    if not isinstance(q, _Tensor) or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    if q.dtype not in DTYPE_IDS:
-        raise ValueError(f"q must be one of {list(DTYPE_IDS)}, got {q.dtype}")
-    device, dtype, lead = q.get_device(), q.dtype, q.shape[:-2]
-    if len(lead) not in (1, 2) or not isinstance(v, torch.Tensor) or v.dim() != q.dim():
+    device, dtype, qs = q.get_device(), q.dtype, q.shape
+    did = DTYPE_IDS.get(dtype)
+    if did is None:
+        raise ValueError(f"q must be one of {list(DTYPE_IDS)}, got {dtype}")
+    if not isinstance(v, _Tensor) or not 3 <= len(qs) <= 4 or v.dim() != len(qs):
         raise ValueError("q, k, v must be [T, heads, d] or [B, T, heads, d]")
-    Hk, dk = q.shape[-2:]
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return _hla(fn, q, k, v, g, z, w, cu_seqlens, nseq, scale, state_in, state_out, slots, seen, out, None)
+    lead = qs[:-2]
+    Hk, dk = qs[-2:]
     H, dv = v.shape[-2:]
-    T = lead[0] if len(lead) == 1 else lead[0] * lead[1]
-    if len(lead) == 2 and cu_seqlens is not None:
-        raise ValueError("cu_seqlens goes with packed [T, heads, d] tensors")
-    ldq, ldk = _rows(q, "q", lead, Hk, dk, dtype, device), _rows(k, "k", lead, Hk, dk, dtype, device)
-    ldv = _rows(v, "v", lead, H, dv, dtype, device)
-    ldz = 0 if z is None else _rows(z, "z", lead, H, dv, dtype, device)
-    if not isinstance(g, torch.Tensor) or g.get_device() != device or g.dtype != torch.float32 \
-            or not g.is_contiguous() or g.shape not in ((H,), (*lead, H)):
-        raise ValueError(f"g must be a contiguous float32 tensor {(*lead, H)} or ({H},) on cuda:{device}")
-    if w is not None and z is None:
+    T, vs = lead[0], (*lead, H, dv)
+    if len(lead) == 2:
+        T *= lead[1]
+        if cu_seqlens is not None:
+            raise ValueError("cu_seqlens goes with packed [T, heads, d] tensors")
+    ldq, ldk, ldv = _pitch(q, "q", dtype, qs, device), _pitch(k, "k", dtype, qs, device), _pitch(v, "v", dtype, vs, device)
+    ldz = pz = pw = 0
+    if z is not None:
+        ldz, pz = _pitch(z, "z", dtype, vs, device), z.data_ptr()
+        if w is not None:
+            pw = _dense(w, "w", _F32, (dv,), device)
+    elif w is not None:
         raise ValueError("w goes with z")
+    per_head = isinstance(g, _Tensor) and g.dim() == 1
+    pg = _dense(g, "g", _F32, (H,) if per_head else (*lead, H), device)
+    pc = pn = ps = pi = po = nslots = 0
     if nseq is None:
-        nseq = lead[0] if len(lead) == 2 else 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    if nseq < 0:
-        raise ValueError("cu_seqlens must have at least one entry")
-    nslots = -1
-    for name, t in (("state_in", state_in), ("state_out", state_out)):
-        if t is not None:
-            if nslots >= 0 and t.shape[0] != nslots:
-                raise ValueError("state_in and state_out must have the same number of states")
-            nslots = t.shape[0]
-    pi, po = _states(state_in, "state_in", H, dk, dv, device), _states(state_out, "state_out", H, dk, dv, device)
-    if nslots >= 0 and slots is None and nslots < nseq:
+        nseq = lead[0] if len(lead) == 2 else 1
+        if cu_seqlens is not None:
+            nseq = cu_seqlens.numel() - 1
+            if nseq < 0:
+                raise ValueError("cu_seqlens must have at least one entry")
+            pc = _dense(cu_seqlens, "cu_seqlens", _I32, (nseq + 1,), device)
+    if slots is not None:
+        ps = _dense(slots, "slots", _I32, (nseq,), device)
+    if seen is not None:
+        pn = _dense(seen, "seen", _I32, (nseq,), device)
+    if state_in is not None:
+        nslots = state_in.shape[0] if isinstance(state_in, _Tensor) and state_in.dim() else 0
+        pi = po = _dense(state_in, "state_in", _F32, (nslots, H, dk, dv), device)
+    if state_out is None:
+        po = 0
+    elif state_out is not state_in:
+        if state_in is None:
+            nslots = state_out.shape[0] if isinstance(state_out, _Tensor) and state_out.dim() else 0
+        po = _dense(state_out, "state_out", _F32, (nslots, H, dk, dv), device)
+    if slots is None and nslots < nseq and (pi or po or state_in is not None or state_out is not None):
         raise ValueError(f"{nseq} sequences need {nseq} states or slots, got {nslots}")
-    pw, ps = _vector(w, "w", dv, torch.float32, device), _vector(slots, "slots", nseq, torch.int32, device)
-    pn, pc = _vector(seen, "seen", nseq, torch.int32, device), _vector(cu_seqlens, "cu_seqlens", nseq + 1,
-                                                                       torch.int32, device)
-    guard, raw = _on(device, stream)
-    lib = load()
-    did = DTYPE_IDS[dtype]
+    ws = pws = ldo = 0
     need = _hla_workspace(device, nseq, T, H, dk, dv, did) if fn == "gtr_hla_fwd" else 0
-    ws = None
-    with _allocating(guard, stream) if guard is not None or stream is not None else contextlib.nullcontext():
-        if out is None:
-            out = torch.empty(v.shape, dtype=dtype, device=v.device)
-        ldo = _rows(out, "out", lead, H, dv, dtype, device)
-        if need and need < 1 << 62:
-            ws = torch.empty(need, dtype=torch.uint8, device=v.device)
-        args = _HLA_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                              0 if z is None else z.data_ptr(), pw, out.data_ptr(), pi, po, ps, pn, pc,
-                              0 if ws is None else ws.data_ptr(), 0 if ws is None else need, ldq, ldk, ldv, ldz, ldo,
-                              nseq, T, Hk, H, dk, dv, max(nslots, 0), g.dim() == 1, did, scale)
-        rc = getattr(lib, fn)(args, raw)
+    if need:
+        ws = torch.empty(need, dtype=torch.uint8, device=v.device)
+        pws = ws.data_ptr()
+    if out is None:
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
+    else:
+        ldo = _pitch(out, "out", dtype, vs, device)
+    args = _HLA_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), pg, pz, pw, out.data_ptr(), pi, po, ps, pn, pc, pws,
+                          need, ldq, ldk, ldv, ldz, ldo, nseq, T, Hk, H, dk, dv, nslots, per_head, did, scale)
+    rc = getattr(_lib or load(), fn)(args, torch._C._cuda_getCurrentRawStream(device))
     if rc:
         _check(fn, rc)
     return out
@@ -588,7 +599,7 @@ def hla_step(q, k, v, g, state_in, z=None, w=None, *, slots=None, scale: float =
     g fp32 [N, H] or [H]; row n updates state slots[n] (None: n; negative: the row is
     skipped and its output left as it was) of state_in, in place or into state_out, and
     gives o_n as in :func:`hla_fwd`."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+    if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be a CUDA tensor [N, Hk, dk]")
     if state_in is None:
         raise ValueError("state_in is needed")
@@ -609,40 +620,57 @@ def residual_norm(x, y=None, *, post_norm: Optional[bool] = None, post_w=None, g
     n)); gate_act: "mul", "sigmoid" or "silu".  post_w, res_scale, pre_w: [D]
     fp32 or None; post_norm / pre_norm default to whether their weight is given.
     """
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in DTYPE_IDS or x.dim() < 1:
+    if not isinstance(x, _Tensor) or not x.is_cuda or x.dtype not in DTYPE_IDS or x.dim() < 1:
         raise ValueError("x must be a CUDA tensor [..., D]")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    device, D = x.get_device(), x.shape[-1]
+    device, shape, xt = x.get_device(), x.shape, x.dtype
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return residual_norm(x, y, post_norm=post_norm, post_w=post_w, gate=gate, gate_act=gate_act,
+                                 res_scale=res_scale, alpha=alpha, pre_norm=pre_norm, pre_w=pre_w, x_out=x_out,
+                                 out=out, eps=eps)
+    D = shape[-1]
     N = x.numel() // D if D else 0
-    dtype = x.dtype if y is None else y.dtype
-    post_norm = post_w is not None if post_norm is None else post_norm
-    pre_norm = pre_w is not None or out is not None if pre_norm is None else pre_norm
-    if post_w is not None and not post_norm:
-        raise ValueError("post_w goes with post_norm")
-    if (pre_w is not None or out is not None) and not pre_norm:
-        raise ValueError("pre_w and out go with pre_norm")
-    rows = 1
-    for name, t, dt in (("y", y, dtype), ("x_out", x_out, x.dtype), ("gate", gate, dtype), ("out", out, dtype)):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != dt or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dt} tensor on cuda:{device}")
-        if t.shape != x.shape:
-            if name != "gate" or t.dim() != 2 or t.shape[1] != D or t.shape[0] < 1 or N % t.shape[0]:
-                raise ValueError(f"{name} must have shape {tuple(x.shape)}, got {tuple(t.shape)}")
-            rows = max(1, N // t.shape[0])
-    guard, raw = _on(device, stream)
-    with _allocating(guard, stream) if guard is not None or stream is not None else contextlib.nullcontext():
-        if pre_norm and out is None:
-            out = torch.empty(x.shape, dtype=dtype, device=x.device)
-        rc = load().gtr_residual_norm(
-            x.data_ptr(), (x if x_out is None else x_out).data_ptr(), DTYPE_IDS[x.dtype],
-            0 if y is None else y.data_ptr(), post_norm, _vector(post_w, "post_w", D, torch.float32, device),
-            0 if gate is None else gate.data_ptr(), GATE_ACTS[gate_act], rows,
-            _vector(res_scale, "res_scale", D, torch.float32, device), alpha,
-            _vector(pre_w, "pre_w", D, torch.float32, device), 0 if out is None else out.data_ptr(), N, D, eps,
-            DTYPE_IDS[dtype], raw)
+    px = x.data_ptr()
+    pxo, py, ppw, pg, prs, pnw, rows, dtype = px, 0, 0, 0, 0, 0, 1, xt
+    if y is not None:
+        dtype = y.dtype if isinstance(y, _Tensor) else None
+        if dtype not in DTYPE_IDS:
+            raise ValueError(f"y must be a tensor of one of {list(DTYPE_IDS)}")
+        py = _dense(y, "y", dtype, shape, device)
+    if x_out is not None:
+        pxo = _dense(x_out, "x_out", xt, shape, device)
+    if gate is not None:
+        gs = gate.shape if isinstance(gate, _Tensor) else None
+        if gs is not None and gs != shape and len(gs) == 2 and gs[0] > 0 and gs[1] == D and N % gs[0] == 0:
+            rows = max(1, N // gs[0])
+        else:
+            gs = shape
+        pg = _dense(gate, "gate", dtype, gs, device)
+    if post_w is not None:
+        if post_norm is False:
+            raise ValueError("post_w goes with post_norm")
+        post_norm, ppw = True, _dense(post_w, "post_w", _F32, (D,), device)
+    if res_scale is not None:
+        prs = _dense(res_scale, "res_scale", _F32, (D,), device)
+    if pre_w is not None or out is not None:
+        if pre_norm is False:
+            raise ValueError("pre_w and out go with pre_norm")
+        pre_norm = True
+        if pre_w is not None:
+            pnw = _dense(pre_w, "pre_w", _F32, (D,), device)
+    po = 0
+    if pre_norm:
+        if out is None:
+            out = torch.empty_like(x if dtype is xt else y)
+            po = out.data_ptr()
+        else:
+            po = _dense(out, "out", dtype, shape, device)
+    rc = (_lib or load()).gtr_residual_norm(
+        _NORM_ARGS.pack(px, pxo, py, ppw, pg, prs, pnw, po, N, rows, D, DTYPE_IDS[xt], DTYPE_IDS[dtype],
+                        bool(post_norm), GATE_ACTS[gate_act], alpha, eps),
+        torch._C._cuda_getCurrentRawStream(device))
     if rc:
         _check("gtr_residual_norm", rc)
     return out

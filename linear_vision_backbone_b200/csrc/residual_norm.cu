@@ -15,6 +15,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "gtr_gla.h"
 #include "common.cuh"
 
@@ -22,7 +24,7 @@ namespace {
 
 using namespace gtr;
 
-constexpr int kMaxD = 16384;             // 512 threads of 32 elements
+constexpr int kMaxD = 16384;             // 1024 threads of 16 elements
 constexpr int kRowWarps = 8;            // rows per block where a warp has a row
 
 struct NormArgs {
@@ -33,35 +35,30 @@ struct NormArgs {
   float alpha, eps;
 };
 
-// VEC consecutive elements as floats: 16-byte accesses for VEC = 8.
+// VEC consecutive elements as loaded (16-byte accesses for VEC = 8), and as fp32.
 template <typename T, int VEC> struct Pack {
-  static __device__ __forceinline__ void load(const T* p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-      v[0] = ld_f(p);
-    } else {
-      constexpr int kWords = VEC * (int)sizeof(T) / 16;
-      uint4 u[kWords];
+  static constexpr int kWords = VEC == 1 ? 1 : VEC * (int)sizeof(T) / 16;
+  using Word = std::conditional_t<VEC == 1, T, uint4>;
+  Word w[kWords];
+  // read once: the caches are left to the weights
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) u[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-      T e[VEC];
-      memcpy(e, u, sizeof(e));
+    for (int i = 0; i < kWords; ++i) w[i] = __ldcs(reinterpret_cast<const Word*>(p) + i);
+  }
+  __device__ __forceinline__ void widen(float (&v)[VEC]) const {
+    T e[VEC];
+    memcpy(e, w, sizeof(e));
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[i] = Elem<T>::to_f(e[i]);
-    }
+    for (int i = 0; i < VEC; ++i) v[i] = Elem<T>::to_f(e[i]);
   }
   static __device__ __forceinline__ void store(T* p, const float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-      *p = Elem<T>::from_f(v[0]);
-    } else {
-      constexpr int kWords = VEC * (int)sizeof(T) / 16;
-      T e[VEC];
+    T e[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) e[i] = Elem<T>::from_f(v[i]);
-      uint4 u[kWords];
-      memcpy(u, e, sizeof(e));
+    for (int i = 0; i < VEC; ++i) e[i] = Elem<T>::from_f(v[i]);
+    Word o[kWords];
+    memcpy(o, e, sizeof(e));
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
-    }
+    for (int i = 0; i < kWords; ++i) reinterpret_cast<Word*>(p)[i] = o[i];
   }
 };
 // A weight vector: shared by every row, so it stays in the caches.
@@ -91,9 +88,8 @@ __device__ __forceinline__ float row_sum(float s, float* red) {
 }
 
 // kV vectors of VEC elements per thread; vector j of a row is thread j % G's.
-template <typename TX, typename TY, int VEC, int kV, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 32 * kRowWarps : 512)
-residual_norm_kernel(const NormArgs a) {
+template <typename TX, typename TY, int VEC, int kV, bool kWarpRow, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) residual_norm_kernel(const NormArgs a) {
   __shared__ float red[2][32];
   const int G = kWarpRow ? 32 : (int)blockDim.x;
   const int t = kWarpRow ? (threadIdx.x & 31) : (int)threadIdx.x;
@@ -107,76 +103,76 @@ residual_norm_kernel(const NormArgs a) {
   const TX* xr = (const TX*)a.x + row * a.D;
   const TY* yr = a.y ? (const TY*)a.y + row * a.D : nullptr;
   const TY* gr = a.gate ? (const TY*)a.gate + row / a.gate_rows * a.D : nullptr;
-  float x[kV][VEC], y[kV][VEC], gt[kV][VEC];
+  Pack<TX, VEC> xp[kV];
+  Pack<TY, VEC> yp[kV], gp[kV];
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
     const int u = t + j * G;
     if (u < nv) {
-      Pack<TX, VEC>::load(xr + (size_t)u * VEC, x[j]);
-      if (yr) Pack<TY, VEC>::load(yr + (size_t)u * VEC, y[j]);
-      if (gr) Pack<TY, VEC>::load(gr + (size_t)u * VEC, gt[j]);
+      xp[j].load(xr + (size_t)u * VEC);
+      if (yr) yp[j].load(yr + (size_t)u * VEC);
+      if (gr) gp[j].load(gr + (size_t)u * VEC);
     }
   }
-  if (yr) {
-    float inv = 1.f;
-    if (a.post_norm) {
-      float s = 0.f;
+  float inv = 1.f;
+  if (a.post_norm) {
+    float s = 0.f;
 #pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (t + j * G < nv)
+    for (int j = 0; j < kV; ++j)
+      if (t + j * G < nv) {
+        float y[VEC];
+        yp[j].widen(y);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) s = fmaf(y[j][e], y[j][e], s);
-      inv = rsqrtf(row_sum<kWarpRow>(s, red[0]) * inv_d + a.eps);
-    }
+        for (int e = 0; e < VEC; ++e) s = fmaf(y[e], y[e], s);
+      }
+    inv = rsqrtf(row_sum<kWarpRow>(s, red[0]) * inv_d + a.eps);
+  }
+  // x + alpha res_scale r, in fp32 until the pre-norm has used it
+  float x[kV][VEC];
+  float s = 0.f;
+  TX* xo = (TX*)a.x_out + row * a.D;
 #pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      const int u = t + j * G;
-      if (u >= nv) continue;
-      float w[VEC];
+  for (int j = 0; j < kV; ++j) {
+    const int u = t + j * G;
+    if (u >= nv) continue;
+    xp[j].widen(x[j]);
+    if (yr) {
+      float y[VEC], w[VEC];
+      yp[j].widen(y);
       if (a.post_norm) {
         if (a.post_w) {
           load_w<VEC>(a.post_w + u * VEC, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) y[j][e] *= inv * w[e];
+          for (int e = 0; e < VEC; ++e) y[e] *= inv * w[e];
         } else {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) y[j][e] *= inv;
+          for (int e = 0; e < VEC; ++e) y[e] *= inv;
         }
       }
       if (gr) {
+        float z[VEC];
+        gp[j].widen(z);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           // z sigmoid(z) and sigmoid(z) = 1 / (1 + e^-z)
-          const float z = gt[j][e];
-          const float sg = a.act == GTR_GATE_MUL ? z : 1.0f / (1.0f + __expf(-z));
-          y[j][e] *= a.act == GTR_GATE_SILU ? z * sg : sg;
+          const float sg = a.act == GTR_GATE_MUL ? z[e] : __fdividef(1.0f, 1.0f + __expf(-z[e]));
+          y[e] *= a.act == GTR_GATE_SILU ? z[e] * sg : sg;
         }
       }
       if (a.res_scale) {
         load_w<VEC>(a.res_scale + u * VEC, w);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) y[j][e] *= w[e];
+        for (int e = 0; e < VEC; ++e) y[e] *= w[e];
       }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[j][e] = fmaf(a.alpha, y[j][e], x[j][e]);
+      for (int e = 0; e < VEC; ++e) x[j][e] = fmaf(a.alpha, y[e], x[j][e]);
     }
-  }
-  TX* xo = (TX*)a.x_out + row * a.D;
-  if (yr || a.x_out != a.x) {
+    if (yr || a.x_out != a.x) Pack<TX, VEC>::store(xo + (size_t)u * VEC, x[j]);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      const int u = t + j * G;
-      if (u < nv) Pack<TX, VEC>::store(xo + (size_t)u * VEC, x[j]);
-    }
+    for (int e = 0; e < VEC; ++e) s = fmaf(x[j][e], x[j][e], s);
   }
   if (!a.out) return;
-  float s = 0.f;
-#pragma unroll
-  for (int j = 0; j < kV; ++j)
-    if (t + j * G < nv)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s = fmaf(x[j][e], x[j][e], s);
-  const float inv = rsqrtf(row_sum<kWarpRow>(s, red[1]) * inv_d + a.eps);
+  inv = rsqrtf(row_sum<kWarpRow>(s, red[1]) * inv_d + a.eps);
   TY* orow = (TY*)a.out + row * a.D;
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
@@ -199,28 +195,30 @@ template <typename TX, typename TY, int VEC, int kV>
 int launch_v(const NormArgs& a, int threads, cudaStream_t st) {
   if (threads == 32) {
     const long long blocks = (a.N + kRowWarps - 1) / kRowWarps;
-    return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, true>, dim3((unsigned)blocks), dim3(32 * kRowWarps), 0,
-                      st, a);
+    return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, true, 32 * kRowWarps>, dim3((unsigned)blocks),
+                      dim3(32 * kRowWarps), 0, st, a);
   }
-  return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, false>, dim3((unsigned)a.N), dim3((unsigned)threads), 0, st,
-                    a);
+  const dim3 grid((unsigned)a.N), block((unsigned)threads);
+  if (threads <= 512) return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, false, 512>, grid, block, 0, st, a);
+  return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, false, 1024>, grid, block, 0, st, a);
 }
+
+int round32(int n) { return (n + 31) / 32 * 32; }
 
 template <typename TX, typename TY>
 int launch_typed(const NormArgs& a, bool vec, cudaStream_t st) {
-  // threads of a row: 32 to 512 in powers of two, at most kPer elements each
-  const int kPer = 32;
-  int threads = 32;
-  while (threads * kPer < a.D) threads *= 2;
-  const int per = (a.D + threads - 1) / threads;   // elements per thread
   if (vec) {
-    const int nv = (a.D / 8 + threads - 1) / threads;
-    if (nv <= 1) return launch_v<TX, TY, 8, 1>(a, threads, st);
-    if (nv <= 2) return launch_v<TX, TY, 8, 2>(a, threads, st);
-    return launch_v<TX, TY, 8, 4>(a, threads, st);
+    // a warp for a row of up to 64 vectors; else two vectors a thread, or one
+    // while that leaves at most 512 threads and few rows (latency)
+    const int nv = a.D / 8;
+    if (nv <= 32) return launch_v<TX, TY, 8, 1>(a, 32, st);
+    if (nv <= 64) return launch_v<TX, TY, 8, 2>(a, 32, st);
+    if (nv <= 512 && a.N <= 592) return launch_v<TX, TY, 8, 1>(a, round32(nv), st);
+    return launch_v<TX, TY, 8, 2>(a, round32((nv + 1) / 2), st);
   }
-  if (per <= 8) return launch_v<TX, TY, 1, 8>(a, threads, st);
-  return launch_v<TX, TY, 1, 32>(a, threads, st);
+  if (a.D <= 256) return launch_v<TX, TY, 1, 8>(a, 32, st);
+  if (a.D <= 4096) return launch_v<TX, TY, 1, 8>(a, round32((a.D + 7) / 8), st);
+  return launch_v<TX, TY, 1, 16>(a, round32((a.D + 15) / 16), st);
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -233,11 +231,10 @@ bool overlap(const void* p, size_t n, const void* q, size_t m) {
 
 }  // namespace
 
-extern "C" GTR_API gtr_status_t gtr_residual_norm(const void* x, void* x_out, int x_dtype, const void* y, int post_norm,
-                                                  const float* post_w, const void* gate, int gate_act,
-                                                  long long gate_rows, const float* res_scale, float alpha,
-                                                  const float* pre_w, void* out, long long N, int D, float eps,
-                                                  int dtype, void* stream) {
+extern "C" GTR_API gtr_status_t gtr_residual_norm(const gtr_residual_norm_args* args, void* stream) {
+  if (!args) return GTR_ERR_INVALID_ARG;
+  const auto [x, x_out, y, post_w, gate, res_scale, pre_w, out, N, gate_rows, D, x_dtype, dtype, post_norm, gate_act,
+              alpha, eps] = *args;
   if (x_dtype < 0 || x_dtype > 2 || dtype < 0 || dtype > 2) return GTR_ERR_INVALID_ARG;
   if (N < 0 || D < 0 || gate_act < GTR_GATE_MUL || gate_act > GTR_GATE_SILU) return GTR_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || !(eps < 3.0e38f)) return GTR_ERR_INVALID_ARG;

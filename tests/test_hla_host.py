@@ -127,31 +127,28 @@ def test_hla_workspace_size(lib):
 
 
 def test_residual_norm_rejects_invalid_arguments_before_any_launch(lib):
-    names = ["x", "x_out", "x_dtype", "y", "post_norm", "post_w", "gate", "gate_act", "gate_rows", "res_scale",
-             "alpha", "pre_w", "out", "N", "D", "eps", "dtype", "stream"]
-    base = dict(x=1 << 20, x_out=1 << 20, x_dtype=0, y=2 << 20, post_norm=0, post_w=None, gate=None, gate_act=0,
-                gate_rows=1, res_scale=None, alpha=1.0, pre_w=None, out=3 << 20, N=4, D=64, eps=1e-5, dtype=1,
-                stream=None)
+    base = dict(x=1 << 20, x_out=1 << 20, y=2 << 20, post_w=0, gate=0, res_scale=0, pre_w=0, out=3 << 20, N=4,
+                gate_rows=1, D=64, x_dtype=0, dtype=1, post_norm=0, gate_act=0, alpha=1.0, eps=1e-5)
 
     def call(**kw):
-        a = dict(base, **kw)
-        return lib.gtr_residual_norm(*[a[n] for n in names])
+        return lib.gtr_residual_norm(binding._NORM_ARGS.pack(*dict(base, **kw).values()), None)
+    assert lib.gtr_residual_norm(None, None) == -1
     assert call(x_dtype=5) == -1 and call(dtype=-1) == -1
     assert call(N=-1) == -1 and call(D=-1) == -1 and call(N=1 << 32) == -1
     assert call(D=0) == -2 and call(D=16385) == -2
     assert call(x_dtype=1, dtype=2) == -2                 # a 16-bit stream has its branch's type
     assert call(gate_act=3) == -1
     assert call(eps=-1.0) == -1 and call(eps=float("nan")) == -1
-    assert call(x=None) == -1 and call(x_out=None) == -1
+    assert call(x=0) == -1 and call(x_out=0) == -1
     assert call(post_w=4 << 20) == -1                     # a weight without its norm
-    assert call(pre_w=4 << 20, out=None) == -1
-    assert call(y=None, post_norm=1) == -1 and call(y=None, gate=4 << 20) == -1 and call(y=None, res_scale=4 << 20) == -1
+    assert call(pre_w=4 << 20, out=0) == -1
+    assert call(y=0, post_norm=1) == -1 and call(y=0, gate=4 << 20) == -1 and call(y=0, res_scale=4 << 20) == -1
     assert call(gate=4 << 20, gate_rows=3) == -1 and call(gate=4 << 20, gate_rows=0) == -1
     assert call(x=(1 << 20) + 2, x_out=(1 << 20) + 2) == -3 and call(y=(2 << 20) + 1) == -3
     assert call(x_out=(1 << 20) + 256) == -1              # x_out over part of x
     assert call(out=1 << 20) == -1 and call(out=2 << 20) == -1
     assert call(gate=3 << 20) == -1                       # out over the gate
-    assert call(N=0, x=None, x_out=None) == 0
+    assert call(N=0, x=0, x_out=0) == 0
 
 
 def test_binding_refuses_what_is_not_a_cuda_tensor():
@@ -166,14 +163,17 @@ def test_binding_refuses_what_is_not_a_cuda_tensor():
         binding.residual_norm(torch.zeros(4, 64))
 
 
-def test_argument_struct_has_the_headers_size(tmp_path):
+def test_argument_structs_have_the_headers_sizes(tmp_path):
     import subprocess
     src = tmp_path / "s.c"
     src.write_text(f'#include "{build.INCLUDE}/gtr_gla.h"\n#include <stdio.h>\n'
-                   'int main(void) { printf("%zu %zu", sizeof(gtr_hla_args), offsetof(gtr_hla_args, nseq)); }\n')
+                   'int main(void) { printf("%zu %zu %zu", sizeof(gtr_hla_args), offsetof(gtr_hla_args, nseq),'
+                   ' sizeof(gtr_residual_norm_args)); }\n')
     subprocess.run(["gcc", str(src), "-o", str(tmp_path / "s")], check=True)
-    size, nseq = map(int, subprocess.run([str(tmp_path / "s")], check=True, capture_output=True).stdout.split())
+    size, nseq, norm = map(int, subprocess.run([str(tmp_path / "s")], check=True, capture_output=True).stdout.split())
     assert size == binding._HLA_ARGS.size
+    # C pads the struct to its 8-byte alignment
+    assert norm == -(-binding._NORM_ARGS.size // 8) * 8
     assert nseq == 13 * 8 + 8 + 5 * 8
 
 
