@@ -55,11 +55,11 @@ void make_plan(int nseq, int T, int H, int dk, int dv, int dtype, bool equal, in
   const bool tc = tc_shape(dk, dv, dtype);
   const long long C = tc ? hla::kC : hla::kSimtBatch;
   const long long slots = tc ? sms / (dv / 64) : (long long)sms * 4;
-  const long long len = equal ? T / nseq : T, longest = len > C ? (len + C - 1) / C : 1;
-  const long long B = H * (equal ? nseq * longest : T / C + nseq);      // at most, with cu_seqlens
+  const long long len = equal ? T / nseq : T, longest = (len + C - 1) / C;
+  const long long B = H * (equal ? nseq * (longest + 1) : T / C + 2ll * nseq);   // units; at most, with cu_seqlens
   const long long items = (long long)nseq * H;
   const long long share = (B + slots - 1) / slots;
-  const double whole = equal ? (double)((items + slots - 1) / slots) * (double)longest
+  const double whole = equal ? (double)((items + slots - 1) / slots) * (double)(longest + 1)
                              : (double)(share > longest ? share : longest);
   p->cut = longest > 1 && whole > share * (1.0 + kSum) + kExtra;
   long long J;
@@ -199,7 +199,7 @@ int check_args(const gtr_hla_args* a, bool step, hla::Params* p, bool* empty) {
   if (a->Hk == 0 || a->H % a->Hk != 0) return GTR_ERR_INVALID_ARG;
   if (a->H > 65535) return GTR_ERR_UNSUPPORTED;
   // blocks of at least 16 tokens of all sequences and heads are counted in 31 bits
-  if (!step && ((long long)a->T / hla::kSimtBatch + a->nseq) * a->H >= (1ll << 31)) return GTR_ERR_UNSUPPORTED;
+  if (!step && ((long long)a->T / hla::kSimtBatch + 2ll * a->nseq) * a->H >= (1ll << 31)) return GTR_ERR_UNSUPPORTED;
   if (step ? (a->T != a->nseq || a->cu_seqlens || a->seen) : (!a->cu_seqlens && a->T % a->nseq != 0))
     return GTR_ERR_INVALID_ARG;
   if (a->T > 0 && (!a->q || !a->k || !a->v || !a->g || !a->out)) return GTR_ERR_INVALID_ARG;
@@ -284,7 +284,8 @@ GTR_API gtr_status_t gtr_hla_fwd(const gtr_hla_args* args, void* stream) {
   if (tc && (map_rows(&maps.q, args->dtype, p.q, p.T, p.Hk, p.dk, p.ldq) ||
              map_rows(&maps.k, args->dtype, p.k, p.T, p.Hk, p.dk, p.ldk) ||
              map_rows(&maps.v, args->dtype, p.v, p.T, p.H, p.dv, p.ldv) ||
-             map_rows(&maps.z, args->dtype, p.z ? p.z : p.v, p.T, p.H, p.dv, p.z ? p.ldz : p.ldv)))
+             map_rows(&maps.z, args->dtype, p.z ? p.z : p.v, p.T, p.H, p.dv, p.z ? p.ldz : p.ldv) ||
+             map_rows(&maps.o, args->dtype, p.out, p.T, p.H, p.dv, p.ldo)))
     return GTR_ERR_CUDA;
   const auto launch = [&](bool sum) {
     return tc ? launch_tc(p, maps, args->dtype, sum, st) : launch_prompt(p, args->dtype, sum, st);

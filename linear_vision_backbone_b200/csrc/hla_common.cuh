@@ -2,12 +2,13 @@
 // their parameters, the split of the work, the scan over its cuts, and the
 // decay.
 //
-// The split.  Sequence n has nb_n = max(1, ceil(len_n / C)) blocks of C tokens
-// in each of its H heads (one, empty, for a length of zero: its state still
-// moves).  All blocks stand in one line, sequence by sequence, head by head,
-// and group j of J takes the blocks [j B / J, (j + 1) B / J) of the B = H sum
-// nb_n.  Only the device knows the lengths, so every kernel finds its range
-// from cu_seqlens by itself.  With `cut` a range may end inside a (sequence,
+// The split.  Sequence n has nb_n = ceil(len_n / C) blocks of C tokens in each of
+// its H heads; each (sequence, head) is a run of nb_n + 1 units, its blocks and
+// one more for what starting and ending it costs (a part of a block's time: the
+// state is read and written).  All units stand in one line, sequence by
+// sequence, head by head, and group j of J takes the blocks among the units [j B
+// / J, (j + 1) B / J) of the B = H sum (nb_n + 1).  Only the device knows the
+// lengths, so every kernel finds its range from cu_seqlens by itself.  With `cut` a range may end inside a (sequence,
 // head): the part before the cut then has a summary (the state it makes from
 // zero, and its decay) in workspace entry j, which the scan turns into the state
 // the next group starts from; there are J entries whatever the sizes.  Without,
@@ -49,22 +50,24 @@ template <int C> __device__ __forceinline__ int seq_rows(const Params& p, int n,
   }
   return b - a;
 }
-__device__ __forceinline__ int n_blocks(int len, int C) { return len <= C ? 1 : (len - 1) / C + 1; }
+__device__ __forceinline__ int n_blocks(int len, int C) { return len <= 0 ? 0 : (len - 1) / C + 1; }
+// Units of the line of blocks that a (sequence, head) of this length takes.
+__device__ __forceinline__ int n_units(int len, int C) { return n_blocks(len, C) + 1; }
 
-// A place in the line of blocks: block b of head h of sequence n.
+// A place in the line: unit b of head h of sequence n.
 struct Place {
   int n, h, b;
-  // the place `off` blocks into sequence n of nb blocks a head
-  __device__ __forceinline__ void set(int seq, int off, int nb) {
+  // the place `off` units into sequence n of `per` units a head
+  __device__ __forceinline__ void set(int seq, int off, int per) {
     n = seq;
-    h = off / nb;
-    b = off - h * nb;
+    h = off / per;
+    b = off - h * per;
   }
 };
 
-// Group j's range: the line's B blocks, the groups J that have any (at most
-// one per block, so that none between two others is empty), the places x0 and
-// x1 it lies between and the sequences they fall into (nseq for x = B).
+// Group j's range: the line's B units, the groups J that have any (at most one
+// per unit), the places x0 and x1 it lies between and the sequences they fall
+// into (nseq for x = B).
 struct Range {
   int B, x0, x1, J;                // B < 2^31: the host refuses more
   Place a, b;
@@ -81,18 +84,18 @@ struct Range {
 // again after the caller's next barrier.
 template <int C> __device__ __forceinline__ void locate(const Params& p, int j, int* scratch, Range& g) {
   if (!p.cu) {
-    const int nb = n_blocks(p.T / p.nseq, C), per = nb * p.H;
+    const int nu = n_units(p.T / p.nseq, C), per = nu * p.H;
     g.set(per * p.nseq, p.J, j);
     const int n0 = g.x0 / per, n1 = g.x1 / per;
-    g.a.set(n0, g.x0 - n0 * per, nb);
-    g.b.set(n1, g.x1 - n1 * per, nb);
+    g.a.set(n0, g.x0 - n0 * per, nu);
+    g.b.set(n1, g.x1 - n1 * per, nu);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int per = (p.nseq + blockDim.x - 1) / (int)blockDim.x;   // sequences per thread, consecutive ones
   const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
   int mine = 0, r;
-  for (int n = n0; n < n1; ++n) mine += n_blocks(seq_rows<C>(p, n, r), C);
+  for (int n = n0; n < n1; ++n) mine += n_units(seq_rows<C>(p, n, r), C);
   int inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -112,11 +115,11 @@ template <int C> __device__ __forceinline__ void locate(const Params& p, int j, 
   }
   g.set(total * p.H, p.J, j);
   for (int n = n0; n < n1; ++n) {
-    const int nb = n_blocks(seq_rows<C>(p, n, r), C);
-    const int s = before * p.H, e = (before + nb) * p.H;
-    if (s <= g.x0 && g.x0 < e) { scratch[32] = n; scratch[33] = g.x0 - s; scratch[34] = nb; }
-    if (s <= g.x1 && g.x1 < e) { scratch[35] = n; scratch[36] = g.x1 - s; scratch[37] = nb; }
-    before += nb;
+    const int nu = n_units(seq_rows<C>(p, n, r), C);
+    const int s = before * p.H, e = (before + nu) * p.H;
+    if (s <= g.x0 && g.x0 < e) { scratch[32] = n; scratch[33] = g.x0 - s; scratch[34] = nu; }
+    if (s <= g.x1 && g.x1 < e) { scratch[35] = n; scratch[36] = g.x1 - s; scratch[37] = nu; }
+    before += nu;
   }
   __syncthreads();
   g.a.set(scratch[32], scratch[33], scratch[34]);
@@ -145,21 +148,23 @@ template <int C> __device__ __forceinline__ bool next_part(const Params& p, Walk
     const int len = seq_rows<C>(p, w.at.n, a);
     const int nb = n_blocks(len, C);
     const int n = w.at.n, h = w.at.h, b0 = w.at.b;
-    int take = min(nb - b0, w.left);
-    w.left -= take;
+    const int units = min(nb + 1 - b0, w.left);
+    int end = min(b0 + units, nb);             // blocks b0 .. end - 1
+    w.left -= units;
     w.at.b = 0;                                // what is left of the range starts the next head
     if (++w.at.h == p.H) { w.at.h = 0; w.at.n++; }
-    if (!p.cut) {
-      if (b0 > 0) continue;                    // another group has it whole
-      take = nb;
+    if (b0 > 0) {
+      if (!p.cut || b0 >= nb) continue;        // another group has it whole, or all of its blocks
+    } else if (!p.cut) {
+      end = nb;
     }
     g.n = n;
     g.h = h;
     g.first = b0 == 0;
-    g.last = b0 + take == nb;
+    g.last = end == nb;
     g.t0 = a + b0 * C;
-    g.len = min(len - b0 * C, take * C);
-    g.nb = len > 0 ? take : 0;
+    g.len = min(len - b0 * C, (end - b0) * C);
+    g.nb = end - b0;
     g.slot = p.slots ? __ldg(p.slots + n) : n;
     if (g.slot >= p.nslots && (p.state_in || p.state_out)) {
       gtr_flag(kStatusBadSlot);
@@ -188,9 +193,9 @@ template <int C> __device__ __forceinline__ bool cut_part(const Params& p, const
   const Place& b = rg.b;
   if (rg.x0 >= rg.x1 || b.n >= p.nseq) return false;
   int a;
-  seq_rows<C>(p, b.n, a);
-  const int h = b.h, e = b.b;                  // e blocks before the cut
-  if (e == 0) return false;
+  const int len = seq_rows<C>(p, b.n, a);
+  const int h = b.h, e = b.b;                  // e units before the cut
+  if (e == 0 || e >= n_blocks(len, C)) return false;   // nothing, or every block
   const int b0 = max(0, e - (rg.x1 - rg.x0));
   g.n = b.n;
   g.h = h;
@@ -235,7 +240,7 @@ template <int C> __global__ void __launch_bounds__(kScanThreads) hla_scan(const 
   if (!cut_part<C>(p, rg, g) || !g.first) return;
   // the summaries of this (sequence, head): of the groups that end before it does
   int r;
-  const int end = rg.x1 - g.nb + n_blocks(seq_rows<C>(p, g.n, r), C);
+  const int end = rg.x1 - g.nb + n_blocks(seq_rows<C>(p, g.n, r), C);   // the unit behind its blocks
   int m = 1;
   while (j + m < rg.J && rg.start(j + m + 1) < end) ++m;
   const int per_state = p.dk * p.dv;

@@ -37,7 +37,7 @@
 //         half row), S <- a S + kv, and its terms for the next block's qs
 //   16    loads of k and v (TMA, 128-byte swizzled tiles of 128 rows x 64 columns)
 //   17    issues the products
-//   18,19 loads of q and of z, each waiting for its own buffers only
+//   18,19 loads of q; loads of z and stores of the outputs
 // The products of a block are issued scores, kv, qs, pv: while the P warps turn
 // block c's scores around and the output warps still read block c - 1's qs and
 // pv, the tensor cores do its kv.
@@ -57,12 +57,12 @@ constexpr int kTcThreads = 20 * 32;
 constexpr int kSumThreads = 10 * 32;
 
 struct Maps {
-  CUtensorMap q, k, v, z;
+  CUtensorMap q, k, v, z, o;
 };
 
 // mbarriers of a block of threads, in 8-byte units
 enum Bars {
-  kQF = 0, kQE = 2, kKF = 4, kKE = 7, kVF = 10, kVE = 13, kZF = 16, kZE = 18, kScF = 20, kPF = 21, kPvF = 22, kOE = 23,
+  kQF = 0, kQE = 2, kKF = 4, kKE = 7, kVF = 10, kVE = 13, kZF = 16, kOS = 18, kScF = 20, kPF = 21, kPvF = 22, kOE = 23,
   kSF = 24, kSE = 25, kWF = 26, kWE = 27, kKvF = 28, kKvE = 29, kGF = 30, kGE = 32, kXF = 34, kXE = 35, kNumBars = 36
 };
 
@@ -111,6 +111,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "[%5];" ::"r"(saddr(dst)), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(saddr(bar))
       : "memory");
 }
+// Shared -> global, as part of the thread's bulk group; no coordinate is negative, c0 is a multiple of 64 elements.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(c0), "r"(c1), "r"(c2), "r"(saddr(src))
+               : "memory");
+}
+// A line of global memory into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0), "r"(c1),
                "r"(c2)
@@ -209,7 +217,7 @@ template <int N> __device__ __forceinline__ void set_registers() {
 // is 64 registers of a thread for dk = 128, 32 for dk = 64).
 template <int DK> struct Regs {
   static constexpr int kP = DK == 128 ? 72 : 96, kBuild = kP, kOut = 96;
-  static constexpr int kState = DK == 128 ? 160 : 104, kMisc = DK == 128 ? 80 : 88;
+  static constexpr int kState = DK == 128 ? 160 : 96, kMisc = DK == 128 ? 80 : 96;
   static_assert(kP + kBuild + kOut + kState + kMisc <= 5 * 96, "no more than the block was launched with");
 };
 
@@ -254,6 +262,11 @@ template <typename T> __device__ __forceinline__ uint32_t term(uint64_t& x) {
   return h;
 }
 
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // One lane of the (whole) warp, the same each time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -338,7 +351,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) {
       if (i < 2) { tc::mbar_init(bar + kQF + i, 1); tc::mbar_init(bar + kQE + i, 1); }
-      if (i < 2) { tc::mbar_init(bar + kZF + i, 1); tc::mbar_init(bar + kZE + i, kC); }
+      if (i < 2) { tc::mbar_init(bar + kZF + i, 1); tc::mbar_init(bar + kOS + i, 4); }
       tc::mbar_init(bar + kKF + i, 1); tc::mbar_init(bar + kKE + i, 1);
       tc::mbar_init(bar + kVF + i, 1); tc::mbar_init(bar + kVE + i, 1);
     }
@@ -375,6 +388,11 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   uint32_t is = 0;                                             // those that had a state before them
   bool ok = true;
   auto wait = [&](int b, uint32_t parity) { return tc::mbar_wait(bar + b, parity); };
+  // two barriers: their first probes are in flight together (a probe takes about 120 cycles)
+  auto wait2 = [&](int b, uint32_t pb, int c, uint32_t pc) {
+    const uint32_t x = tc::mbar_try(bar + b, pb), y = tc::mbar_try(bar + c, pc);
+    return (x || tc::mbar_wait(bar + b, pb)) && (y || tc::mbar_wait(bar + c, pc));
+  };
   // one arrival for a warp, after all its lanes
   auto warp_arrive = [&](int b) {
     __syncwarp();
@@ -432,11 +450,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         const uint8_t* K = sm + L::kK + sk * L::kQTile;
         const uint8_t* V = sm + L::kV + sv * kTile;
         const uint8_t* W = sm + L::kW;
-        ok = wait(kKF + sk, i / L::kNK & 1);
         if constexpr (!kSum) {
           const int sq = i % L::kNQ;
           const uint8_t* Q = sm + L::kQ + sq * L::kQTile;
-          ok = ok && wait(kQF + sq, i / L::kNQ & 1);
+          ok = wait2(kKF + sk, i / L::kNK & 1, kQF + sq, i / L::kNQ & 1);
           if (!ok) break;
           tc::tc_after_sync();
           const uint64_t aq = tc::sdesc(saddr(Q), 16, 1024), bk = tc::sdesc(saddr(K), 16, 1024);
@@ -449,8 +466,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             tc::mma_commit(bar + kScF);
           }
           __syncwarp();
+        } else {
+          ok = wait(kKF + sk, i / L::kNK & 1);
         }
-        ok = ok && wait(kWF, par) && wait(kKvE, par ^ 1);
+        ok = ok && wait2(kWF, par, kKvE, par ^ 1);
         if (!ok) break;
         tc::tc_after_sync();
         if ((c + 1 < nb || want_end) && lead) {
@@ -474,12 +493,12 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         if constexpr (!kSum) {
           const int sq = i % L::kNQ;
           const uint64_t aq = tc::sdesc(saddr(sm + L::kQ + sq * L::kQTile), 16, 1024);
-          ok = wait(kOE, par ^ 1);                               // qs and pv of the block before are read
+          // the terms of S; qs and pv of the block before are read
+          const bool state = c > 0 || has_start(g);
+          ok = state ? wait2(kSF, is & 1, kOE, par ^ 1) : wait(kOE, par ^ 1);
           if (!ok) break;
-          if (c > 0 || has_start(g)) {
-            ok = wait(kSF, is & 1);
-            if (!ok) break;
-            tc::tc_after_sync();
+          tc::tc_after_sync();
+          if (state) {
             const uint64_t bs = tc::sdesc(saddr(sm + L::kS), L::kSTile, 1024);
             if (lead) {
 #pragma unroll
@@ -679,10 +698,26 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       warp_arrive(kSF);
       return true;
     };
+    // the row of the state a part starts from, on its way into L2 while the part before is at work
+    Walk ahead{rg.a, rg.x1 - rg.x0};
+    auto look_ahead = [&]() {
+      if constexpr (!kSum) {
+        Part n;
+        if (!p.state_in || !next_part<kC>(p, ahead, n)) return;
+        const float* src = start_state(p, n, group_j);
+        if (src) {
+          src += (size_t)r * p.dv + half * 64 + (DK == 128 ? 0 : (lane >> 4) * 32);
+          prefetch_l2(src);
+          if (DK == 128) prefetch_l2(src + 32);
+        }
+      }
+    };
+    look_ahead();                                                 // the first part itself
     for_parts([&](const Part& g) {
       const bool want_end = wants_end(g);
       const size_t hs = (size_t)DK * p.dv, at = (size_t)r * p.dv + half * 64;
       const float* src = kSum ? nullptr : start_state(p, g, group_j);
+      look_ahead();
 #pragma unroll
       for (int x = 0; x < kRuns; ++x)
 #pragma unroll
@@ -755,7 +790,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       for_parts([&](const Part& g) {
         for (int c = 0; c < g.nb && ok; ++c) {
           const uint32_t i = it + c, par = i & 1;
-          ok = wait(kGF + (i & 1), i >> 1 & 1) && wait(kScF, par);
+          ok = wait2(kGF + (i & 1), i >> 1 & 1, kScF, par);
           if (!ok) break;
           tc::tc_after_sync();
           const float* G = Gs + (i & 1) * kC;
@@ -846,7 +881,8 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         for (int c = 0; c < g.nb && ok; ++c) {
           const uint32_t i = it + c, par = i & 1;
           const int nv = min(kC, g.len - c * kC);
-          ok = wait(kGF + (i & 1), i >> 1 & 1);
+          const int sz = i % L::kNZ;
+          ok = wait2(kGF + (i & 1), i >> 1 & 1, kZF + sz, i / L::kNZ & 1);   // z, or the buffer alone
           if (!ok) break;
           const float Gi = Gs[(i & 1) * kC + row];
           warp_arrive(kGE + (i & 1));
@@ -879,7 +915,6 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
                 y[e] = tc::ffma2(f11, add2(pack2(a[2 * e], a[2 * e + 1]), pack2(b[2 * e], b[2 * e + 1])), y[e]);
             }
           };
-          const int sz = i % L::kNZ;
           uint8_t* Z = sm + L::kZ + sz * kTile;
           uint64_t inv2 = both(1.f);
           if (gated) {
@@ -905,38 +940,28 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
               peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));
             }
             inv2 = both(rsqrtf(ss / (float)p.dv + kRmsEps));
-            ok = wait(kZF + sz, i / L::kNZ & 1);
-            if (!ok) break;
-          } else {
-            // the copies of the block that used this buffer before are done
-            tc::named_barrier(3, 128);
           }
           const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(p.w + half * 64);
-#pragma unroll 1
+#pragma unroll 2
           for (int u = 0; u < 8; ++u) {
             uint4* unit16 = reinterpret_cast<uint4*>(Z + row * 128 + ((u ^ (row & 7)) << 4));
             uint64_t y[4];
             if (gated) {
-              uint64_t wt[4] = {inv2, inv2, inv2, inv2};
-              if (p.w) {
-                const ulonglong2 wa = __ldg(wp + 2 * u), wb = __ldg(wp + 2 * u + 1);
-                wt[0] = tc::fmul2(wa.x, inv2); wt[1] = tc::fmul2(wa.y, inv2);
-                wt[2] = tc::fmul2(wb.x, inv2); wt[3] = tc::fmul2(wb.y, inv2);
-              }
+              ulonglong2 wa = make_ulonglong2(both(1.f), both(1.f)), wb = wa;
+              if (p.w) { wa = __ldg(wp + 2 * u); wb = __ldg(wp + 2 * u + 1); }
               const uint4 zu = *unit16;
               const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
+              columns(u, y);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 // z sigmoid(z) = z / (1 + 2^(-z log2 e))
                 const uint64_t z = widen<T>(zw[e]);
                 const float2 m = tc::f2unpack(tc::fmul2(z, both(-kLog2e)));
                 const float2 q = tc::f2unpack(add2(tc::f2pack(tc::ex2(m.x), tc::ex2(m.y)), both(1.f)));
-                const float2 zf = tc::f2unpack(z);
-                wt[e] = tc::fmul2(wt[e], tc::f2pack(__fdividef(zf.x, q.x), __fdividef(zf.y, q.y)));
+                y[e] = tc::fmul2(tc::fmul2(y[e], inv2), tc::fmul2(z, tc::f2pack(rcp(q.x), rcp(q.y))));
               }
-              columns(u, y);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = tc::fmul2(y[e], wt[e]);
+              y[0] = tc::fmul2(y[0], wa.x); y[1] = tc::fmul2(y[1], wa.y);
+              y[2] = tc::fmul2(y[2], wb.x); y[3] = tc::fmul2(y[3], wb.y);
             } else {
               columns(u, y);
             }
@@ -944,22 +969,18 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           }
           tc::tc_before_sync();
           warp_arrive(kOE);
-          tc::named_barrier(3, 128);
-          {
+          if (nv < kC) {
+            // behind the sequence's last token the rows are not ours: copied row by row
+            tc::named_barrier(3, 128);
             const int u = row & 7;
             T* dst = (T*)p.out + (long long)(g.t0 + c * kC) * p.ldo + (long long)g.h * p.dv + half * 64 + u * 8;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int r = (row >> 3) + 16 * e;
-              if (r < nv)
-                *reinterpret_cast<uint4*>(dst + r * p.ldo) =
-                    *reinterpret_cast<const uint4*>(Z + r * 128 + ((u ^ (r & 7)) << 4));
-            }
+#pragma unroll 1
+            for (int r = row >> 3; r < nv; r += 16)
+              *reinterpret_cast<uint4*>(dst + r * p.ldo) =
+                  *reinterpret_cast<const uint4*>(Z + r * 128 + ((u ^ (r & 7)) << 4));
           }
-          if (gated) {
-            tc::fence_async_smem();                             // the next z is written by the async proxy
-            tc::mbar_arrive_one(bar + kZE + sz);
-          }
+          tc::fence_async_smem();                               // for the copy engine: the stores, and the next z
+          warp_arrive(kOS + sz);
         }
         it += g.nb;
       });
@@ -984,22 +1005,55 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         it += g.nb;
       });
     } else if (role == kLoadZ) {
+      // z tiles in, output tiles out: one buffer holds a block's z, then its
+      // outputs; it is free once the store has read it
       set_registers<Regs<DK>::kMisc>();
-      if (gated)
-        for_parts([&](const Part& g) {
-          if (lane == 0) {
-            for (int c = 0; c < g.nb && ok; ++c) {
-              const uint32_t i = it + c;
-              const int sz = i % L::kNZ;
-              ok = wait(kZE + sz, (i / L::kNZ & 1) ^ 1);
+      int pt[L::kNZ] = {}, ph[L::kNZ] = {};                      // the block in each buffer: row (-1: no store), head
+      auto finish = [&](uint32_t i, int sz) {
+        if (!wait(kOS + sz, i / L::kNZ & 1)) return false;
+        if (pt[sz] >= 0) {
+          tma_store_3d(&maps.o, sm + L::kZ + sz * kTile, half * 64, ph[sz], pt[sz]);
+          tc::bulk_commit();
+          tc::bulk_wait_read<0>();
+        }
+        return true;
+      };
+      for_parts([&](const Part& g) {
+        if (lane == 0) {
+          for (int c = 0; c < g.nb && ok; ++c) {
+            const uint32_t i = it + c;
+            const int t = g.t0 + c * kC;
+#pragma unroll
+            for (int sz = 0; sz < L::kNZ; ++sz) {
+              if (i % L::kNZ != sz) continue;
+              if (i >= L::kNZ) ok = finish(i - L::kNZ, sz);
               if (!ok) break;
-              tc::mbar_arrive_tx(bar + kZF + sz, kTile);
-              tma_load_3d(sm + L::kZ + sz * kTile, &maps.z, half * 64, g.h, g.t0 + c * kC, bar + kZF + sz);
+              pt[sz] = g.len - c * kC >= kC ? t : -1;
+              ph[sz] = g.h;
+              if (gated) {
+                tc::mbar_arrive_tx(bar + kZF + sz, kTile);
+                tma_load_3d(sm + L::kZ + sz * kTile, &maps.z, half * 64, g.h, t, bar + kZF + sz);
+              } else {
+                tc::mbar_arrive_one(bar + kZF + sz);
+              }
             }
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          it += g.nb;
-        });
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        it += g.nb;
+      });
+      if (lane == 0 && ok) {
+#pragma unroll
+        for (int back = L::kNZ; back > 0; --back) {
+          if (it < (uint32_t)back) continue;
+          const uint32_t i = it - back;
+#pragma unroll
+          for (int sz = 0; sz < L::kNZ; ++sz)
+            if (i % L::kNZ == sz) ok = ok && finish(i, sz);
+        }
+        tc::bulk_wait<0>();
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   }
   // a bounded wait that ran out ends every warp's walk the same way; loads and

@@ -180,34 +180,36 @@ def test_argument_structs_have_the_headers_sizes(tmp_path):
 # --------------------------------------------------- the split of the work
 def _ranges(lens, H, C, groups):
     """The kernels' arithmetic (hla_common.cuh): the parts of every group and the cuts."""
-    nb = [max(1, -(-n // C)) for n in lens]
-    B = H * sum(nb)
+    nb = [-(-n // C) for n in lens]
+    B = H * sum(n + 1 for n in nb)
     J = min(groups, B)
-    starts = []                                     # first place of each sequence
-    x = 0
+    starts, x = [], 0                               # first unit of each sequence
     for n in nb:
         starts.append(x)
-        x += n * H
+        x += (n + 1) * H
+    at = lambda x: (max(i for i, s in enumerate(starts) if s <= x),)  # noqa: E731
     parts, cuts = [], []
     for j in range(groups):
         x0, x1 = B * min(j, J) // J, B * min(j + 1, J) // J
         mine, x = [], x0
         while x < x1:
-            n = max(i for i, s in enumerate(starts) if s <= x)
-            h, b0 = divmod(x - starts[n], nb[n])
-            take = min(nb[n] - b0, x1 - x)
-            mine.append((n, h, b0, take))
-            x += take
+            n, = at(x)
+            h, b0 = divmod(x - starts[n], nb[n] + 1)
+            units = min(nb[n] + 1 - b0, x1 - x)
+            end = min(b0 + units, nb[n])
+            if b0 == 0 or b0 < nb[n]:
+                mine.append((n, h, b0, end - b0, end == nb[n]))
+            x += units
         parts.append(mine)
-        if x1 < B and x1 > x0:
-            n = max(i for i, s in enumerate(starts) if s <= x1)
-            h, e = divmod(x1 - starts[n], nb[n])
-            if e:
-                b0 = 0 if e <= x1 - x0 else e - (x1 - x0)
+        if x0 < x1 < B:
+            n, = at(x1)
+            h, e = divmod(x1 - starts[n], nb[n] + 1)
+            if 0 < e < nb[n]:
+                b0 = max(0, e - (x1 - x0))
                 m = 0
                 if b0 == 0:                          # the scan's walk from here
                     end, m = x1 - e + nb[n], 1
-                    while j + m < J and B * (j + m + 1) // J < end:
+                    while j + m < J and B * min(j + m + 1, J) // J < end:
                         m += 1
                 cuts.append((j, n, h, b0, e - b0, m))
     return nb, J, parts, cuts
@@ -220,18 +222,21 @@ def test_every_block_is_in_one_part_and_every_cut_is_scanned():
         lens = [rng.choice([0, 1, C - 1, C, C + 1, rng.randrange(9 * C)]) for _ in range(rng.randrange(1, 9))]
         H, groups = rng.choice([1, 3, 8]), rng.choice([1, 5, 74, 148])
         nb, J, parts, cuts = _ranges(lens, H, C, groups)
-        seen = [(n, h, b) for mine in parts for n, h, b0, take in mine for b in range(b0, b0 + take)]
+        seen = [(n, h, b) for mine in parts for n, h, b0, k, _ in mine for b in range(b0, b0 + k)]
         assert seen == [(n, h, b) for n in range(len(lens)) for h in range(H) for b in range(nb[n])]
-        assert all(parts[j] for j in range(J)) and not any(parts[J:])     # no empty group between two others
+        # the state of every (sequence, head), empty ones too, is started once and ended once
+        heads = [(n, h) for n in range(len(lens)) for h in range(H)]
+        assert [(n, h) for mine in parts for n, h, b0, k, last in mine if b0 == 0] == heads
+        assert [(n, h) for mine in parts for n, h, b0, k, last in mine if last] == heads
         # a part that does not start its (sequence, head) starts its group, and the group before has its summary
         entry = {j: (n, h, b0 + k) for j, n, h, b0, k, _ in cuts}
         for j, mine in enumerate(parts):
-            for x, (n, h, b0, take) in enumerate(mine):
+            for x, (n, h, b0, k, last) in enumerate(mine):
                 if b0:
                     assert x == 0 and entry[j - 1] == (n, h, b0)
-            n, h, b0, take = mine[-1] if mine else (0, 0, 0, 0)
-            if mine and b0 + take < nb[n]:
-                assert [(c[3], c[4]) for c in cuts if c[0] == j] == [(b0, take)]
+                if not last:
+                    assert [(c[1], c[2], c[3], c[4]) for c in cuts if c[0] == j] == [(n, h, b0, k)] and k > 0
+        assert sum(not p[4] for mine in parts for p in mine) == len(cuts)
         # each cut is walked by exactly one scan, from its (sequence, head)'s first group on
         walked = [j + u for j, *_, m in cuts for u in range(m)]
         assert sorted(walked) == sorted(c[0] for c in cuts)
