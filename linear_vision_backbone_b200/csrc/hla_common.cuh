@@ -132,7 +132,7 @@ struct Part {
   int t0, len;        // its first token row, its tokens
   int nb;             // its blocks of C tokens (0: an empty sequence)
   bool first, last;   // it has the first / the last block of the (sequence, head)
-  long long slot;     // state row, or -1: the sequence is skipped
+  int slot;           // state row, or -1: the sequence is skipped
   bool start;         // the sequence starts from state_in
 };
 

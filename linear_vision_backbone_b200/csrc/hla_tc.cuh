@@ -28,16 +28,16 @@
 //
 // One block of threads per SM and 64 value columns of a head (dv = 128: two
 // blocks share a head, as a cluster when the norm needs the sum over both),
-// walking its parts' blocks of 128 tokens.  20 warps, each group one step of the
+// walking its parts' blocks of 128 tokens.  24 warps, each group one step of the
 // pipeline, joined by mbarriers:
 //   0-3   scores -> decayed, masked P (a thread has a row)
 //   4-7   the decay sums; wv terms; zeros behind the last token
-//   8-11  outputs: qs and pv joined, norm, gate, stores
-//   12-15 the state: fp32 in registers (a thread has a row of 64 columns, or a
+//   8-15  outputs: qs and pv joined, norm, gate (a thread has half a row)
+//   16-19 the state: fp32 in registers (a thread has a row of 64 columns, or a
 //         half row), S <- a S + kv, and its terms for the next block's qs
-//   16    loads of k and v (TMA, 128-byte swizzled tiles of 128 rows x 64 columns)
-//   17    issues the products
-//   18,19 loads of q; loads of z and stores of the outputs
+//   20    loads of k and v (TMA, 128-byte swizzled tiles of 128 rows x 64 columns)
+//   21    issues the products
+//   22,23 loads of q; loads of z and stores of the outputs
 // The products of a block are issued scores, kv, qs, pv: while the P warps turn
 // block c's scores around and the output warps still read block c - 1's qs and
 // pv, the tensor cores do its kv.
@@ -53,7 +53,7 @@ namespace hla {
 using tc::saddr;
 
 constexpr int kTile = kC * 128;          // 128 rows x 64 16-bit columns: 16 KB
-constexpr int kTcThreads = 20 * 32;
+constexpr int kTcThreads = 24 * 32;
 constexpr int kSumThreads = 10 * 32;
 
 struct Maps {
@@ -83,7 +83,7 @@ template <typename T, int DK, bool kSum> struct Layout {
   static constexpr int kZ = kS + (kSum ? 0 : 2 * kSTile);   // z, then the outputs over it
   static constexpr int kG = kZ + (kSum ? 0 : kNZ * kTile);         // [2][128] G
   static constexpr int kU = kG + 2 * kC * 4;          // [2][128] e^{G_b - G_j}
-  static constexpr int kX = kU + 2 * kC * 4;          // [128] the other half's sums of squares
+  static constexpr int kX = kU + 2 * kC * 4;          // [128] sums of squares on their way
   static constexpr int kMisc = kX + kC * 4;
   // misc: warp sums [2][4], maxima [4] + [4], exponents of wv [2] and S [2], tensor memory address; barriers
   static constexpr int kBars = kMisc + 96;
@@ -207,18 +207,19 @@ __device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint64_t both(float a) { return tc::f2pack(a, a); }
 
-// The registers of a thread of a warp group, out of the 96 it was launched with.
+// The registers of a thread of a warp group, out of the kLaunchRegs it was launched with.
+constexpr int kLaunchRegs = 80;    // 65536 / 768, a multiple of 8
 template <int N> __device__ __forceinline__ void set_registers() {
   static_assert(N % 8 == 0 && N >= 24 && N <= 256, "");
-  if constexpr (N > 96) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-  if constexpr (N < 96) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N > kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N < kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// Shares of the five warp groups: without spills as far as they go (the state
-// is 64 registers of a thread for dk = 128, 32 for dk = 64).
+// Shares of the six warp groups (the state is 64 registers of a thread for dk
+// = 128, 32 for dk = 64).
 template <int DK> struct Regs {
-  static constexpr int kP = DK == 128 ? 72 : 96, kBuild = kP, kOut = 96;
-  static constexpr int kState = DK == 128 ? 160 : 96, kMisc = DK == 128 ? 80 : 96;
-  static_assert(kP + kBuild + kOut + kState + kMisc <= 5 * 96, "no more than the block was launched with");
+  static constexpr int kP = DK == 128 ? 56 : 64, kBuild = kP, kOut = DK == 128 ? 88 : 96;
+  static constexpr int kState = DK == 128 ? 128 : 80, kMisc = DK == 128 ? 64 : 80;
+  static_assert(kP + kBuild + 2 * kOut + kState + kMisc <= 6 * kLaunchRegs, "no more than the block was launched with");
 };
 
 __device__ __forceinline__ void tm_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // roles: the summary has no score and output warps
   enum { kP = 0, kBuild = 1, kOut = 2, kState = 3, kLoad = 4, kMma = 5, kLoadQ = 6, kLoadZ = 7 };
-  const int role = kSum ? (warp < 4 ? kBuild : warp < 8 ? kState : warp - 4) : (warp < 16 ? warp >> 2 : warp - 12);
+  const int role = kSum ? (warp < 4 ? kBuild : warp < 8 ? kState : warp - 4) : (warp < 8 ? warp >> 2 : warp < 16 ? kOut : warp < 20 ? kState : warp - 16);
   if ((saddr(sm) & 1023u) != 0u) {
     if (tid == 0) gtr_flag(kStatusBadShape);
     return;
@@ -351,15 +352,16 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) {
       if (i < 2) { tc::mbar_init(bar + kQF + i, 1); tc::mbar_init(bar + kQE + i, 1); }
-      if (i < 2) { tc::mbar_init(bar + kZF + i, 1); tc::mbar_init(bar + kOS + i, 4); }
+      if (i < 2) { tc::mbar_init(bar + kZF + i, 1); tc::mbar_init(bar + kOS + i, 8); }
       tc::mbar_init(bar + kKF + i, 1); tc::mbar_init(bar + kKE + i, 1);
       tc::mbar_init(bar + kVF + i, 1); tc::mbar_init(bar + kVE + i, 1);
     }
     for (int b : {kScF, kPvF, kSE, kWE, kKvF}) tc::mbar_init(bar + b, 1);
-    for (int b : {kPF, kOE, kWF, kSF, kKvE}) tc::mbar_init(bar + b, 4);
+    for (int b : {kPF, kWF, kSF, kKvE}) tc::mbar_init(bar + b, 4);
+    tc::mbar_init(bar + kOE, 8);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar + kGF + i, 4);
-      tc::mbar_init(bar + kGE + i, kSum ? 4 : 12);
+      tc::mbar_init(bar + kGE + i, kSum ? 4 : 16);
     }
     tc::mbar_init(bar + kXF, kC);
     tc::mbar_init(bar + kXE, kC);
@@ -876,7 +878,11 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         it += g.nb;
       });
     } else if (role == kOut) {
+      set_registers<Regs<DK>::kOut>();
       const uint32_t rank = kPair ? blockIdx.x & 1u : 0u;
+      const int sub = warp >> 2 & 1;                             // this thread's half of the row: columns 32 sub ..
+      const uint32_t pv = tm + lane_base + kTmPV + 32 * sub, qs = tm + lane_base + kTmQS + 32 * sub;
+      const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(p.w + half * 64 + 32 * sub);
       for_parts([&](const Part& g) {
         for (int c = 0; c < g.nb && ok; ++c) {
           const uint32_t i = it + c, par = i & 1;
@@ -897,61 +903,65 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           }
           const uint64_t f11 = both(f1), f22 = both(f2);
           if (state) ++is;
-          // 8 columns of o: qs (hi + lo) and pv joined
-          auto columns = [&](int u, uint64_t (&y)[4]) {
+          // o = qs (hi + lo) and pv joined: 32 columns, two to a register pair
+          uint64_t o[16];
+          uint64_t ss2 = both(0.f);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
             uint32_t a[8], b[8], d[8];
-            tm_ld8(tm + lane_base + kTmPV + 8 * u, d);
+            tm_ld8(pv + 8 * x, d);
             if (state) {
-              tm_ld8(tm + lane_base + kTmQS + 8 * u, a);
-              tm_ld8(tm + lane_base + kTmQS + 64 + 8 * u, b);
+              tm_ld8(qs + 8 * x, a);
+              tm_ld8(qs + 64 + 8 * x, b);
               tm_wait(a);
               tm_wait(b);
             }
             tm_wait(d);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              y[e] = tc::fmul2(f22, pack2(d[2 * e], d[2 * e + 1]));
+              uint64_t y = tc::fmul2(f22, pack2(d[2 * e], d[2 * e + 1]));
               if (state)
-                y[e] = tc::ffma2(f11, add2(pack2(a[2 * e], a[2 * e + 1]), pack2(b[2 * e], b[2 * e + 1])), y[e]);
+                y = tc::ffma2(f11, add2(pack2(a[2 * e], a[2 * e + 1]), pack2(b[2 * e], b[2 * e + 1])), y);
+              o[4 * x + e] = y;
+              ss2 = tc::ffma2(y, y, ss2);
             }
-          };
-          uint8_t* Z = sm + L::kZ + sz * kTile;
-          uint64_t inv2 = both(1.f);
+          }
+          tc::tc_before_sync();
+          warp_arrive(kOE);
+          uint8_t* Z = sm + L::kZ + sz * kTile + row * 128;
+          auto unit = [&](int u) { return reinterpret_cast<uint4*>(Z + (((4 * sub + u) ^ (row & 7)) << 4)); };
           if (gated) {
-            uint64_t ss2 = both(0.f);
-#pragma unroll 2
-            for (int u = 0; u < 8; ++u) {
-              uint64_t y[4];
-              columns(u, y);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) ss2 = tc::ffma2(y[e], y[e], ss2);
-            }
             const float2 sf = tc::f2unpack(ss2);
             float ss = sf.x + sf.y;
-            if constexpr (kPair) {
-              // the other half's sum of this row; its copy of ours is free once it has read the block before
-              ok = cluster_wait(bar + kXE, par ^ 1);
-              if (!ok) break;
-              peer_store(peer_addr(saddr(Xs + row), rank ^ 1u), ss);
-              peer_arrive(peer_addr(saddr(bar + kXF), rank ^ 1u));
-              ok = cluster_wait(bar + kXF, par);
-              if (!ok) break;
-              ss += *reinterpret_cast<volatile float*>(Xs + row);
-              peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));
+            // Xs[row] carries the second thread's sum to the first, then (a pair)
+            // the other block's to this one, then the total to the second thread
+            volatile float* X = Xs + row;
+            if (sub == 1) *X = ss;
+            tc::named_barrier(3, 256);
+            if (sub == 0) {
+              ss += *X;
+              if constexpr (kPair) {
+                peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));   // the other may write here
+                ok = cluster_wait(bar + kXE, par);
+                if (ok) {
+                  peer_store(peer_addr(saddr(Xs + row), rank ^ 1u), ss);
+                  peer_arrive(peer_addr(saddr(bar + kXF), rank ^ 1u));
+                  ok = cluster_wait(bar + kXF, par);
+                }
+                ss += *X;
+              }
+              *X = ss;
             }
-            inv2 = both(rsqrtf(ss / (float)p.dv + kRmsEps));
-          }
-          const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(p.w + half * 64);
-#pragma unroll 2
-          for (int u = 0; u < 8; ++u) {
-            uint4* unit16 = reinterpret_cast<uint4*>(Z + row * 128 + ((u ^ (row & 7)) << 4));
-            uint64_t y[4];
-            if (gated) {
+            tc::named_barrier(3, 256);
+            ss = *X;
+            const uint64_t inv2 = both(rsqrtf(ss / (float)p.dv + kRmsEps));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
               ulonglong2 wa = make_ulonglong2(both(1.f), both(1.f)), wb = wa;
               if (p.w) { wa = __ldg(wp + 2 * u); wb = __ldg(wp + 2 * u + 1); }
-              const uint4 zu = *unit16;
+              const uint4 zu = *unit(u);
               const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
-              columns(u, y);
+              uint64_t* y = o + 4 * u;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 // z sigmoid(z) = z / (1 + 2^(-z log2 e))
@@ -962,22 +972,22 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
               }
               y[0] = tc::fmul2(y[0], wa.x); y[1] = tc::fmul2(y[1], wa.y);
               y[2] = tc::fmul2(y[2], wb.x); y[3] = tc::fmul2(y[3], wb.y);
-            } else {
-              columns(u, y);
             }
-            *unit16 = make_uint4(narrow<T>(y[0]), narrow<T>(y[1]), narrow<T>(y[2]), narrow<T>(y[3]));
           }
-          tc::tc_before_sync();
-          warp_arrive(kOE);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            *unit(u) = make_uint4(narrow<T>(o[4 * u]), narrow<T>(o[4 * u + 1]), narrow<T>(o[4 * u + 2]),
+                                  narrow<T>(o[4 * u + 3]));
           if (nv < kC) {
             // behind the sequence's last token the rows are not ours: copied row by row
-            tc::named_barrier(3, 128);
-            const int u = row & 7;
+            tc::named_barrier(3, 256);
+            const int t = sub * 128 + row, u = t & 7;
             T* dst = (T*)p.out + (long long)(g.t0 + c * kC) * p.ldo + (long long)g.h * p.dv + half * 64 + u * 8;
+            const uint8_t* tile = sm + L::kZ + sz * kTile;
 #pragma unroll 1
-            for (int r = row >> 3; r < nv; r += 16)
+            for (int r = t >> 3; r < nv; r += 32)
               *reinterpret_cast<uint4*>(dst + r * p.ldo) =
-                  *reinterpret_cast<const uint4*>(Z + r * 128 + ((u ^ (r & 7)) << 4));
+                  *reinterpret_cast<const uint4*>(tile + r * 128 + ((u ^ (r & 7)) << 4));
           }
           tc::fence_async_smem();                               // for the copy engine: the stores, and the next z
           warp_arrive(kOS + sz);
