@@ -22,7 +22,7 @@
 //   pv      = P hi v + P lo v   M 128, N 64, K 128, P in tensor memory
 // Two bf16 terms carry 16 significant bits, so an output is off by about 2^-17
 // of its terms before its own rounding (one term would cost as much as that
-// rounding again); the state, which is returned in fp32, takes three.  fp16
+// rounding again); a state that is returned, in fp32, takes three.  fp16
 // terms are scaled by a power of two (per row of P, per block of wv, per S),
 // undone on the fp32 result, which keeps them in fp16's range: two are 22 bits.
 //
@@ -60,12 +60,6 @@ struct Maps {
   CUtensorMap q, k, v, z, o;
 };
 
-// mbarriers of a block of threads, in 8-byte units
-enum Bars {
-  kQF = 0, kQE = 2, kKF = 4, kKE = 7, kVF = 10, kVE = 13, kZF = 16, kOS = 18, kScF = 20, kPF = 21, kPvF = 22, kOE = 23,
-  kSF = 24, kSE = 25, kWF = 26, kWE = 27, kKvF = 28, kKvE = 29, kGF = 30, kGE = 32, kXF = 34, kXE = 35, kNumBars = 36
-};
-
 template <typename T, int DK, bool kSum> struct Layout {
   static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   static constexpr int kTerms = kBf16 ? 3 : 2;       // of wv
@@ -83,12 +77,20 @@ template <typename T, int DK, bool kSum> struct Layout {
   static constexpr int kZ = kS + (kSum ? 0 : 2 * kSTile);   // z, then the outputs over it
   static constexpr int kG = kZ + (kSum ? 0 : kNZ * kTile);         // [2][128] G
   static constexpr int kU = kG + 2 * kC * 4;          // [2][128] e^{G_b - G_j}
-  static constexpr int kX = kU + 2 * kC * 4;          // [128] sums of squares on their way
-  static constexpr int kMisc = kX + kC * 4;
-  // misc: warp sums [2][4], maxima [4] + [4], exponents of wv [2] and S [2], tensor memory address; barriers
-  static constexpr int kBars = kMisc + 96;
-  static constexpr int kPExp = kBars + kNumBars * 8;  // fp16: exponents of P [2][128], one byte each
-  static constexpr int kSmem = kPExp + (kBf16 ? 0 : 2 * kC);
+  static constexpr int kX = kU + 2 * kC * 4;          // [128] the other half's sums of squares
+  static constexpr int kRms = kX + kC * 4;            // [64] the norm's weights
+  static constexpr int kMisc = kRms + 64 * 4;         // warp sums [2][4]; the tensor memory address before them
+  static constexpr int kBars = kMisc + 32;
+  // mbarriers, as indexes
+  static constexpr int kQF = 0, kQE = kQF + kNQ, kKF = kQE + kNQ, kKE = kKF + kNK, kVF = kKE + kNK, kVE = kVF + kNV;
+  static constexpr int kZF = kVE + kNV, kOS = kZF + kNZ, kScF = kOS + kNZ, kPF = kScF + 1, kPvF = kPF + 1;
+  static constexpr int kOE = kPvF + 1, kSF = kOE + 1, kSE = kSF + 1, kWF = kSE + 1, kWE = kWF + 1, kKvF = kWE + 1;
+  static constexpr int kKvE = kKvF + 1, kGF = kKvE + 1, kGE = kGF + 2, kXF = kGE + 2, kXE = kXF + 1;
+  static constexpr int kNumBars = kXE + 1;
+  // fp16 only: exponents of P [2][128], one byte each, of wv [2] and S [2]; maxima of the builders and of S [4]
+  static constexpr int kPExp = kBars + kNumBars * 8;
+  static constexpr int kExp = kPExp + (kBf16 ? 0 : 2 * kC);
+  static constexpr int kSmem = kExp + (kBf16 ? 0 : 64);
   static_assert(kSmem <= 232448, "shared memory of one block");
 };
 
@@ -283,8 +285,11 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void peer_store(uint32_t a, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+// Four bytes into the other block's shared memory, counted on its barrier as they land.
+__device__ __forceinline__ void peer_send(uint32_t a, float v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(a),
+               "r"(__float_as_uint(v)), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -334,13 +339,18 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   float* Gs = reinterpret_cast<float*>(sm + L::kG);
   float* Us = reinterpret_cast<float*>(sm + L::kU);
   float* Xs = reinterpret_cast<float*>(sm + L::kX);
+  float* rmsw = reinterpret_cast<float*>(sm + L::kRms);
   float* wsum = reinterpret_cast<float*>(sm + L::kMisc);           // [2][4]
-  float* wmax = wsum + 8;                                           // [4] builders, [4] state
-  int* ew = reinterpret_cast<int*>(wmax + 8);                       // [2] exponent of wv
-  int* es = ew + 2;                                                 // [2] exponent of S
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(es + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBars);
-  int8_t* pexp = reinterpret_cast<int8_t*>(sm + L::kPExp);          // [2][128], fp16 only
+  int8_t* pexp = reinterpret_cast<int8_t*>(sm + L::kPExp);          // fp16 only, as the next three
+  int* ew = reinterpret_cast<int*>(sm + L::kExp);
+  int* es = ew + 2;
+  float* wmax = reinterpret_cast<float*>(ew + 4);
+  constexpr int kQF = L::kQF, kQE = L::kQE, kKF = L::kKF, kKE = L::kKE, kVF = L::kVF, kVE = L::kVE, kZF = L::kZF;
+  constexpr int kOS = L::kOS, kScF = L::kScF, kPF = L::kPF, kPvF = L::kPvF, kOE = L::kOE, kSF = L::kSF, kSE = L::kSE;
+  constexpr int kWF = L::kWF, kWE = L::kWE, kKvF = L::kKvF, kKvE = L::kKvE, kGF = L::kGF, kGE = L::kGE, kXF = L::kXF;
+  constexpr int kXE = L::kXE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // roles: the summary has no score and output warps
   enum { kP = 0, kBuild = 1, kOut = 2, kState = 3, kLoad = 4, kMma = 5, kLoadQ = 6, kLoadZ = 7 };
@@ -350,21 +360,13 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) {
-      if (i < 2) { tc::mbar_init(bar + kQF + i, 1); tc::mbar_init(bar + kQE + i, 1); }
-      if (i < 2) { tc::mbar_init(bar + kZF + i, 1); tc::mbar_init(bar + kOS + i, 8); }
-      tc::mbar_init(bar + kKF + i, 1); tc::mbar_init(bar + kKE + i, 1);
-      tc::mbar_init(bar + kVF + i, 1); tc::mbar_init(bar + kVE + i, 1);
+    for (int i = 0; i < L::kNumBars; ++i) {
+      // arrivals: one (a copy's issue, a product's commit), or one of each warp of the group
+      const bool out = i == kOE || (i >= kOS && i < kOS + L::kNZ);
+      const bool four = i == kPF || i == kWF || i == kSF || i == kKvE || (i >= kGF && i < kGF + 2);
+      const bool readers = i >= kGE && i < kGE + 2;
+      tc::mbar_init(bar + i, out ? 8 : four ? 4 : readers ? (kSum ? 4 : 16) : i == kXE ? kC : 1);
     }
-    for (int b : {kScF, kPvF, kSE, kWE, kKvF}) tc::mbar_init(bar + b, 1);
-    for (int b : {kPF, kWF, kSF, kKvE}) tc::mbar_init(bar + b, 4);
-    tc::mbar_init(bar + kOE, 8);
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(bar + kGF + i, 4);
-      tc::mbar_init(bar + kGE + i, kSum ? 4 : 16);
-    }
-    tc::mbar_init(bar + kXF, kC);
-    tc::mbar_init(bar + kXE, kC);
     tc::mbar_fence_init();
   }
   if (role == kMma) {
@@ -381,6 +383,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   const int half = (int)blockIdx.x % halves, group_j = (int)blockIdx.x / halves;
   Range rg;
   locate<kC>(p, group_j, reinterpret_cast<int*>(Gs), rg);
+  if (!kSum && tid < 64) rmsw[tid] = p.w ? __ldg(p.w + half * 64 + tid) : 1.f;
   __syncthreads();                                             // the scratch becomes the decay sums
   const int w4 = warp & 3, row = w4 * 32 + lane;               // a token row, or a lane of an accumulator
   const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
@@ -446,6 +449,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       // the same in every lane; the reduction says so to the compiler
       const int nb = (int)__reduce_max_sync(0xffffffffu, (unsigned)g.nb);
       const bool want_end = wants_end(g);
+      const int terms = want_end ? L::kTerms : 2;
       for (int c = 0; c < nb && ok; ++c) {
         const uint32_t i = it + c, par = i & 1;
         const int sk = i % L::kNK, sv = i % L::kNV;
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
 #pragma unroll
           for (int s = 0; s < kC / 16; ++s)
             tc::mma_f16(tm + kTmKV, ak + s * tc::kStepMN, bw + s * tc::kStepMN, kIdKV, s > 0);
-          if (L::kTerms == 3) {
+          if (L::kTerms == 3 && terms == 3) {
             const uint64_t bw3 = tc::sdesc(saddr(W + 2 * kTile), kTile, 1024);
 #pragma unroll
             for (int s = 0; s < kC / 16; ++s)
@@ -628,7 +632,8 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             const int off = (u ^ (row & 7)) << 4;
 #pragma unroll
             for (int n = 0; n < L::kTerms; ++n)
-              *reinterpret_cast<uint4*>(W + n * kTile + off) = make_uint4(t[n][0], t[n][1], t[n][2], t[n][3]);
+              if (n < 2 || want_end)
+                *reinterpret_cast<uint4*>(W + n * kTile + off) = make_uint4(t[n][0], t[n][1], t[n][2], t[n][3]);
           }
         }
         if (nv < kC) {
@@ -882,7 +887,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       const uint32_t rank = kPair ? blockIdx.x & 1u : 0u;
       const int sub = warp >> 2 & 1;                             // this thread's half of the row: columns 32 sub ..
       const uint32_t pv = tm + lane_base + kTmPV + 32 * sub, qs = tm + lane_base + kTmQS + 32 * sub;
-      const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(p.w + half * 64 + 32 * sub);
+      const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(rmsw + 32 * sub);
       for_parts([&](const Part& g) {
         for (int c = 0; c < g.nb && ok; ++c) {
           const uint32_t i = it + c, par = i & 1;
@@ -891,7 +896,6 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           ok = wait2(kGF + (i & 1), i >> 1 & 1, kZF + sz, i / L::kNZ & 1);   // z, or the buffer alone
           if (!ok) break;
           const float Gi = Gs[(i & 1) * kC + row];
-          warp_arrive(kGE + (i & 1));
           ok = wait(kPvF, par);
           if (!ok) break;
           tc::tc_after_sync();
@@ -933,22 +937,22 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           if (gated) {
             const float2 sf = tc::f2unpack(ss2);
             float ss = sf.x + sf.y;
-            // Xs[row] carries the second thread's sum to the first, then (a pair)
-            // the other block's to this one, then the total to the second thread
-            volatile float* X = Xs + row;
+            // this row's entry of U is free (P is done): the two threads' sums meet there
+            volatile float* X = Us + (i & 1) * kC + row;
             if (sub == 1) *X = ss;
             tc::named_barrier(3, 256);
             if (sub == 0) {
               ss += *X;
               if constexpr (kPair) {
-                peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));   // the other may write here
-                ok = cluster_wait(bar + kXE, par);
+                // the other half's sum: its copy of ours is free once it has read the block before
+                if (row == 0) tc::mbar_arrive_tx(bar + kXF, kC * 4);
+                ok = cluster_wait(bar + kXE, par ^ 1);
                 if (ok) {
-                  peer_store(peer_addr(saddr(Xs + row), rank ^ 1u), ss);
-                  peer_arrive(peer_addr(saddr(bar + kXF), rank ^ 1u));
+                  peer_send(peer_addr(saddr(Xs + row), rank ^ 1u), ss, peer_addr(saddr(bar + kXF), rank ^ 1u));
                   ok = cluster_wait(bar + kXF, par);
                 }
-                ss += *X;
+                ss += *reinterpret_cast<volatile float*>(Xs + row);
+                peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));
               }
               *X = ss;
             }
@@ -957,8 +961,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             const uint64_t inv2 = both(rsqrtf(ss / (float)p.dv + kRmsEps));
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              ulonglong2 wa = make_ulonglong2(both(1.f), both(1.f)), wb = wa;
-              if (p.w) { wa = __ldg(wp + 2 * u); wb = __ldg(wp + 2 * u + 1); }
+              const ulonglong2 wa = wp[2 * u], wb = wp[2 * u + 1];
               const uint4 zu = *unit(u);
               const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
               uint64_t* y = o + 4 * u;
@@ -974,6 +977,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
               y[2] = tc::fmul2(y[2], wb.x); y[3] = tc::fmul2(y[3], wb.y);
             }
           }
+          warp_arrive(kGE + (i & 1));
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             *unit(u) = make_uint4(narrow<T>(o[4 * u]), narrow<T>(o[4 * u + 1]), narrow<T>(o[4 * u + 2]),
