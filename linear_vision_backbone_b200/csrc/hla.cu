@@ -41,7 +41,7 @@ bool tc_shape(int dk, int dv, int dtype) { return dtype != GTR_F32 && dk >= 64 &
 // How the work is split (hla_common.cuh) and the workspace that takes.
 struct Plan {
   int J, cut;
-  size_t off_0, off_a, bytes; // workspace: summaries, initial states, log-decays
+  size_t off_0, off_c, off_a, bytes; // workspace: summaries, initial states, chains, log-decays
 };
 
 // `slots` groups can run at once.  Cutting spreads a long sequence evenly over
@@ -68,7 +68,8 @@ void make_plan(int nseq, int T, int H, int dk, int dv, int dtype, bool equal, in
   p->J = (int)J;
   const size_t state = (size_t)dk * dv * sizeof(float);
   p->off_0 = p->cut ? J * state : 0;
-  p->off_a = 2 * p->off_0;
+  p->off_c = 2 * p->off_0;
+  p->off_a = p->off_c + (p->cut ? J * sizeof(hla::Chain) : 0);
   p->bytes = p->off_a + (p->cut ? J * sizeof(float) : 0);
 }
 
@@ -226,7 +227,7 @@ int check_args(const gtr_hla_args* a, bool step, hla::Params* p, bool* empty) {
     if (x < y + n && y < x + n) return GTR_ERR_INVALID_ARG;
   }
   *p = hla::Params{a->q, a->k, a->v, a->g, a->outgate, a->rms_w, a->out, a->state_in, a->state_out, a->slots, a->seen,
-                   a->cu_seqlens, nullptr, nullptr, nullptr, ld[0], ld[1], ld[2], ld[3], ld[4], a->nseq, a->T, a->Hk, a->H,
+                   a->cu_seqlens, nullptr, nullptr, nullptr, nullptr, ld[0], ld[1], ld[2], ld[3], ld[4], a->nseq, a->T, a->Hk, a->H,
                    a->dk, a->dv, a->nslots, a->g_per_head != 0, a->scale, 0, 0};
   *empty = false;
   return GTR_OK;
@@ -277,6 +278,7 @@ GTR_API gtr_status_t gtr_hla_fwd(const gtr_hla_args* args, void* stream) {
   p.wsS = (float*)args->workspace;
   p.ws0 = (float*)((char*)args->workspace + pl.off_0);
   p.wsA = (float*)((char*)args->workspace + pl.off_a);
+  p.chains = (hla::Chain*)((char*)args->workspace + pl.off_c);
   const cudaStream_t st = (cudaStream_t)stream;
   // an empty call (T = 0) only copies states: no tensor to map
   const bool tc = tc_shape(p.dk, p.dv, args->dtype) && p.T > 0;
@@ -292,9 +294,8 @@ GTR_API gtr_status_t gtr_hla_fwd(const gtr_hla_args* args, void* stream) {
   };
   if (pl.cut) {
     if (launch(true)) return GTR_ERR_CUDA;
-    const dim3 grid((unsigned)p.J, (unsigned)((p.dk * p.dv / 4 + hla::kScanThreads - 1) / hla::kScanThreads));
-    const auto scan = tc ? hla::hla_scan<hla::kC> : hla::hla_scan<hla::kSimtBatch>;
-    if (launch_pdl(scan, grid, dim3(hla::kScanThreads), 0, st, p)) return GTR_ERR_CUDA;
+    const dim3 grid((unsigned)p.J, (unsigned)((p.dk * p.dv + hla::kScanThreads - 1) / hla::kScanThreads));
+    if (launch_pdl(hla::hla_scan, grid, dim3(hla::kScanThreads), 0, st, p)) return GTR_ERR_CUDA;
   }
   return launch(false) ? GTR_ERR_CUDA : GTR_OK;
 }

@@ -25,12 +25,20 @@ constexpr int kC = 128;            // tokens per block of the tensor-core kernel
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLog = -110.0f; // e^-110 is zero in fp32
 
+// The cuts of a (sequence, head), at the group with its first block: the
+// summaries from there on (0: no such cut), the head, the state row, and
+// whether it starts from state_in.
+struct Chain {
+  int m, h, slot, start;
+};
+
 struct Params {
   const void* q; const void* k; const void* v; const float* g; const void* z; const float* w; void* out;
   const float* state_in; float* state_out; const int* slots; const int* seen; const int* cu;
   float* wsS;                      // [J][dk][dv]: summaries, then start states of the next group
   float* ws0;                      // [J][dk][dv]: initial states of cut (sequence, head)s, by their first group
   float* wsA;                      // [J]: the summaries' log2-decays
+  Chain* chains;                   // [J]
   long long ldq, ldk, ldv, ldz, ldo;
   int nseq, T, Hk, H, dk, dv, nslots, g_per_head;
   float scale;
@@ -220,55 +228,54 @@ __device__ __forceinline__ float load_decay(const Params& p, int t, int h) {
   return log2_decay(__ldg(p.g + (p.g_per_head ? (size_t)h : (size_t)t * p.H + h)));
 }
 
+// The chain that starts at group j with cut part g.
+template <int C> __device__ __forceinline__ Chain chain_of(const Params& p, const Range& rg, const Part& g, int j) {
+  if (!g.first) return Chain{0, 0, 0, 0};
+  // the summaries of this (sequence, head): of the groups that end before its blocks do
+  int r, m = 1;
+  const int end = rg.x1 - g.nb + n_blocks(seq_rows<C>(p, g.n, r), C);   // the unit behind them
+  while (j + m < rg.J && rg.start(j + m + 1) < end) ++m;
+  return Chain{m, g.h, g.slot, g.start};
+}
+
 // ---------------------------------------------------------------------------
 // The states groups start from.  The group with the first block of a cut
 // (sequence, head) walks its cuts: S = the initial state (copied to ws0), then
 // entry i becomes S = e^{decay of part i} S + summary of part i.  One thread
-// per four state elements; grid (J, dk dv / 4 / 128), most blocks have no such
-// cut and end at once.
+// per state element and up to kScanAhead parts' loads in flight together, so
+// that a chain costs about one memory latency; grid (J, dk dv / 128), blocks of
+// groups where no chain starts end at once.
 constexpr int kScanThreads = 128;
-constexpr int kScanAhead = 12;     // parts whose loads are in flight together
+constexpr int kScanAhead = 24;
 
-template <int C> __global__ void __launch_bounds__(kScanThreads) hla_scan(const Params p) {
-  __shared__ int scratch[40];
+__global__ void __launch_bounds__(kScanThreads) hla_scan(const Params p) {
   pdl_wait();
   pdl_trigger();
   const int j = blockIdx.x;
-  Range rg;
-  locate<C>(p, j, scratch, rg);
-  Part g;
-  if (!cut_part<C>(p, rg, g) || !g.first) return;
-  // the summaries of this (sequence, head): of the groups that end before it does
-  int r;
-  const int end = rg.x1 - g.nb + n_blocks(seq_rows<C>(p, g.n, r), C);   // the unit behind its blocks
-  int m = 1;
-  while (j + m < rg.J && rg.start(j + m + 1) < end) ++m;
-  const int per_state = p.dk * p.dv;
-  const int e = (blockIdx.y * kScanThreads + threadIdx.x) * 4;
+  const Chain ch = p.chains[j];
+  if (ch.m == 0) return;
+  const int per_state = p.dk * p.dv, e = blockIdx.y * kScanThreads + threadIdx.x;
   if (e >= per_state) return;
-  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (g.start) {
-    S = *reinterpret_cast<const float4*>(p.state_in + ((size_t)g.slot * p.H + g.h) * per_state + e);
-    *reinterpret_cast<float4*>(p.ws0 + (size_t)j * per_state + e) = S;
-  }
   float* ws = p.wsS + (size_t)j * per_state + e;
   const float* wa = p.wsA + j;
-  for (int i0 = 0; i0 < m; i0 += kScanAhead) {
-    float4 d[kScanAhead];
-    float l[kScanAhead];
+  float S = 0.f;
+  for (int i0 = 0; i0 < ch.m; i0 += kScanAhead) {
+    float d[kScanAhead], l[kScanAhead];
 #pragma unroll
     for (int u = 0; u < kScanAhead; ++u)
-      if (i0 + u < m) {
-        d[u] = *reinterpret_cast<const float4*>(ws + (size_t)(i0 + u) * per_state);
+      if (i0 + u < ch.m) {
+        d[u] = ws[(size_t)(i0 + u) * per_state];
         l[u] = wa[i0 + u];
       }
+    if (i0 == 0 && ch.start) {
+      S = p.state_in[((size_t)ch.slot * p.H + ch.h) * per_state + e];
+      p.ws0[(size_t)j * per_state + e] = S;
+    }
 #pragma unroll
     for (int u = 0; u < kScanAhead; ++u)
-      if (i0 + u < m) {
-        const float f = exp2f(l[u]);
-        S.x = fmaf(f, S.x, d[u].x); S.y = fmaf(f, S.y, d[u].y);
-        S.z = fmaf(f, S.z, d[u].z); S.w = fmaf(f, S.w, d[u].w);
-        *reinterpret_cast<float4*>(ws + (size_t)(i0 + u) * per_state) = S;
+      if (i0 + u < ch.m) {
+        S = fmaf(exp2f(l[u]), S, d[u]);
+        ws[(size_t)(i0 + u) * per_state] = S;
       }
   }
 }

@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
   Part g;
   const int tid = threadIdx.x, j = tid % dv, r0 = tid / dv * ROWS;
   const size_t hs = (size_t)dk * dv;
+  if (kSum && threadIdx.x == 0 && !cut_part<kSimtBatch>(p, rg, g)) p.chains[blockIdx.x] = Chain{0, 0, 0, 0};
   while (kSum ? cut_part<kSimtBatch>(p, rg, g) : next_part<kSimtBatch>(p, walk, g)) {
     const int h = g.h, hk = h / (p.H / p.Hk);
     float S[ROWS];
@@ -113,7 +114,10 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
       float* dst = p.wsS + (size_t)blockIdx.x * hs;
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) dst[(size_t)(r0 + r) * dv + j] = S[r];
-      if (tid == 0) p.wsA[blockIdx.x] = total;
+      if (tid == 0) {
+        p.wsA[blockIdx.x] = total;
+        p.chains[blockIdx.x] = chain_of<kSimtBatch>(p, rg, g, blockIdx.x);
+      }
       return;
     }
     if (g.last && p.state_out) {

@@ -54,7 +54,7 @@ using tc::saddr;
 
 constexpr int kTile = kC * 128;          // 128 rows x 64 16-bit columns: 16 KB
 constexpr int kTcThreads = 24 * 32;
-constexpr int kSumThreads = 10 * 32;
+constexpr int kSumThreads = 14 * 32;
 
 struct Maps {
   CUtensorMap q, k, v, z, o;
@@ -65,14 +65,16 @@ template <typename T, int DK, bool kSum> struct Layout {
   static constexpr int kTerms = kBf16 ? 3 : 2;       // of wv
   static constexpr int kQTile = DK / 64 * kTile;
   static constexpr int kNQ = kSum ? 0 : DK == 64 ? 2 : 1;   // stages: q of the next block comes from L2 for dk = 128
-  static constexpr int kNK = kSum ? 3 : 2;
-  static constexpr int kNV = kSum ? 3 : 2;
+  static constexpr int kNK = kSum && DK == 64 ? 3 : 2;
+  static constexpr int kNV = kNK;
+  static constexpr int kNW = kSum ? 2 : 1;            // wv tiles, and kv accumulators
   static constexpr int kNZ = DK == 64 ? 2 : 1;
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + kNQ * kQTile;
   static constexpr int kV = kK + kNK * kQTile;
   static constexpr int kW = kV + kNV * kTile;
-  static constexpr int kS = kW + kTerms * kTile;      // S hi, S lo: dk rows x 64 columns each
+  static constexpr int kWTile = kTerms * kTile;
+  static constexpr int kS = kW + kNW * kWTile;        // S hi, S lo: dk rows x 64 columns each
   static constexpr int kSTile = DK * 128;
   static constexpr int kZ = kS + (kSum ? 0 : 2 * kSTile);   // z, then the outputs over it
   static constexpr int kG = kZ + (kSum ? 0 : kNZ * kTile);         // [2][128] G
@@ -84,13 +86,13 @@ template <typename T, int DK, bool kSum> struct Layout {
   // mbarriers, as indexes
   static constexpr int kQF = 0, kQE = kQF + kNQ, kKF = kQE + kNQ, kKE = kKF + kNK, kVF = kKE + kNK, kVE = kVF + kNV;
   static constexpr int kZF = kVE + kNV, kOS = kZF + kNZ, kScF = kOS + kNZ, kPF = kScF + 1, kPvF = kPF + 1;
-  static constexpr int kOE = kPvF + 1, kSF = kOE + 1, kSE = kSF + 1, kWF = kSE + 1, kWE = kWF + 1, kKvF = kWE + 1;
-  static constexpr int kKvE = kKvF + 1, kGF = kKvE + 1, kGE = kGF + 2, kXF = kGE + 2, kXE = kXF + 1;
+  static constexpr int kOE = kPvF + 1, kSF = kOE + 1, kSE = kSF + 1, kWF = kSE + 1, kWE = kWF + kNW;
+  static constexpr int kKvF = kWE + kNW, kKvE = kKvF + kNW, kGF = kKvE + kNW, kGE = kGF + 2, kXF = kGE + 2, kXE = kXF + 1;
   static constexpr int kNumBars = kXE + 1;
-  // fp16 only: exponents of P [2][128], one byte each, of wv [2] and S [2]; maxima of the builders and of S [4]
+  // fp16 only: exponents of P [2][128], one byte each, of wv [4] and S [2]; maxima of the builders [8] and of S [4]
   static constexpr int kPExp = kBars + kNumBars * 8;
   static constexpr int kExp = kPExp + (kBf16 ? 0 : 2 * kC);
-  static constexpr int kSmem = kExp + (kBf16 ? 0 : 64);
+  static constexpr int kSmem = kExp + (kBf16 ? 0 : 72);
   static_assert(kSmem <= 232448, "shared memory of one block");
 };
 
@@ -345,8 +347,8 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBars);
   int8_t* pexp = reinterpret_cast<int8_t*>(sm + L::kPExp);          // fp16 only, as the next three
   int* ew = reinterpret_cast<int*>(sm + L::kExp);
-  int* es = ew + 2;
-  float* wmax = reinterpret_cast<float*>(ew + 4);
+  int* es = ew + 4;
+  float* wmax = reinterpret_cast<float*>(ew + 6);                   // [8] builders, [4] state
   constexpr int kQF = L::kQF, kQE = L::kQE, kKF = L::kKF, kKE = L::kKE, kVF = L::kVF, kVE = L::kVE, kZF = L::kZF;
   constexpr int kOS = L::kOS, kScF = L::kScF, kPF = L::kPF, kPvF = L::kPvF, kOE = L::kOE, kSF = L::kSF, kSE = L::kSE;
   constexpr int kWF = L::kWF, kWE = L::kWE, kKvF = L::kKvF, kKvE = L::kKvE, kGF = L::kGF, kGE = L::kGE, kXF = L::kXF;
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // roles: the summary has no score and output warps
   enum { kP = 0, kBuild = 1, kOut = 2, kState = 3, kLoad = 4, kMma = 5, kLoadQ = 6, kLoadZ = 7 };
-  const int role = kSum ? (warp < 4 ? kBuild : warp < 8 ? kState : warp - 4) : (warp < 8 ? warp >> 2 : warp < 16 ? kOut : warp < 20 ? kState : warp - 16);
+  const int role = kSum ? (warp < 8 ? kBuild : warp < 12 ? kState : warp - 8) : (warp < 8 ? warp >> 2 : warp < 16 ? kOut : warp < 20 ? kState : warp - 16);
   if ((saddr(sm) & 1023u) != 0u) {
     if (tid == 0) gtr_flag(kStatusBadShape);
     return;
@@ -363,9 +365,11 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     for (int i = 0; i < L::kNumBars; ++i) {
       // arrivals: one (a copy's issue, a product's commit), or one of each warp of the group
       const bool out = i == kOE || (i >= kOS && i < kOS + L::kNZ);
-      const bool four = i == kPF || i == kWF || i == kSF || i == kKvE || (i >= kGF && i < kGF + 2);
+      const bool four = i == kPF || (i >= kWF && i < kWF + L::kNW) || i == kSF || (i >= kKvE && i < kKvE + L::kNW) ||
+                        (i >= kGF && i < kGF + 2);
       const bool readers = i >= kGE && i < kGE + 2;
-      tc::mbar_init(bar + i, out ? 8 : four ? 4 : readers ? (kSum ? 4 : 16) : i == kXE ? kC : 1);
+      const bool wf = i >= kWF && i < kWF + L::kNW;
+      tc::mbar_init(bar + i, out || (kSum && wf) ? 8 : four ? 4 : readers ? (kSum ? 4 : 16) : i == kXE ? kC : 1);
     }
     tc::mbar_fence_init();
   }
@@ -412,6 +416,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       while (ok && next_part<kC>(p, walk, g)) body(g);
     }
   };
+  if (kSum && tid == 0 && half == 0 && group_j < p.J) {
+    Part g;
+    if (!cut_part<kC>(p, rg, g)) p.chains[group_j] = Chain{0, 0, 0, 0};
+  }
   // the state after the part is needed / there is one before it
   auto wants_end = [&](const Part& g) { return kSum || (g.last && p.state_out); };
   auto has_start = [&](const Part& g) { return !kSum && (!g.first || g.start); };
@@ -455,7 +463,9 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         const int sk = i % L::kNK, sv = i % L::kNV;
         const uint8_t* K = sm + L::kK + sk * L::kQTile;
         const uint8_t* V = sm + L::kV + sv * kTile;
-        const uint8_t* W = sm + L::kW;
+        const int sw = i % L::kNW;                               // wv tile and kv accumulator
+        const uint32_t pw = i / L::kNW & 1, kv = tm + kTmKV - 128 * sw;
+        const uint8_t* W = sm + L::kW + sw * L::kWTile;
         if constexpr (!kSum) {
           const int sq = i % L::kNQ;
           const uint8_t* Q = sm + L::kQ + sq * L::kQTile;
@@ -475,24 +485,24 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         } else {
           ok = wait(kKF + sk, i / L::kNK & 1);
         }
-        ok = ok && wait2(kWF, par, kKvE, par ^ 1);
+        ok = ok && wait2(kWF + sw, pw, kKvE + sw, pw ^ 1);
         if (!ok) break;
         tc::tc_after_sync();
         if ((c + 1 < nb || want_end) && lead) {
           const uint64_t ak = tc::sdesc(saddr(K), kTile, 1024), bw = tc::sdesc(saddr(W), kTile, 1024);
 #pragma unroll
           for (int s = 0; s < kC / 16; ++s)
-            tc::mma_f16(tm + kTmKV, ak + s * tc::kStepMN, bw + s * tc::kStepMN, kIdKV, s > 0);
+            tc::mma_f16(kv, ak + s * tc::kStepMN, bw + s * tc::kStepMN, kIdKV, s > 0);
           if (L::kTerms == 3 && terms == 3) {
             const uint64_t bw3 = tc::sdesc(saddr(W + 2 * kTile), kTile, 1024);
 #pragma unroll
             for (int s = 0; s < kC / 16; ++s)
-              tc::mma_f16(tm + kTmKV + 64, ak + s * tc::kStepMN, bw3 + s * tc::kStepMN, kIdKV3, 1u);
+              tc::mma_f16(kv + 64, ak + s * tc::kStepMN, bw3 + s * tc::kStepMN, kIdKV3, 1u);
           }
         }
         if (lead) {
-          tc::mma_commit(bar + kKvF);
-          tc::mma_commit(bar + kWE);
+          tc::mma_commit(bar + kKvF + sw);
+          tc::mma_commit(bar + kWE + sw);
           tc::mma_commit(bar + kKE + sk);
         }
         __syncwarp();
@@ -544,11 +554,14 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     }
   } else if (role == kBuild) {
     if constexpr (!kSum) set_registers<Regs<DK>::kBuild>();
+    // the summary, where nothing else hides it: two threads a row
+    constexpr int kSubs = kSum ? 2 : 1, kUnits = 8 / kSubs;
+    const int sub = kSum ? warp >> 2 : 0, u0 = sub * kUnits;
     for_parts([&](const Part& g) {
       const bool want_end = wants_end(g);
       float l = row < g.len ? load_decay(p, g.t0 + row, g.h) : 0.f;
       for (int c = 0; c < g.nb && ok; ++c) {
-        const uint32_t i = it + c, par = i & 1;
+        const uint32_t i = it + c;
         const int nv = min(kC, g.len - c * kC);                  // tokens of this block
         const float lc = l;
         if (c + 1 < g.nb) {
@@ -563,10 +576,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           if (lane >= d) pre += a;
           if (lane + d < 32) suf += b;
         }
-        if (lane == 31) wsum[(i & 1) * 4 + w4] = pre;
+        if (lane == 31 && sub == 0) wsum[(i & 1) * 4 + w4] = pre;
         const float in_warp = __shfl_down_sync(0xffffffffu, suf, 1);
         suf = lane == 31 ? 0.f : in_warp;
-        tc::named_barrier(1, 128);
+        tc::named_barrier(1, 128 * kSubs);
         const float* ws = wsum + (i & 1) * 4;
         float G = pre, R = suf;
 #pragma unroll
@@ -574,11 +587,13 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           if (x < w4) G += ws[x];
           if (x > w4) R += ws[x];
         }
-        ok = wait(kGE + (i & 1), (i >> 1 & 1) ^ 1);
-        if (!ok) break;
-        Gs[(i & 1) * kC + row] = G;
-        Us[(i & 1) * kC + row] = tc::ex2(suf);
-        warp_arrive(kGF + (i & 1));
+        if (sub == 0) {
+          ok = wait(kGE + (i & 1), (i >> 1 & 1) ^ 1);
+          if (!ok) break;
+          Gs[(i & 1) * kC + row] = G;
+          Us[(i & 1) * kC + row] = tc::ex2(suf);
+          warp_arrive(kGF + (i & 1));
+        }
         const int sv = i % L::kNV, sk = i % L::kNK;
         ok = wait(kVF + sv, i / L::kNV & 1);
         if (!ok) break;
@@ -597,7 +612,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           // a power of two that brings the block's largest |w v| under 2^15
           uint32_t mx = 0;                                       // |fp16| orders as its bits, NaN on top
 #pragma unroll 2
-          for (int u = 0; u < 8; ++u) {
+          for (int u = u0; u < u0 + kUnits; ++u) {
             const uint4 v = unit(u);
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -605,20 +620,24 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           }
           const float2 f = tc::f2unpack(widen<T>(mx));
           const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(f.x, f.y) * w)));
-          if (lane == 0) wmax[w4] = m;
-          tc::named_barrier(1, 128);
-          exp_w = tc::scale_exp(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])));
+          if (lane == 0) wmax[4 * sub + w4] = m;
+          tc::named_barrier(1, 128 * kSubs);
+          float top = 0.f;
+#pragma unroll
+          for (int x = 0; x < 4 * kSubs; ++x) top = fmaxf(top, wmax[x]);
+          exp_w = tc::scale_exp(top);
           up = tc::pow2i(exp_w);
         }
-        ok = wait(kWE, par ^ 1);
+        const int sw = i % L::kNW;
+        ok = wait(kWE + sw, (i / L::kNW & 1) ^ 1);
         if (!ok) break;
         if (build) {
-          // the kv of the block before is done, so the one before that, with this slot's exponent, is read
-          if (!kBf16 && row == 0) ew[i & 1] = exp_w;
-          uint8_t* W = sm + L::kW + row * 128;
+          // the tile's last product is done; the exponent of four blocks ago, in this slot, is long read
+          if (!kBf16 && row == 0 && sub == 0) ew[i & 3] = exp_w;
+          uint8_t* W = sm + L::kW + sw * L::kWTile + row * 128;
           const uint64_t f = both(w * up);
 #pragma unroll 2
-          for (int u = 0; u < 8; ++u) {
+          for (int u = u0; u < u0 + kUnits; ++u) {
             const uint4 v = unit(u);
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
             uint32_t t[L::kTerms][4];
@@ -645,15 +664,16 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             uint8_t* K = sm + L::kK + sk * L::kQTile + row * 128;
             const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              *reinterpret_cast<uint4*>(V + (u << 4)) = zero;
+            for (int u = u0; u < u0 + kUnits; ++u) {
+              // (any unit's place in the row: all of them are zeroed, by one of the two threads)
+              *reinterpret_cast<uint4*>(V + ((u ^ (row & 7)) << 4)) = zero;
 #pragma unroll
-              for (int x = 0; x < DK / 64; ++x) *reinterpret_cast<uint4*>(K + x * kTile + (u << 4)) = zero;
+              for (int x = 0; x < DK / 64; ++x) *reinterpret_cast<uint4*>(K + x * kTile + ((u ^ (row & 7)) << 4)) = zero;
             }
           }
         }
         tc::fence_async_smem();
-        warp_arrive(kWF);
+        warp_arrive(kWF + sw);
       }
       it += g.nb;
     });
@@ -674,9 +694,9 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           mx = max(mx, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
         }
         const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, mx));
-        if (lane == 0) wmax[4 + w4] = m;
+        if (lane == 0) wmax[8 + w4] = m;
         tc::named_barrier(2, 128);
-        const int e = tc::scale_exp(fmaxf(fmaxf(wmax[4], wmax[5]), fmaxf(wmax[6], wmax[7])));
+        const int e = tc::scale_exp(fmaxf(fmaxf(wmax[8], wmax[9]), fmaxf(wmax[10], wmax[11])));
         tc::named_barrier(2, 128);                               // read before the next block's are written
         up = both(tc::pow2i(e));
         if (w4 == 0 && lane == 0) es[is & 1] = e;
@@ -737,27 +757,27 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       if (g.nb > 0 && has_start(g)) ok = put();
       float total = 0.f;
       for (int c = 0; c < g.nb && ok; ++c) {
-        const uint32_t i = it + c, par = i & 1;
-        ok = wait(kGF + (i & 1), i >> 1 & 1);
+        const uint32_t i = it + c;
+        const int sw = i % L::kNW;
+        const uint32_t kv = tm + lane_base + kTmKV - 128 * sw;
+        ok = wait2(kGF + (i & 1), i >> 1 & 1, kKvF + sw, i / L::kNW & 1);
         if (!ok) break;
         const float la = Gs[(i & 1) * kC + kC - 1];
         warp_arrive(kGE + (i & 1));
-        ok = wait(kKvF, par);
-        if (!ok) break;
         tc::tc_after_sync();
         if (c + 1 < g.nb || want_end) {
           total += la;
           const uint64_t a = both(tc::ex2(la));
-          const uint64_t down = both(kBf16 ? 1.f : tc::pow2i(-ew[i & 1]));
+          const uint64_t down = both(kBf16 ? 1.f : tc::pow2i(-ew[i & 3]));
 #pragma unroll
           for (int x = 0; x < kRuns; ++x) {
             uint32_t hi[16], lo[16];
             if constexpr (DK == 128) {
-              tm_ld16(tm + lane_base + kTmKV + 16 * x, hi);
-              tm_ld16(tm + lane_base + kTmKV + 64 + 16 * x, lo);
+              tm_ld16(kv + 16 * x, hi);
+              tm_ld16(kv + 64 + 16 * x, lo);
             } else {
-              tm_ld16x2(tm + lane_base + kTmKV + 32 * x, hi);
-              tm_ld16x2(tm + lane_base + kTmKV + 64 + 32 * x, lo);
+              tm_ld16x2(kv + 32 * x, hi);
+              tm_ld16x2(kv + 64 + 32 * x, lo);
             }
             tm_wait(hi);
             tm_wait(lo);
@@ -770,7 +790,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           }
         }
         tc::tc_before_sync();
-        warp_arrive(kKvE);
+        warp_arrive(kKvE + sw);
         if (!kSum && c + 1 < g.nb) ok = put();
       }
       it += g.nb;
@@ -783,7 +803,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             const float2 a = tc::f2unpack(S[8 * x + 2 * e]), b = tc::f2unpack(S[8 * x + 2 * e + 1]);
             *reinterpret_cast<float4*>(dst + at + SC::col(x, lane) + 4 * e) = make_float4(a.x, a.y, b.x, b.y);
           }
-        if (kSum && half == 0 && w4 == 0 && lane == 0) p.wsA[group_j] = total;
+        if (kSum && half == 0 && w4 == 0 && lane == 0) {
+          p.wsA[group_j] = total;
+          p.chains[group_j] = chain_of<kC>(p, rg, g, group_j);
+        }
       }
     });
   } else if constexpr (!kSum) {
