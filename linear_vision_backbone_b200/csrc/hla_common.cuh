@@ -224,9 +224,10 @@ __device__ __forceinline__ float log2_decay(float g) {
   g = g < kMinLog ? kMinLog : g;
   return g * kLog2e;
 }
-__device__ __forceinline__ float load_decay(const Params& p, int t, int h) {
-  return log2_decay(__ldg(p.g + (p.g_per_head ? (size_t)h : (size_t)t * p.H + h)));
+__device__ __forceinline__ float load_g(const Params& p, int t, int h) {
+  return __ldg(p.g + (p.g_per_head ? (size_t)h : (size_t)t * p.H + h));
 }
+__device__ __forceinline__ float load_decay(const Params& p, int t, int h) { return log2_decay(load_g(p, t, h)); }
 
 // The chain that starts at group j with cut part g.
 template <int C> __device__ __forceinline__ Chain chain_of(const Params& p, const Range& rg, const Part& g, int j) {

@@ -52,6 +52,7 @@ namespace hla {
 
 using tc::saddr;
 
+constexpr int kPUnroll = 2, kBuildUnroll = 2;
 constexpr int kTile = kC * 128;          // 128 rows x 64 16-bit columns: 16 KB
 constexpr int kTcThreads = 24 * 32;
 constexpr int kSumThreads = 14 * 32;
@@ -490,12 +491,12 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         tc::tc_after_sync();
         if ((c + 1 < nb || want_end) && lead) {
           const uint64_t ak = tc::sdesc(saddr(K), kTile, 1024), bw = tc::sdesc(saddr(W), kTile, 1024);
-#pragma unroll
+#pragma unroll 1
           for (int s = 0; s < kC / 16; ++s)
             tc::mma_f16(kv, ak + s * tc::kStepMN, bw + s * tc::kStepMN, kIdKV, s > 0);
           if (L::kTerms == 3 && terms == 3) {
             const uint64_t bw3 = tc::sdesc(saddr(W + 2 * kTile), kTile, 1024);
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < kC / 16; ++s)
               tc::mma_f16(kv + 64, ak + s * tc::kStepMN, bw3 + s * tc::kStepMN, kIdKV3, 1u);
           }
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           if (state) {
             const uint64_t bs = tc::sdesc(saddr(sm + L::kS), L::kSTile, 1024);
             if (lead) {
-#pragma unroll
+#pragma unroll 1
               for (int s = 0; s < DK / 16; ++s) {
                 const uint64_t o = (uint64_t)((s >> 2) * (kTile >> 4) + (s & 3) * tc::kStepK);
                 tc::mma_f16(tm + kTmQS, aq + o, bs + s * tc::kStepMN, kIdQS, s > 0);
@@ -533,10 +534,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           tc::tc_after_sync();
           const uint64_t bv = tc::sdesc(saddr(V), kTile, 1024);
           if (lead) {
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < kC / 16; ++s)
               tc::mma_f16_ts(tm + kTmPV, tm + kTmSc + 8 * s, bv + s * tc::kStepMN, kIdPV, s > 0);
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < kC / 16; ++s)
               tc::mma_f16_ts(tm + kTmPV, tm + kTmPlo + 8 * s, bv + s * tc::kStepMN, kIdPV, 1u);
             tc::mma_commit(bar + kPvF);
@@ -559,14 +560,14 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     const int sub = kSum ? warp >> 2 : 0, u0 = sub * kUnits;
     for_parts([&](const Part& g) {
       const bool want_end = wants_end(g);
-      float l = row < g.len ? load_decay(p, g.t0 + row, g.h) : 0.f;
+      float raw = row < g.len ? load_g(p, g.t0 + row, g.h) : 0.f;   // a block ahead, turned when it is used
       for (int c = 0; c < g.nb && ok; ++c) {
         const uint32_t i = it + c;
         const int nv = min(kC, g.len - c * kC);                  // tokens of this block
-        const float lc = l;
+        const float lc = log2_decay(raw);
         if (c + 1 < g.nb) {
           const int r = (c + 1) * kC + row;
-          l = r < g.len ? load_decay(p, g.t0 + r, g.h) : 0.f;
+          raw = r < g.len ? load_g(p, g.t0 + r, g.h) : 0.f;
         }
         // inclusive sums from the front, exclusive ones from the back
         float pre = lc, suf = lc;
@@ -611,7 +612,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         if (!kBf16 && build) {
           // a power of two that brings the block's largest |w v| under 2^15
           uint32_t mx = 0;                                       // |fp16| orders as its bits, NaN on top
-#pragma unroll 2
+#pragma unroll kBuildUnroll
           for (int u = u0; u < u0 + kUnits; ++u) {
             const uint4 v = unit(u);
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           if (!kBf16 && row == 0 && sub == 0) ew[i & 3] = exp_w;
           uint8_t* W = sm + L::kW + sw * L::kWTile + row * 128;
           const uint64_t f = both(w * up);
-#pragma unroll 2
+#pragma unroll kBuildUnroll
           for (int u = u0; u < u0 + kUnits; ++u) {
             const uint4 v = unit(u);
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -846,7 +847,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           }
           // runs of 16 columns; P hi goes over scores already read (columns
           // [8 b, 8 b + 8) of run b / 2)
-#pragma unroll 2
+#pragma unroll kPUnroll
           for (int b = 0; b < 2 * w4; ++b) {
             uint32_t x[16], hi[8], lo[8];
             tm_ld16(sc + 16 * b, x);
@@ -970,18 +971,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
                 // the other half's sum: its copy of ours is free once it has read the block before
                 if (row == 0) tc::mbar_arrive_tx(bar + kXF, kC * 4);
                 ok = cluster_wait(bar + kXE, par ^ 1);
-                if (ok) {
-                  peer_send(peer_addr(saddr(Xs + row), rank ^ 1u), ss, peer_addr(saddr(bar + kXF), rank ^ 1u));
-                  ok = cluster_wait(bar + kXF, par);
-                }
-                ss += *reinterpret_cast<volatile float*>(Xs + row);
-                peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));
+                if (ok) peer_send(peer_addr(saddr(Xs + row), rank ^ 1u), ss, peer_addr(saddr(bar + kXF), rank ^ 1u));
               }
-              *X = ss;
             }
-            tc::named_barrier(3, 256);
-            ss = *X;
-            const uint64_t inv2 = both(rsqrtf(ss / (float)p.dv + kRmsEps));
+            // meanwhile the weight and the gate, without the norm's factor
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const ulonglong2 wa = wp[2 * u], wb = wp[2 * u + 1];
@@ -994,11 +987,23 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
                 const uint64_t z = widen<T>(zw[e]);
                 const float2 m = tc::f2unpack(tc::fmul2(z, both(-kLog2e)));
                 const float2 q = tc::f2unpack(add2(tc::f2pack(tc::ex2(m.x), tc::ex2(m.y)), both(1.f)));
-                y[e] = tc::fmul2(tc::fmul2(y[e], inv2), tc::fmul2(z, tc::f2pack(rcp(q.x), rcp(q.y))));
+                y[e] = tc::fmul2(y[e], tc::fmul2(z, tc::f2pack(rcp(q.x), rcp(q.y))));
               }
               y[0] = tc::fmul2(y[0], wa.x); y[1] = tc::fmul2(y[1], wa.y);
               y[2] = tc::fmul2(y[2], wb.x); y[3] = tc::fmul2(y[3], wb.y);
             }
+            if (sub == 0) {
+              if constexpr (kPair) {
+                ok = ok && cluster_wait(bar + kXF, par);
+                ss += *reinterpret_cast<volatile float*>(Xs + row);
+                peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));
+              }
+              *X = rsqrtf(ss / (float)p.dv + kRmsEps);
+            }
+            tc::named_barrier(3, 256);
+            const uint64_t inv2 = both(*X);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = tc::fmul2(o[e], inv2);
           }
           warp_arrive(kGE + (i & 1));
 #pragma unroll
