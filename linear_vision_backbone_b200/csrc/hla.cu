@@ -228,7 +228,7 @@ int check_args(const gtr_hla_args* a, bool step, hla::Params* p, bool* empty) {
   }
   *p = hla::Params{a->q, a->k, a->v, a->g, a->outgate, a->rms_w, a->out, a->state_in, a->state_out, a->slots, a->seen,
                    a->cu_seqlens, nullptr, nullptr, nullptr, nullptr, ld[0], ld[1], ld[2], ld[3], ld[4], a->nseq, a->T, a->Hk, a->H,
-                   a->dk, a->dv, a->nslots, a->g_per_head != 0, a->scale, 0, 0};
+                   a->dk, a->dv, a->nslots, a->g_per_head != 0, a->T / a->nseq, a->scale, 0, 0};
   *empty = false;
   return GTR_OK;
 }

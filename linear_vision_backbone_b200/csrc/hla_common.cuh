@@ -41,6 +41,7 @@ struct Params {
   Chain* chains;                   // [J]
   long long ldq, ldk, ldv, ldz, ldo;
   int nseq, T, Hk, H, dk, dv, nslots, g_per_head;
+  int seq_len;                     // T / nseq, without cu
   float scale;
   int J, cut;
 };
@@ -52,9 +53,8 @@ template <int C> __device__ __forceinline__ int seq_rows(const Params& p, int n,
     a = min(max(__ldg(p.cu + n), 0), p.T);
     b = min(max(__ldg(p.cu + n + 1), a), p.T);
   } else {
-    const int len = p.T / p.nseq;
-    a = n * len;
-    b = a + len;
+    a = n * p.seq_len;
+    b = a + p.seq_len;
   }
   return b - a;
 }
@@ -92,7 +92,7 @@ struct Range {
 // again after the caller's next barrier.
 template <int C> __device__ __forceinline__ void locate(const Params& p, int j, int* scratch, Range& g) {
   if (!p.cu) {
-    const int nu = n_units(p.T / p.nseq, C), per = nu * p.H;
+    const int nu = n_units(p.seq_len, C), per = nu * p.H;
     g.set(per * p.nseq, p.J, j);
     const int n0 = g.x0 / per, n1 = g.x1 / per;
     g.a.set(n0, g.x0 - n0 * per, nu);
@@ -145,12 +145,13 @@ struct Part {
 };
 
 // Steps through a range of the line; every thread (or warp) of a group can
-// walk it by itself and sees the same parts.
+// walk it by itself and sees the same parts.  kFlag: of those that see a slot
+// outside the pool, the one that records it.
 struct Walk {
   Place at;
   int left;
 };
-template <int C> __device__ __forceinline__ bool next_part(const Params& p, Walk& w, Part& g) {
+template <int C, bool kFlag = false> __device__ __forceinline__ bool next_part(const Params& p, Walk& w, Part& g) {
   while (w.left > 0 && w.at.n < p.nseq) {
     int a;
     const int len = seq_rows<C>(p, w.at.n, a);
@@ -175,7 +176,7 @@ template <int C> __device__ __forceinline__ bool next_part(const Params& p, Walk
     g.nb = end - b0;
     g.slot = p.slots ? __ldg(p.slots + n) : n;
     if (g.slot >= p.nslots && (p.state_in || p.state_out)) {
-      gtr_flag(kStatusBadSlot);
+      if (kFlag) gtr_flag(kStatusBadSlot);
       g.slot = -1;
     }
     g.start = p.state_in && (!p.seen || __ldg(p.seen + n) > 0);

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
   const int tid = threadIdx.x, j = tid % dv, r0 = tid / dv * ROWS;
   const size_t hs = (size_t)dk * dv;
   if (kSum && threadIdx.x == 0 && !cut_part<kSimtBatch>(p, rg, g)) p.chains[blockIdx.x] = Chain{0, 0, 0, 0};
-  while (kSum ? cut_part<kSimtBatch>(p, rg, g) : next_part<kSimtBatch>(p, walk, g)) {
+  while (kSum ? cut_part<kSimtBatch>(p, rg, g) : next_part<kSimtBatch, true>(p, walk, g)) {
     const int h = g.h, hk = h / (p.H / p.Hk);
     float S[ROWS];
     const float* src = kSum ? nullptr : start_state(p, g, blockIdx.x);

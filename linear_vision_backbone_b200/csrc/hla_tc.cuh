@@ -297,11 +297,22 @@ __device__ __forceinline__ void peer_send(uint32_t a, float v, uint32_t bar) {
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Bounded wait that acquires what the other block of the cluster released.
+// Bounded waits, short in code (there are some 35 of them): a probe that fails
+// has slept for at most 20 us, so kProbes of them, a second or so as they are
+// seen here and 20 s at the very most, end any wait.
+constexpr uint32_t kProbes = 1u << 20;
+__device__ __forceinline__ bool probe(uint64_t* b, uint32_t parity) {
+  uint32_t n = kProbes;
+#pragma unroll 1
+  while (!tc::mbar_try(b, parity))
+    if (--n == 0) return false;
+  return true;
+}
+// The same, acquiring what the other block of the cluster released.
 __device__ __forceinline__ bool cluster_wait(uint64_t* b, uint32_t parity) {
-  const unsigned long long t0 = tc::globaltimer();
-  for (;;) {
-    uint32_t ok;
+  uint32_t n = kProbes, ok = 0;
+#pragma unroll 1
+  while (true) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
@@ -310,7 +321,7 @@ __device__ __forceinline__ bool cluster_wait(uint64_t* b, uint32_t parity) {
         : "r"(saddr(b)), "r"(parity), "r"(20000u)
         : "memory");
     if (ok) return true;
-    if (tc::globaltimer() - t0 > tc::kWaitNs) return false;
+    if (--n == 0) return false;
   }
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -397,26 +408,29 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   uint32_t it = 0;                                             // blocks of tokens since the start
   uint32_t is = 0;                                             // those that had a state before them
   bool ok = true;
-  auto wait = [&](int b, uint32_t parity) { return tc::mbar_wait(bar + b, parity); };
+  // bounded: a failed probe returns at the latest after 20 us, so kProbes of them end in any case
+  auto wait = [&](int b, uint32_t parity) { return probe(bar + b, parity); };
   // two barriers: their first probes are in flight together (a probe takes about 120 cycles)
   auto wait2 = [&](int b, uint32_t pb, int c, uint32_t pc) {
     const uint32_t x = tc::mbar_try(bar + b, pb), y = tc::mbar_try(bar + c, pc);
-    return (x || tc::mbar_wait(bar + b, pb)) && (y || tc::mbar_wait(bar + c, pc));
+    return (x || probe(bar + b, pb)) && (y || probe(bar + c, pc));
   };
   // one arrival for a warp, after all its lanes
   auto warp_arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) tc::mbar_arrive_one(bar + b);
   };
-  auto for_parts = [&](auto&& body) {
+  auto for_parts = [&](auto&& body, auto flag) {
     Part g;
     if constexpr (kSum) {
       if (cut_part<kC>(p, rg, g)) body(g);
     } else {
       Walk walk{rg.a, rg.x1 - rg.x0};
-      while (ok && next_part<kC>(p, walk, g)) body(g);
+      while (ok && next_part<kC, decltype(flag)::value>(p, walk, g)) body(g);
     }
   };
+  constexpr std::true_type kRecord{};                          // the role that records bad slots
+  constexpr std::false_type kQuiet{};
   if (kSum && tid == 0 && half == 0 && group_j < p.J) {
     Part g;
     if (!cut_part<kC>(p, rg, g)) p.chains[group_j] = Chain{0, 0, 0, 0};
@@ -447,7 +461,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       it += g.nb;
-    });
+    }, kRecord);
   } else if (role == kMma) {
     if constexpr (!kSum) set_registers<Regs<DK>::kMisc>();
     const bool lead = elect_one();
@@ -547,7 +561,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         __syncwarp();
       }
       it += nb;
-    });
+    }, kQuiet);
     if (ok && it > 0) {
       // the last arrival a product makes on this memory
       const uint32_t i = it - 1;
@@ -677,7 +691,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         warp_arrive(kWF + sw);
       }
       it += g.nb;
-    });
+    }, kQuiet);
   } else if (role == kState) {
     if constexpr (!kSum) set_registers<Regs<DK>::kState>();
     using SC = StateCols<DK>;
@@ -726,26 +740,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       warp_arrive(kSF);
       return true;
     };
-    // the row of the state a part starts from, on its way into L2 while the part before is at work
-    Walk ahead{rg.a, rg.x1 - rg.x0};
-    auto look_ahead = [&]() {
-      if constexpr (!kSum) {
-        Part n;
-        if (!p.state_in || !next_part<kC>(p, ahead, n)) return;
-        const float* src = start_state(p, n, group_j);
-        if (src) {
-          src += (size_t)r * p.dv + half * 64 + (DK == 128 ? 0 : (lane >> 4) * 32);
-          prefetch_l2(src);
-          if (DK == 128) prefetch_l2(src + 32);
-        }
-      }
-    };
-    look_ahead();                                                 // the first part itself
-    for_parts([&](const Part& g) {
+    const size_t hs = (size_t)DK * p.dv, at = (size_t)r * p.dv + half * 64;
+    auto run = [&](const Part& g) {
       const bool want_end = wants_end(g);
-      const size_t hs = (size_t)DK * p.dv, at = (size_t)r * p.dv + half * 64;
       const float* src = kSum ? nullptr : start_state(p, g, group_j);
-      look_ahead();
 #pragma unroll
       for (int x = 0; x < kRuns; ++x)
 #pragma unroll
@@ -755,43 +753,45 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           S[8 * x + 2 * e] = tc::f2pack(f.x, f.y);
           S[8 * x + 2 * e + 1] = tc::f2pack(f.z, f.w);
         }
-      if (g.nb > 0 && has_start(g)) ok = put();
       float total = 0.f;
-      for (int c = 0; c < g.nb && ok; ++c) {
-        const uint32_t i = it + c;
-        const int sw = i % L::kNW;
-        const uint32_t kv = tm + lane_base + kTmKV - 128 * sw;
-        ok = wait2(kGF + (i & 1), i >> 1 & 1, kKvF + sw, i / L::kNW & 1);
-        if (!ok) break;
-        const float la = Gs[(i & 1) * kC + kC - 1];
-        warp_arrive(kGE + (i & 1));
-        tc::tc_after_sync();
-        if (c + 1 < g.nb || want_end) {
-          total += la;
-          const uint64_t a = both(tc::ex2(la));
-          const uint64_t down = both(kBf16 ? 1.f : tc::pow2i(-ew[i & 3]));
+      // c = -1: the terms of the state before the first block
+      for (int c = has_start(g) ? -1 : 0; c < g.nb && ok; ++c) {
+        if (c >= 0) {
+          const uint32_t i = it + c;
+          const int sw = i % L::kNW;
+          const uint32_t kv = tm + lane_base + kTmKV - 128 * sw;
+          ok = wait2(kGF + (i & 1), i >> 1 & 1, kKvF + sw, i / L::kNW & 1);
+          if (!ok) break;
+          const float la = Gs[(i & 1) * kC + kC - 1];
+          warp_arrive(kGE + (i & 1));
+          tc::tc_after_sync();
+          if (c + 1 < g.nb || want_end) {
+            total += la;
+            const uint64_t a = both(tc::ex2(la));
+            const uint64_t down = both(kBf16 ? 1.f : tc::pow2i(-ew[i & 3]));
 #pragma unroll
-          for (int x = 0; x < kRuns; ++x) {
-            uint32_t hi[16], lo[16];
-            if constexpr (DK == 128) {
-              tm_ld16(kv + 16 * x, hi);
-              tm_ld16(kv + 64 + 16 * x, lo);
-            } else {
-              tm_ld16x2(kv + 32 * x, hi);
-              tm_ld16x2(kv + 64 + 32 * x, lo);
-            }
-            tm_wait(hi);
-            tm_wait(lo);
+            for (int x = 0; x < kRuns; ++x) {
+              uint32_t hi[16], lo[16];
+              if constexpr (DK == 128) {
+                tm_ld16(kv + 16 * x, hi);
+                tm_ld16(kv + 64 + 16 * x, lo);
+              } else {
+                tm_ld16x2(kv + 32 * x, hi);
+                tm_ld16x2(kv + 64 + 32 * x, lo);
+              }
+              tm_wait(hi);
+              tm_wait(lo);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              uint64_t d = add2(pack2(hi[2 * e], hi[2 * e + 1]), pack2(lo[2 * e], lo[2 * e + 1]));
-              if (!kBf16) d = tc::fmul2(d, down);
-              S[8 * x + e] = tc::ffma2(a, S[8 * x + e], d);
+              for (int e = 0; e < 8; ++e) {
+                uint64_t d = add2(pack2(hi[2 * e], hi[2 * e + 1]), pack2(lo[2 * e], lo[2 * e + 1]));
+                if (!kBf16) d = tc::fmul2(d, down);
+                S[8 * x + e] = tc::ffma2(a, S[8 * x + e], d);
+              }
             }
           }
+          tc::tc_before_sync();
+          warp_arrive(kKvE + sw);
         }
-        tc::tc_before_sync();
-        warp_arrive(kKvE + sw);
         if (!kSum && c + 1 < g.nb) ok = put();
       }
       it += g.nb;
@@ -809,7 +809,29 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           p.chains[group_j] = chain_of<kC>(p, rg, g, group_j);
         }
       }
-    });
+    };
+    if constexpr (kSum) {
+      for_parts(run, kQuiet);
+    } else {
+      // a part behind: the state the next one starts from is on its way into L2 meanwhile
+      Walk walk{rg.a, rg.x1 - rg.x0};
+      Part g, n;
+      bool have = false;
+      while (ok) {
+        const bool more = next_part<kC>(p, walk, n);
+        if (more) {
+          const float* src = start_state(p, n, group_j);
+          if (src) {
+            prefetch_l2(src + at + SC::col(0, lane));
+            if (DK == 128) prefetch_l2(src + at + 32);
+          }
+        }
+        if (have) run(g);
+        if (!more) break;
+        g = n;
+        have = true;
+      }
+    }
   } else if constexpr (!kSum) {
     if (role == kP) {
       set_registers<Regs<DK>::kP>();
@@ -905,7 +927,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           warp_arrive(kGE + (i & 1));
         }
         it += g.nb;
-      });
+      }, kQuiet);
     } else if (role == kOut) {
       set_registers<Regs<DK>::kOut>();
       const uint32_t rank = kPair ? blockIdx.x & 1u : 0u;
@@ -1025,7 +1047,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           warp_arrive(kOS + sz);
         }
         it += g.nb;
-      });
+      }, kQuiet);
     } else if (role == kLoadQ) {
       set_registers<Regs<DK>::kMisc>();
       for_parts([&](const Part& g) {
@@ -1045,7 +1067,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         it += g.nb;
-      });
+      }, kQuiet);
     } else if (role == kLoadZ) {
       // z tiles in, output tiles out: one buffer holds a block's z, then its
       // outputs; it is free once the store has read it
@@ -1083,7 +1105,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         it += g.nb;
-      });
+      }, kQuiet);
       if (lane == 0 && ok) {
 #pragma unroll
         for (int back = L::kNZ; back > 0; --back) {
