@@ -109,10 +109,10 @@ int map_rows(CUtensorMap* map, int dtype, const void* base, int T, int heads, in
   return r == CUDA_SUCCESS ? GTR_OK : GTR_ERR_CUDA;
 }
 
-template <typename T, int DK, bool kSum, bool kPair>
+template <typename T, int DK, bool kSum, bool kGated, bool kPair>
 int launch_tc_kernel(const hla::Params& p, const hla::Maps& maps, int halves, cudaStream_t st) {
   constexpr int smem = hla::Layout<T, DK, kSum>::kSmem;
-  const auto kern = hla::hla_tc<T, DK, kSum, kPair>;
+  const auto kern = hla::hla_tc<T, DK, kSum, kGated, kPair>;
   static std::atomic<bool> done[kMaxDevices];
   int dev;
   if (cudaGetDevice(&dev) != cudaSuccess) return GTR_ERR_CUDA;
@@ -138,9 +138,10 @@ int launch_tc_kernel(const hla::Params& p, const hla::Maps& maps, int halves, cu
 template <typename T, int DK>
 int launch_tc_dk(const hla::Params& p, const hla::Maps& maps, bool sum, cudaStream_t st) {
   const int halves = p.dv / 64;
-  if (sum) return launch_tc_kernel<T, DK, true, false>(p, maps, halves, st);
-  if (halves == 2 && p.z) return launch_tc_kernel<T, DK, false, true>(p, maps, halves, st);
-  return launch_tc_kernel<T, DK, false, false>(p, maps, halves, st);
+  if (sum) return launch_tc_kernel<T, DK, true, false, false>(p, maps, halves, st);
+  if (!p.z) return launch_tc_kernel<T, DK, false, false, false>(p, maps, halves, st);
+  if (halves == 2) return launch_tc_kernel<T, DK, false, true, true>(p, maps, halves, st);
+  return launch_tc_kernel<T, DK, false, true, false>(p, maps, halves, st);
 }
 int launch_tc(const hla::Params& p, const hla::Maps& maps, int dtype, bool sum, cudaStream_t st) {
   if (dtype == GTR_F16)

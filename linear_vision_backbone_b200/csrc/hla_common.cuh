@@ -6,8 +6,8 @@
 // its H heads; each (sequence, head) is a run of nb_n + 1 units, its blocks and
 // one more for what starting and ending it costs (a part of a block's time: the
 // state is read and written).  All units stand in one line, sequence by
-// sequence, head by head, and group j of J takes the blocks among the units [j B
-// / J, (j + 1) B / J) of the B = H sum (nb_n + 1).  Only the device knows the
+// sequence, head by head, and each of J groups takes an even share of the B = H
+// sum (nb_n + 1) units and the blocks among them.  Only the device knows the
 // lengths, so every kernel finds its range from cu_seqlens by itself.  With `cut` a range may end inside a (sequence,
 // head): the part before the cut then has a summary (the state it makes from
 // zero, and its decay) in workspace entry j, which the scan turns into the state
@@ -68,7 +68,7 @@ struct Place {
   // the place `off` units into sequence n of `per` units a head
   __device__ __forceinline__ void set(int seq, int off, int per) {
     n = seq;
-    h = off / per;
+    h = (unsigned)off / (unsigned)per;
     b = off - h * per;
   }
 };
@@ -78,11 +78,14 @@ struct Place {
 // into (nseq for x = B).
 struct Range {
   int B, x0, x1, J;                // B < 2^31: the host refuses more
+  int q, r;                        // B = q J + r: the first r groups have q + 1 units
   Place a, b;
-  __device__ __forceinline__ int start(int j) const { return (int)((long long)B * min(j, J) / J); }
-  __device__ __forceinline__ void set(int blocks, int groups, int j) {
-    B = blocks;
-    J = min(groups, blocks);
+  __device__ __forceinline__ int start(int j) const { return j >= J ? B : q * j + min(j, r); }
+  __device__ __forceinline__ void set(int units, int groups, int j) {
+    B = units;
+    J = min(groups, units);
+    q = (unsigned)B / (unsigned)J;
+    r = B - q * J;
     x0 = start(j);
     x1 = start(j + 1);
   }
@@ -94,13 +97,13 @@ template <int C> __device__ __forceinline__ void locate(const Params& p, int j, 
   if (!p.cu) {
     const int nu = n_units(p.seq_len, C), per = nu * p.H;
     g.set(per * p.nseq, p.J, j);
-    const int n0 = g.x0 / per, n1 = g.x1 / per;
+    const int n0 = (unsigned)g.x0 / (unsigned)per, n1 = (unsigned)g.x1 / (unsigned)per;
     g.a.set(n0, g.x0 - n0 * per, nu);
     g.b.set(n1, g.x1 - n1 * per, nu);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  const int per = (p.nseq + blockDim.x - 1) / (int)blockDim.x;   // sequences per thread, consecutive ones
+  const int per = (p.nseq + blockDim.x - 1u) / blockDim.x;       // sequences per thread, consecutive ones
   const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
   int mine = 0, r;
   for (int n = n0; n < n1; ++n) mine += n_units(seq_rows<C>(p, n, r), C);

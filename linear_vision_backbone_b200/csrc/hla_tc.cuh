@@ -52,7 +52,6 @@ namespace hla {
 
 using tc::saddr;
 
-constexpr int kPUnroll = 2, kBuildUnroll = 2;
 constexpr int kTile = kC * 128;          // 128 rows x 64 16-bit columns: 16 KB
 constexpr int kTcThreads = 24 * 32;
 constexpr int kSumThreads = 14 * 32;
@@ -341,8 +340,9 @@ template <int DK> struct StateCols {
   }
 };
 
-// kPair: the two halves of dv = 128 with a norm, as a cluster of two.
-template <typename T, int DK, bool kSum, bool kPair>
+// kGated: with the norm and the gate.  kPair: the two halves of dv = 128 with a
+// norm, as a cluster of two.
+template <typename T, int DK, bool kSum, bool kGated, bool kPair>
 __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(const Params p,
                                                                              const __grid_constant__ Maps maps,
                                                                              const int halves) {
@@ -373,16 +373,13 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     if (tid == 0) gtr_flag(kStatusBadShape);
     return;
   }
-  if (tid == 0) {
-    for (int i = 0; i < L::kNumBars; ++i) {
-      // arrivals: one (a copy's issue, a product's commit), or one of each warp of the group
-      const bool out = i == kOE || (i >= kOS && i < kOS + L::kNZ);
-      const bool four = i == kPF || (i >= kWF && i < kWF + L::kNW) || i == kSF || (i >= kKvE && i < kKvE + L::kNW) ||
-                        (i >= kGF && i < kGF + 2);
-      const bool readers = i >= kGE && i < kGE + 2;
-      const bool wf = i >= kWF && i < kWF + L::kNW;
-      tc::mbar_init(bar + i, out || (kSum && wf) ? 8 : four ? 4 : readers ? (kSum ? 4 : 16) : i == kXE ? kC : 1);
-    }
+  if (tid < L::kNumBars) {
+    // arrivals: one (a copy's issue, a product's commit), or one of each warp of the group
+    const int i = tid;
+    const bool out = i == kOE || (i >= kOS && i < kOS + L::kNZ);
+    const bool wf = i >= kWF && i < kWF + L::kNW, readers = i >= kGE && i < kGE + 2;
+    const bool four = i == kPF || wf || i == kSF || (i >= kKvE && i < kKvE + L::kNW) || (i >= kGF && i < kGF + 2);
+    tc::mbar_init(bar + i, out || (kSum && wf) ? 8 : four ? 4 : readers ? (kSum ? 4 : 16) : i == kXE ? kC : 1);
     tc::mbar_fence_init();
   }
   if (role == kMma) {
@@ -399,12 +396,17 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   const int half = (int)blockIdx.x % halves, group_j = (int)blockIdx.x / halves;
   Range rg;
   locate<kC>(p, group_j, reinterpret_cast<int*>(Gs), rg);
-  if (!kSum && tid < 64) rmsw[tid] = p.w ? __ldg(p.w + half * 64 + tid) : 1.f;
+  if (kGated && tid < 64) rmsw[tid] = p.w ? __ldg(p.w + half * 64 + tid) : 1.f;
   __syncthreads();                                             // the scratch becomes the decay sums
+  Part cut;                                                    // the summary's one part
+  bool has_cut = false;
+  if constexpr (kSum) {
+    has_cut = cut_part<kC>(p, rg, cut);
+    if (!has_cut && tid == 0 && half == 0) p.chains[group_j] = Chain{0, 0, 0, 0};
+  }
   const int w4 = warp & 3, row = w4 * 32 + lane;               // a token row, or a lane of an accumulator
   const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
   const int share = p.H / p.Hk;                                // heads of a key head
-  const bool gated = p.z != nullptr;
   uint32_t it = 0;                                             // blocks of tokens since the start
   uint32_t is = 0;                                             // those that had a state before them
   bool ok = true;
@@ -421,20 +423,16 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     if (lane == 0) tc::mbar_arrive_one(bar + b);
   };
   auto for_parts = [&](auto&& body, auto flag) {
-    Part g;
     if constexpr (kSum) {
-      if (cut_part<kC>(p, rg, g)) body(g);
+      if (has_cut) body(cut);
     } else {
+      Part g;
       Walk walk{rg.a, rg.x1 - rg.x0};
       while (ok && next_part<kC, decltype(flag)::value>(p, walk, g)) body(g);
     }
   };
   constexpr std::true_type kRecord{};                          // the role that records bad slots
   constexpr std::false_type kQuiet{};
-  if (kSum && tid == 0 && half == 0 && group_j < p.J) {
-    Part g;
-    if (!cut_part<kC>(p, rg, g)) p.chains[group_j] = Chain{0, 0, 0, 0};
-  }
   // the state after the part is needed / there is one before it
   auto wants_end = [&](const Part& g) { return kSum || (g.last && p.state_out); };
   auto has_start = [&](const Part& g) { return !kSum && (!g.first || g.start); };
@@ -626,7 +624,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         if (!kBf16 && build) {
           // a power of two that brings the block's largest |w v| under 2^15
           uint32_t mx = 0;                                       // |fp16| orders as its bits, NaN on top
-#pragma unroll kBuildUnroll
+#pragma unroll 1
           for (int u = u0; u < u0 + kUnits; ++u) {
             const uint4 v = unit(u);
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -651,7 +649,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           if (!kBf16 && row == 0 && sub == 0) ew[i & 3] = exp_w;
           uint8_t* W = sm + L::kW + sw * L::kWTile + row * 128;
           const uint64_t f = both(w * up);
-#pragma unroll kBuildUnroll
+#pragma unroll 1
           for (int u = u0; u < u0 + kUnits; ++u) {
             const uint4 v = unit(u);
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -869,7 +867,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           }
           // runs of 16 columns; P hi goes over scores already read (columns
           // [8 b, 8 b + 8) of run b / 2)
-#pragma unroll kPUnroll
+#pragma unroll 1
           for (int b = 0; b < 2 * w4; ++b) {
             uint32_t x[16], hi[8], lo[8];
             tm_ld16(sc + 16 * b, x);
@@ -980,7 +978,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           warp_arrive(kOE);
           uint8_t* Z = sm + L::kZ + sz * kTile + row * 128;
           auto unit = [&](int u) { return reinterpret_cast<uint4*>(Z + (((4 * sub + u) ^ (row & 7)) << 4)); };
-          if (gated) {
+          if constexpr (kGated) {
             const float2 sf = tc::f2unpack(ss2);
             float ss = sf.x + sf.y;
             // this row's entry of U is free (P is done): the two threads' sums meet there
@@ -1094,7 +1092,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
               if (!ok) break;
               pt[sz] = g.len - c * kC >= kC ? t : -1;
               ph[sz] = g.h;
-              if (gated) {
+              if constexpr (kGated) {
                 tc::mbar_arrive_tx(bar + kZF + sz, kTile);
                 tma_load_3d(sm + L::kZ + sz * kTile, &maps.z, half * 64, g.h, t, bar + kZF + sz);
               } else {

@@ -188,9 +188,10 @@ def _ranges(lens, H, C, groups):
         starts.append(x)
         x += (n + 1) * H
     at = lambda x: (max(i for i, s in enumerate(starts) if s <= x),)  # noqa: E731
+    start = lambda j: B if j >= J else B // J * j + min(j, B % J)  # noqa: E731
     parts, cuts = [], []
     for j in range(groups):
-        x0, x1 = B * min(j, J) // J, B * min(j + 1, J) // J
+        x0, x1 = start(j), start(j + 1)
         mine, x = [], x0
         while x < x1:
             n, = at(x)
@@ -209,7 +210,7 @@ def _ranges(lens, H, C, groups):
                 m = 0
                 if b0 == 0:                          # the scan's walk from here
                     end, m = x1 - e + nb[n], 1
-                    while j + m < J and B * min(j + m + 1, J) // J < end:
+                    while j + m < J and start(j + m + 1) < end:
                         m += 1
                 cuts.append((j, n, h, b0, e - b0, m))
     return nb, J, parts, cuts
