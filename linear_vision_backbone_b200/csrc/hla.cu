@@ -295,7 +295,7 @@ GTR_API gtr_status_t gtr_hla_fwd(const gtr_hla_args* args, void* stream) {
   };
   if (pl.cut) {
     if (launch(true)) return GTR_ERR_CUDA;
-    const dim3 grid((unsigned)p.J, (unsigned)((p.dk * p.dv + hla::kScanThreads - 1) / hla::kScanThreads));
+    const dim3 grid((unsigned)p.J, (unsigned)((p.dk * p.dv / 4 + hla::kScanThreads - 1) / hla::kScanThreads));
     if (launch_pdl(hla::hla_scan, grid, dim3(hla::kScanThreads), 0, st, p)) return GTR_ERR_CUDA;
   }
   return launch(false) ? GTR_ERR_CUDA : GTR_OK;

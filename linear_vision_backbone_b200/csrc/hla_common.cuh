@@ -228,8 +228,11 @@ __device__ __forceinline__ float log2_decay(float g) {
   g = g < kMinLog ? kMinLog : g;
   return g * kLog2e;
 }
+// Issued where it stands (a plain load may sink to its use, behind the wait it was to cover).
 __device__ __forceinline__ float load_g(const Params& p, int t, int h) {
-  return __ldg(p.g + (p.g_per_head ? (size_t)h : (size_t)t * p.H + h));
+  float x;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(p.g + (p.g_per_head ? (size_t)h : (size_t)t * p.H + h)));
+  return x;
 }
 __device__ __forceinline__ float load_decay(const Params& p, int t, int h) { return log2_decay(load_g(p, t, h)); }
 
@@ -247,11 +250,13 @@ template <int C> __device__ __forceinline__ Chain chain_of(const Params& p, cons
 // The states groups start from.  The group with the first block of a cut
 // (sequence, head) walks its cuts: S = the initial state (copied to ws0), then
 // entry i becomes S = e^{decay of part i} S + summary of part i.  One thread
-// per state element and up to kScanAhead parts' loads in flight together, so
-// that a chain costs about one memory latency; grid (J, dk dv / 128), blocks of
-// groups where no chain starts end at once.
-constexpr int kScanThreads = 128;
-constexpr int kScanAhead = 24;
+// per four state elements and up to kScanAhead parts' loads in flight together.
+// Bound by latency: a chain is a few thousand cycles whatever its width, so the
+// grid (J, dk dv / 1024) is one wave of blocks, most of which have no chain and
+// end at once (one element a thread: four waves, 16 us where this takes 8 with
+// cold caches, dk = dv = 128, 74 groups).
+constexpr int kScanThreads = 256;
+constexpr int kScanAhead = 8;
 
 __global__ void __launch_bounds__(kScanThreads) hla_scan(const Params p) {
   pdl_wait();
@@ -259,28 +264,33 @@ __global__ void __launch_bounds__(kScanThreads) hla_scan(const Params p) {
   const int j = blockIdx.x;
   const Chain ch = p.chains[j];
   if (ch.m == 0) return;
-  const int per_state = p.dk * p.dv, e = blockIdx.y * kScanThreads + threadIdx.x;
+  const int per_state = p.dk * p.dv, e = (blockIdx.y * kScanThreads + threadIdx.x) * 4;
   if (e >= per_state) return;
   float* ws = p.wsS + (size_t)j * per_state + e;
   const float* wa = p.wsA + j;
-  float S = 0.f;
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (ch.start) {
+    S = *reinterpret_cast<const float4*>(p.state_in + ((size_t)ch.slot * p.H + ch.h) * per_state + e);
+    *reinterpret_cast<float4*>(p.ws0 + (size_t)j * per_state + e) = S;
+  }
+#pragma unroll 1
   for (int i0 = 0; i0 < ch.m; i0 += kScanAhead) {
-    float d[kScanAhead], l[kScanAhead];
+    const int n = min(kScanAhead, ch.m - i0);
+    float4 d[kScanAhead];
+    float l[kScanAhead];
 #pragma unroll
     for (int u = 0; u < kScanAhead; ++u)
-      if (i0 + u < ch.m) {
-        d[u] = ws[(size_t)(i0 + u) * per_state];
+      if (u < n) {
+        d[u] = *reinterpret_cast<const float4*>(ws + (size_t)(i0 + u) * per_state);
         l[u] = wa[i0 + u];
       }
-    if (i0 == 0 && ch.start) {
-      S = p.state_in[((size_t)ch.slot * p.H + ch.h) * per_state + e];
-      p.ws0[(size_t)j * per_state + e] = S;
-    }
 #pragma unroll
     for (int u = 0; u < kScanAhead; ++u)
-      if (i0 + u < ch.m) {
-        S = fmaf(exp2f(l[u]), S, d[u]);
-        ws[(size_t)(i0 + u) * per_state] = S;
+      if (u < n) {
+        const float f = exp2f(l[u]);
+        S.x = fmaf(f, S.x, d[u].x); S.y = fmaf(f, S.y, d[u].y);
+        S.z = fmaf(f, S.z, d[u].z); S.w = fmaf(f, S.w, d[u].w);
+        *reinterpret_cast<float4*>(ws + (size_t)(i0 + u) * per_state) = S;
       }
   }
 }

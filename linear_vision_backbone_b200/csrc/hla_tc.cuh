@@ -572,15 +572,13 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     const int sub = kSum ? warp >> 2 : 0, u0 = sub * kUnits;
     for_parts([&](const Part& g) {
       const bool want_end = wants_end(g);
-      float raw = row < g.len ? load_g(p, g.t0 + row, g.h) : 0.f;   // a block ahead, turned when it is used
+      // a block ahead, and turned when it is used (rows past the end read the last one)
+      float raw = g.len > 0 ? load_g(p, g.t0 + min(row, g.len - 1), g.h) : 0.f;
       for (int c = 0; c < g.nb && ok; ++c) {
         const uint32_t i = it + c;
         const int nv = min(kC, g.len - c * kC);                  // tokens of this block
-        const float lc = log2_decay(raw);
-        if (c + 1 < g.nb) {
-          const int r = (c + 1) * kC + row;
-          raw = r < g.len ? load_g(p, g.t0 + r, g.h) : 0.f;
-        }
+        const float lc = row < nv ? log2_decay(raw) : 0.f;
+        if (c + 1 < g.nb) raw = load_g(p, g.t0 + min((c + 1) * kC + row, g.len - 1), g.h);
         // inclusive sums from the front, exclusive ones from the back
         float pre = lc, suf = lc;
 #pragma unroll
@@ -1095,6 +1093,8 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
               if constexpr (kGated) {
                 tc::mbar_arrive_tx(bar + kZF + sz, kTile);
                 tma_load_3d(sm + L::kZ + sz * kTile, &maps.z, half * 64, g.h, t, bar + kZF + sz);
+                // one buffer: the next z at least from memory into L2
+                if (L::kNZ == 1 && c + 1 < g.nb) tma_prefetch_3d(&maps.z, half * 64, g.h, t + kC);
               } else {
                 tc::mbar_arrive_one(bar + kZF + sz);
               }
