@@ -2,6 +2,8 @@
 // attention: prompts token by token (every dtype and head dim), and the form
 // for single tokens.
 #pragma once
+#include <string.h>
+
 #include "hla_common.cuh"
 
 namespace gtr {
@@ -12,21 +14,73 @@ constexpr int kSimtBatch = 16;     // tokens staged in shared memory per pass
 constexpr float kLn2 = 0.6931471805599453f;
 
 __host__ __device__ inline int simt_smem_floats(int dk, int dv, bool sum) {
-  return kSimtBatch * (1 + (sum ? 1 : 2) * dk + dv + (sum ? 0 : kSimtThreads));
+  return kSimtBatch * (2 + (sum ? 1 : 2) * dk + dv + (sum ? 0 : kSimtThreads));
 }
+
+// Four consecutive elements as fp32.
+__device__ __forceinline__ float4 ld4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+template <typename T> __device__ __forceinline__ float4 ld4(const T* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  T e[4];
+  memcpy(e, &u, 8);
+  return make_float4(Elem<T>::to_f(e[0]), Elem<T>::to_f(e[1]), Elem<T>::to_f(e[2]), Elem<T>::to_f(e[3]));
+}
+
+// One batch of tokens of one head on its way from memory to shared memory:
+// thread tid has the four-element units tid, tid + 256 of each tensor's rows
+// (at most 16 x 128 elements), held in registers while the batch before is
+// computed.
+template <typename T, bool kSum> struct Batch {
+  float4 k[2], q[2], v[2];
+  float l;
+  __device__ __forceinline__ void load(const Params& p, long long t0, int n, int h, int hk, int lgk, int lgv) {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int e = (tid + x * kSimtThreads) * 4;
+      const int tk = e >> lgk, tv = e >> lgv;
+      if (tk < n) {
+        const long long off = (long long)hk * p.dk + (e & (p.dk - 1));
+        k[x] = ld4((const T*)p.k + (t0 + tk) * p.ldk + off);
+        if (!kSum) q[x] = ld4((const T*)p.q + (t0 + tk) * p.ldq + off);
+      }
+      if (tv < n) v[x] = ld4((const T*)p.v + (t0 + tv) * p.ldv + (long long)h * p.dv + (e & (p.dv - 1)));
+    }
+    if (tid < n) l = load_g(p, (int)(t0 + tid), h);
+  }
+  // as: a - 1, and a where a is not near one
+  __device__ __forceinline__ void put(float* as, float* ks, float* qs, float* vs, int n, int lgk, int lgv, float scale) {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int e = (tid + x * kSimtThreads) * 4;
+      if (e >> lgk < n) {
+        *reinterpret_cast<float4*>(ks + e) = k[x];
+        if (!kSum)
+          *reinterpret_cast<float4*>(qs + e) = make_float4(q[x].x * scale, q[x].y * scale, q[x].z * scale, q[x].w * scale);
+      }
+      if (e >> lgv < n) *reinterpret_cast<float4*>(vs + e) = v[x];
+    }
+    if (tid < n) {
+      const float x = log2_decay(l);
+      as[tid] = x;
+      as[kSimtBatch + tid] = x > -1.f ? expm1f(x * kLn2) : exp2f(x);
+    }
+  }
+};
 
 // A group's parts by the recurrence itself, the state spread over the block:
 // thread tid has column tid % dv and the ROWS rows from (tid / dv) ROWS, so a
 // warp reads a token's k and q values as broadcasts.  kSum: the summary of the
 // part before the group's cut; else the outputs, and final states.  Bound by the
 // serial chain of its tokens (two products and a sum per state element and
-// token in fp32).
+// token in fp32), so the tokens are split over many short parts.
 template <typename T, int ROWS, bool kSum>
 __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
   extern __shared__ __align__(16) float sm[];
-  const int dk = p.dk, dv = p.dv;
-  float* as = sm;                            // [batch] log-decays
-  float* ks = as + kSimtBatch;               // [batch][dk]
+  const int dk = p.dk, dv = p.dv, lgk = __ffs(dk) - 1, lgv = __ffs(dv) - 1;
+  float* as = sm;                            // [2][batch] log-decays, decays
+  float* ks = as + 2 * kSimtBatch;           // [batch][dk]
   float* qs = ks + kSimtBatch * dk;          // [batch][dk], outputs only
   float* vs = qs + (kSum ? 0 : kSimtBatch * dk);   // [batch][dv]
   float* part = vs + kSimtBatch * dv;        // [batch][threads]: partial o, outputs only
@@ -37,11 +91,13 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
   locate<kSimtBatch>(p, blockIdx.x, scratch, rg);
   Walk walk{rg.a, rg.x1 - rg.x0};
   Part g;
-  const int tid = threadIdx.x, j = tid % dv, r0 = tid / dv * ROWS;
+  const int tid = threadIdx.x, j = tid & (dv - 1), r0 = (tid >> lgv) * ROWS, groups = kSimtThreads >> lgv;
   const size_t hs = (size_t)dk * dv;
-  if (kSum && threadIdx.x == 0 && !cut_part<kSimtBatch>(p, rg, g)) p.chains[blockIdx.x] = Chain{0, 0, 0, 0};
+  if (kSum && tid == 0 && !cut_part<kSimtBatch>(p, rg, g)) p.chains[blockIdx.x] = Chain{0, 0, 0, 0};
   while (kSum ? cut_part<kSimtBatch>(p, rg, g) : next_part<kSimtBatch, true>(p, walk, g)) {
     const int h = g.h, hk = h / (p.H / p.Hk);
+    Batch<T, kSum> b;
+    b.load(p, g.t0, min(kSimtBatch, g.len), h, hk, lgk, lgv);
     float S[ROWS];
     const float* src = kSum ? nullptr : start_state(p, g, blockIdx.x);
 #pragma unroll
@@ -51,32 +107,32 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
       const int n = min(kSimtBatch, g.len - b0);
       const long long t0 = (long long)g.t0 + b0;
       __syncthreads();
-      if (tid < n) as[tid] = load_decay(p, (int)(t0 + tid), h);
-      for (int e = tid; e < n * dk; e += kSimtThreads) {
-        const int t = e / dk, i = e - t * dk;
-        ks[e] = ld_f((const T*)p.k + (t0 + t) * p.ldk + (long long)hk * dk + i);
-        if (!kSum) qs[e] = ld_f((const T*)p.q + (t0 + t) * p.ldq + (long long)hk * dk + i) * p.scale;
-      }
-      for (int e = tid; e < n * dv; e += kSimtThreads) {
-        const int t = e / dv, i = e - t * dv;
-        vs[e] = ld_f((const T*)p.v + (t0 + t) * p.ldv + (long long)h * dv + i);
-      }
+      b.put(as, ks, qs, vs, n, lgk, lgv, p.scale);
       __syncthreads();
+      if (b0 + kSimtBatch < g.len) b.load(p, t0 + kSimtBatch, min(kSimtBatch, g.len - b0 - kSimtBatch), h, hk, lgk, lgv);
+#pragma unroll 1
       for (int t = 0; t < n; ++t) {
         // S <- a S + k v as S + (a - 1) S + k v for a near one: rounding a itself
         // would be the same relative error at every token, 2^-25 a token for as
         // long as the state remembers
-        const float l = as[t], v = vs[t * dv + j];
+        const float l = as[t], a = as[kSimtBatch + t], v = vs[t * dv + j];
         const bool near_one = l > -1.f;
-        const float a = near_one ? expm1f(l * kLn2) : exp2f(l);
         total += l;
         const float* k = ks + t * dk + r0;
         const float* q = qs + t * dk + r0;
         float o = 0.f;
+        if (near_one) {
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          S[r] = fmaf(a, S[r], near_one ? fmaf(k[r], v, S[r]) : k[r] * v);
-          if (!kSum) o = fmaf(q[r], S[r], o);
+          for (int r = 0; r < ROWS; ++r) {
+            S[r] = fmaf(a, S[r], fmaf(k[r], v, S[r]));
+            if (!kSum) o = fmaf(q[r], S[r], o);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            S[r] = fmaf(a, S[r], k[r] * v);
+            if (!kSum) o = fmaf(q[r], S[r], o);
+          }
         }
         if (!kSum) part[t * kSimtThreads + tid] = o;
       }
@@ -85,26 +141,27 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
         // one warp per token: the rows' partial sums, then the norm and the gate
         const int lane = tid & 31;
         for (int t = tid >> 5; t < n; t += kSimtThreads / 32) {
-          float o[4];
+          const T* zrow = p.z ? (const T*)p.z + (t0 + t) * p.ldz + (long long)h * dv : nullptr;
+          float o[4], z[4];
           float ss = 0.f;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int col = lane + 32 * c;
             o[c] = 0.f;
+            if (zrow && col < dv) z[c] = ld_f(zrow + col);
             if (col < dv)
-              for (int r = 0; r < kSimtThreads / dv; ++r) o[c] += part[t * kSimtThreads + r * dv + col];
+              for (int r = 0; r < groups; ++r) o[c] += part[t * kSimtThreads + r * dv + col];
             ss = fmaf(o[c], o[c], ss);
           }
           float inv = 1.f;
           if (p.z) inv = rsqrtf(warp_sum(ss) / (float)dv + kRmsEps);
           T* orow = (T*)p.out + (t0 + t) * p.ldo + (long long)h * dv;
-          const T* zrow = p.z ? (const T*)p.z + (t0 + t) * p.ldz + (long long)h * dv : nullptr;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int col = lane + 32 * c;
             if (col >= dv) continue;
             float y = o[c];
-            if (zrow) y = y * inv * (p.w ? p.w[col] : 1.f) * silu_f(ld_f(zrow + col));
+            if (zrow) y = y * inv * (p.w ? p.w[col] : 1.f) * silu_f(z[c]);
             orow[col] = Elem<T>::from_f(y);
           }
         }
