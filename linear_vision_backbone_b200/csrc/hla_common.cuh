@@ -103,6 +103,27 @@ template <int C> __device__ __forceinline__ void locate(const Params& p, int j, 
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  if (p.nseq <= 32) {
+    // a lane for a sequence, every warp for itself: one load's latency and no barrier
+    int r;
+    const int nu = lane < p.nseq ? n_units(seq_rows<C>(p, lane, r), C) : 0;
+    int e = nu;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, e, d);
+      if (lane >= d) e += o;
+    }
+    g.set(__shfl_sync(0xffffffffu, e, 31) * p.H, p.J, j);
+    const int s = (e - nu) * p.H;                                // this sequence's first unit
+    auto at = [&](int x, Place& q) {
+      if (x >= g.B) { q.set(p.nseq, 0, 1); return; }
+      const int n = __popc(__ballot_sync(0xffffffffu, lane < p.nseq && s <= x)) - 1;
+      q.set(n, x - __shfl_sync(0xffffffffu, s, n), __shfl_sync(0xffffffffu, nu, n));
+    };
+    at(g.x0, g.a);
+    at(g.x1, g.b);
+    return;
+  }
   const int per = (p.nseq + blockDim.x - 1u) / blockDim.x;       // sequences per thread, consecutive ones
   const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
   int mine = 0, r;

@@ -5,12 +5,13 @@
 #include <string.h>
 
 #include "hla_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace gtr {
 namespace hla {
 
 constexpr int kSimtThreads = 256;
-constexpr int kSimtBatch = 16;     // tokens staged in shared memory per pass
+constexpr int kSimtBatch = 16;     // tokens staged in shared memory per pass: two a warp
 constexpr float kLn2 = 0.6931471805599453f;
 
 __host__ __device__ inline int simt_smem_floats(int dk, int dv, bool sum) {
@@ -93,12 +94,15 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
   Part g;
   const int tid = threadIdx.x, j = tid & (dv - 1), r0 = (tid >> lgv) * ROWS, groups = kSimtThreads >> lgv;
   const size_t hs = (size_t)dk * dv;
+  float wt[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) wt[c] = !kSum && p.w && (tid & 31) + 32 * c < dv ? __ldg(p.w + (tid & 31) + 32 * c) : 1.f;
   if (kSum && tid == 0 && !cut_part<kSimtBatch>(p, rg, g)) p.chains[blockIdx.x] = Chain{0, 0, 0, 0};
   while (kSum ? cut_part<kSimtBatch>(p, rg, g) : next_part<kSimtBatch, true>(p, walk, g)) {
     const int h = g.h, hk = h / (p.H / p.Hk);
     Batch<T, kSum> b;
     b.load(p, g.t0, min(kSimtBatch, g.len), h, hk, lgk, lgv);
-    float S[ROWS];
+    alignas(8) float S[ROWS];
     const float* src = kSum ? nullptr : start_state(p, g, blockIdx.x);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) S[r] = src ? src[(size_t)(r0 + r) * dv + j] : 0.f;
@@ -110,6 +114,19 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
       b.put(as, ks, qs, vs, n, lgk, lgv, p.scale);
       __syncthreads();
       if (b0 + kSimtBatch < g.len) b.load(p, t0 + kSimtBatch, min(kSimtBatch, g.len - b0 - kSimtBatch), h, hk, lgk, lgv);
+      // a warp finishes the outputs of tokens warp and warp + 8: their z is on its way meanwhile
+      const int lane = tid & 31, warp = tid >> 5;
+      float z[2][4];
+      if (!kSum && p.z) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int t = warp + 8 * x;
+          const T* zrow = (const T*)p.z + (t0 + t) * p.ldz + (long long)h * dv;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (t < n && lane + 32 * c < dv) z[x][c] = ld_f(zrow + lane + 32 * c);
+        }
+      }
 #pragma unroll 1
       for (int t = 0; t < n; ++t) {
         // S <- a S + k v as S + (a - 1) S + k v for a near one: rounding a itself
@@ -120,49 +137,75 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
         total += l;
         const float* k = ks + t * dk + r0;
         const float* q = qs + t * dk + r0;
-        float o = 0.f;
-        if (near_one) {
+        float sum = 0.f;
+        if constexpr (ROWS < 4) {
 #pragma unroll
           for (int r = 0; r < ROWS; ++r) {
-            S[r] = fmaf(a, S[r], fmaf(k[r], v, S[r]));
-            if (!kSum) o = fmaf(q[r], S[r], o);
+            S[r] = fmaf(a, S[r], near_one ? fmaf(k[r], v, S[r]) : k[r] * v);
+            if (!kSum) sum = fmaf(q[r], S[r], sum);
           }
         } else {
+          // two rows to an instruction; the branch is the block's
+          const uint64_t a2 = tc::f2pack(a, a), v2 = tc::f2pack(v, v);
+          uint64_t o2 = tc::f2pack(0.f, 0.f), p2 = o2;
+          uint64_t* S2 = reinterpret_cast<uint64_t*>(S);
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) {
-            S[r] = fmaf(a, S[r], k[r] * v);
-            if (!kSum) o = fmaf(q[r], S[r], o);
+          for (int r = 0; r < ROWS / 2; r += 2) {
+            const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(k + 2 * r);
+            if (near_one) {
+              S2[r] = tc::ffma2(a2, S2[r], tc::ffma2(kk.x, v2, S2[r]));
+              S2[r + 1] = tc::ffma2(a2, S2[r + 1], tc::ffma2(kk.y, v2, S2[r + 1]));
+            } else {
+              S2[r] = tc::ffma2(a2, S2[r], tc::fmul2(kk.x, v2));
+              S2[r + 1] = tc::ffma2(a2, S2[r + 1], tc::fmul2(kk.y, v2));
+            }
+            if (!kSum) {
+              const ulonglong2 qq = *reinterpret_cast<const ulonglong2*>(q + 2 * r);
+              o2 = tc::ffma2(qq.x, S2[r], o2);
+              p2 = tc::ffma2(qq.y, S2[r + 1], p2);
+            }
           }
+          const float2 x = tc::f2unpack(o2), y = tc::f2unpack(p2);
+          sum = x.x + x.y + (y.x + y.y);
         }
-        if (!kSum) part[t * kSimtThreads + tid] = o;
+        if (!kSum) {
+          part[t * kSimtThreads + tid] = sum;
+        }
       }
       if (!kSum) {
         __syncthreads();
-        // one warp per token: the rows' partial sums, then the norm and the gate
-        const int lane = tid & 31;
-        for (int t = tid >> 5; t < n; t += kSimtThreads / 32) {
-          const T* zrow = p.z ? (const T*)p.z + (t0 + t) * p.ldz + (long long)h * dv : nullptr;
-          float o[4], z[4];
+        // the rows' partial sums, then the norm and the gate
+        float o[2][4], inv[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int t = min(warp + 8 * x, n - 1);                // past the end: a row again, not stored
           float ss = 0.f;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int col = lane + 32 * c;
-            o[c] = 0.f;
-            if (zrow && col < dv) z[c] = ld_f(zrow + col);
-            if (col < dv)
-              for (int r = 0; r < groups; ++r) o[c] += part[t * kSimtThreads + r * dv + col];
-            ss = fmaf(o[c], o[c], ss);
+            o[x][c] = 0.f;
+            if (lane + 32 * c < dv) {
+              const float* row = part + t * kSimtThreads + lane + 32 * c;
+              float y[2] = {0.f, 0.f};
+              for (int r = 0; r < groups; r += 2) {              // two or more
+                y[0] += row[r * dv];
+                y[1] += row[(r + 1) * dv];
+              }
+              o[x][c] = y[0] + y[1];
+            }
+            ss = fmaf(o[x][c], o[x][c], ss);
           }
-          float inv = 1.f;
-          if (p.z) inv = rsqrtf(warp_sum(ss) / (float)dv + kRmsEps);
-          T* orow = (T*)p.out + (t0 + t) * p.ldo + (long long)h * dv;
+          inv[x] = p.z ? rsqrtf(warp_sum(ss) / (float)dv + kRmsEps) : 1.f;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int t = warp + 8 * x;
+          T* orow = (T*)p.out + (t0 + t) * p.ldo + (long long)h * dv + lane;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int col = lane + 32 * c;
-            if (col >= dv) continue;
-            float y = o[c];
-            if (zrow) y = y * inv * (p.w ? p.w[col] : 1.f) * silu_f(z[c]);
-            orow[col] = Elem<T>::from_f(y);
+            if (t >= n || lane + 32 * c >= dv) continue;
+            float y = o[x][c];
+            if (p.z) y = y * inv[x] * wt[c] * silu_f(z[x][c]);
+            orow[32 * c] = Elem<T>::from_f(y);
           }
         }
       }
