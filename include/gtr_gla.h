@@ -397,7 +397,9 @@ GTR_API gtr_status_t gtr_stack_fwd(float *x, const gtr_block_weights *blocks, in
  *   seen     device int32 [nseq] or NULL: sequence n starts from state_in only
  *            where seen[n] > 0 (the number of tokens its state has taken so
  *            far), else from zero.  NULL: every sequence does.
- *   dk, dv in {16, 32, 64, 128}; Hk divides H; T < 2^31.
+ *   dk, dv in {16, 32, 64, 128}; Hk divides H <= 65535; T < 2^31; for the
+ *   prompt form also (T / 16 + 2 nseq) H < 2^31.
+ * No element of out may be one of q, k, v, g, outgate or of a state.
  * A non-finite q, k or v element reaches only its own sequence and head, but
  * there any output of its block of 128 tokens and what follows.  States, decay
  * sums and the norm are fp32; 16-bit products carry at least 16 significant
@@ -414,7 +416,7 @@ GTR_API gtr_status_t gtr_stack_fwd(float *x, const gtr_block_weights *blocks, in
  *     into state_out, both required, and gives its output row.  Rows with a
  *     negative slot are skipped.
  * Errors: GTR_ERR_INVALID_ARG (NULL, negative or inconsistent sizes, Hk not
- * dividing H), GTR_ERR_UNSUPPORTED (head dims), GTR_ERR_ALIGNMENT (q, k, v,
+ * dividing H, overlaps), GTR_ERR_UNSUPPORTED (head dims, the limits above), GTR_ERR_ALIGNMENT (q, k, v,
  * outgate, rms_w, out, states or workspace not 16-byte aligned, or a row pitch that is
  * not a multiple of 16 bytes), GTR_ERR_NO_MEMORY (workspace too small).
  */

@@ -189,6 +189,23 @@ int launch_step(const hla::Params& p, cudaStream_t st) {
   }
 }
 
+// n rows of `width` bytes, `pitch` apart.
+struct Rows {
+  const void* p;
+  long long pitch, width, n;
+};
+// Whether two sets of rows share a byte.  Column blocks of one buffer (the same
+// pitch, each between the other's columns) do not; sets of different pitches
+// count as sharing when the ranges they span do.
+bool overlap(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || a.n < 1 || b.n < 1) return false;
+  const long long x = (long long)(uintptr_t)a.p, y = (long long)(uintptr_t)b.p;
+  if (x >= y + (b.n - 1) * b.pitch + b.width || y >= x + (a.n - 1) * a.pitch + a.width) return false;
+  if (a.pitch != b.pitch) return true;
+  const long long d = ((y - x) % a.pitch + a.pitch) % a.pitch;   // b's columns behind a's
+  return d < a.width || a.pitch - d < b.width;
+}
+
 // Checks shared by both forms; on GTR_OK with *empty false, `p` is filled but
 // for the workspace and the plan.
 int check_args(const gtr_hla_args* a, bool step, hla::Params* p, bool* empty) {
@@ -226,6 +243,19 @@ int check_args(const gtr_hla_args* a, bool step, hla::Params* p, bool* empty) {
     const uintptr_t n = (uintptr_t)a->nslots * a->H * a->dk * a->dv * sizeof(float);
     const uintptr_t x = (uintptr_t)a->state_in, y = (uintptr_t)a->state_out;
     if (x < y + n && y < x + n) return GTR_ERR_INVALID_ARG;
+  }
+  if (a->T > 0) {
+    const Rows out{a->out, ld[4] * es, (long long)a->H * a->dv * es, a->T};
+    const long long st = (long long)a->H * a->dk * a->dv * (long long)sizeof(float);
+    const Rows in[7] = {{a->q, ld[0] * es, (long long)a->Hk * a->dk * es, a->T},
+                        {a->k, ld[1] * es, (long long)a->Hk * a->dk * es, a->T},
+                        {a->v, ld[2] * es, (long long)a->H * a->dv * es, a->T},
+                        {a->outgate, ld[3] * es, (long long)a->H * a->dv * es, a->T},
+                        {a->g, a->H * 4ll, a->H * 4ll, a->g_per_head ? 1 : a->T},
+                        {a->state_in, st, st, a->nslots},
+                        {a->state_out, st, st, a->nslots}};
+    for (const Rows& r : in)
+      if (overlap(out, r)) return GTR_ERR_INVALID_ARG;
   }
   *p = hla::Params{a->q, a->k, a->v, a->g, a->outgate, a->rms_w, a->out, a->state_in, a->state_out, a->slots, a->seen,
                    a->cu_seqlens, nullptr, nullptr, nullptr, nullptr, ld[0], ld[1], ld[2], ld[3], ld[4], a->nseq, a->T, a->Hk, a->H,

@@ -161,6 +161,24 @@ def test_small_and_large_values(dtype, size):
     check(d, 2, dtype, f"size {size}")
 
 
+@pytest.mark.parametrize("dtype,dk", [("bf16", 64), ("f16", 128), ("f32", 64)])
+def test_output_between_the_inputs_columns(dtype, dk):
+    # v, out and z as column blocks of one buffer, in this order
+    d = make([150, 33], 4, 2, dk, dk, dtype, seed=31)
+    c = dev(d)
+    want = binding.hla_fwd(c["q"], c["k"], c["v"], c["g"], c["z"], c["w"], cu_seqlens=c["cu"], scale=d["scale"])
+    T = c["v"].shape[0]
+    buf = torch.full((T, 4 * dk * 3), 7.0, device="cuda", dtype=DT[dtype])
+    v, out, z = (buf[:, i * 4 * dk:(i + 1) * 4 * dk].unflatten(1, (4, dk)) for i in range(3))
+    v.copy_(c["v"])
+    z.copy_(c["z"])
+    got = binding.hla_fwd(c["q"], c["k"], v, c["g"], z, c["w"], cu_seqlens=c["cu"], scale=d["scale"], out=out)
+    assert got.data_ptr() == out.data_ptr()
+    assert torch.equal(out, want) and torch.equal(v, c["v"]) and torch.equal(z, c["z"])
+    with pytest.raises(binding.GtrError):
+        binding.hla_fwd(c["q"], c["k"], v, c["g"], z, c["w"], cu_seqlens=c["cu"], scale=d["scale"], out=z)
+
+
 @pytest.mark.parametrize("dtype,dk,dv", [("f16", 64, 64), ("bf16", 128, 128), ("f32", 64, 32)])
 def test_non_finite_rows_stay_in_their_sequence_and_head(dtype, dk, dv):
     d = make([70, 130, 60], 2, 2, dk, dv, dtype, seed=16, lead=5, tail=9, gated=False)

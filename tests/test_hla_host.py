@@ -106,6 +106,28 @@ def test_hla_fwd_rejects_invalid_arguments_before_any_launch(lib):
     assert call(T=0, q=0, k=0, v=0, g=0, out=0) == 0
 
 
+@pytest.mark.parametrize("kw", [
+    dict(q=1 << 20), dict(k=(1 << 20) + 1024 - 16), dict(v=(1 << 20) - 16), dict(outgate=1 << 20),
+    dict(g=(1 << 20) + 4), dict(state_in=(1 << 20) + 16, nslots=1),
+    dict(state_out=(1 << 20) - 65536 + 16, nslots=1),   # of 65536 bytes
+    dict(v=(1 << 20) + 256, ldv=512, ldo=512),            # columns 128 .. 383 on 0 .. 255
+    dict(v=(1 << 20) + 768, ldv=512, ldo=512),            # columns 384 .. 511 and the next row's 0 .. 127
+    dict(q=(1 << 20) + 512, ldq=256, ldo=512),            # other pitches: whole ranges count
+])
+def test_hla_output_over_an_input_is_refused(lib, kw):
+    # q, k: 2 heads, v, g, out: 4 heads, 4 tokens, bf16
+    ptrs = {n: (i + 2) << 24 for i, n in enumerate(["q", "k", "v", "g"])}
+    assert lib.gtr_hla_fwd(hla_args(**{**ptrs, "out": 1 << 20, **kw}), None) == -1
+    if "ldv" not in kw and "ldq" not in kw:               # the same for single tokens: four rows, dense
+        step = {"state_in": 1 << 27, "state_out": 1 << 27, "nslots": 4, "nseq": 4}
+        kw = {n: a for n, a in kw.items() if n != "nslots"}
+        if "state_in" in kw:
+            kw["state_out"] = kw["state_in"]
+        if "state_out" in kw:
+            kw["state_in"] = kw["state_out"]
+        assert lib.gtr_hla_step(hla_args(**{**ptrs, "out": 1 << 20, **step, **kw}), None) == -1
+
+
 def test_hla_step_rejects_invalid_arguments_before_any_launch(lib):
     def call(**kw):
         return lib.gtr_hla_step(hla_args(**dict(dict(nseq=4, state_in=1 << 20, state_out=1 << 20, nslots=4), **kw)),
