@@ -5,6 +5,7 @@
 // segments).
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "gtr_gla.h"
@@ -44,27 +45,40 @@ struct Plan {
   size_t off_0, off_c, off_a, bytes; // workspace: summaries, initial states, chains, log-decays
 };
 
-// `slots` groups can run at once.  Cutting spreads a long sequence evenly over
-// them, and costs the summaries (k and v before the cuts are read a second
-// time) and two more launches; whole (sequence, head)s need neither, but the
-// longest one bounds the time.  In units of one block of tokens of the outputs
-// kernel, a summary's block costs about kSum and the two launches kExtra.
-// With cu_seqlens the longest sequence may have all the tokens.
+// Cutting spreads a long sequence evenly over the SMs, and costs the summaries
+// (k and v before the cuts are read a second time) and two more launches; whole
+// (sequence, head)s need neither, but the longest one bounds the time.  In units
+// of one block of tokens of the outputs kernel on an SM of its own, a summary's
+// block costs about kSum and the two launches kExtra.  With cu_seqlens the
+// longest sequence may have all the tokens.  Whole and cut, gated, in us:
+//   bf16, 6 heads of 64:   1 x 256 tokens 12.4 and 17.1, 1 x 1024 28.1 and 18.2,
+//     8 x 1600 41.8 and 37.0, 24 x 1600 49 and 77
+//   bf16, 16 heads of 128: 1 x 512 24.3 and 27.9, 1 x 1024 40.1 and 32.1,
+//     8 x 1600 130 and 147
+//   fp32, 6 heads of 64:   1 x 32 11.9 and 15.3, 1 x 64 20.1 and 15.3,
+//     8 x 1600 412 and 216, 24 x 512 136 and 212
+// (over 45 such cases the choice costs 0.8 % of the better one's time with the
+// tensor cores' constants).  The CUDA-core kernel cuts for two groups per SM: 24
+// x 1600 with 4 heads of 128 takes 842 us, one group 1051, three 927, four 850;
+// with even shares rounded up, 8 x 1600 takes 313 us for 291.  Whole, an SM gains
+// nothing by a second group, and each gets a (sequence, head).
 void make_plan(int nseq, int T, int H, int dk, int dv, int dtype, bool equal, int sms, Plan* p) {
-  constexpr double kSum = 0.35, kExtra = 4.0;
   const bool tc = tc_shape(dk, dv, dtype);
+  const double kSum = tc ? 0.35 : 0.5, kExtra = tc ? 4.0 : 3.0;
   const long long C = tc ? hla::kC : hla::kSimtBatch;
-  const long long slots = tc ? sms / (dv / 64) : (long long)sms * 4;
+  const long long slots = tc ? sms / (dv / 64) : sms;
   const long long len = equal ? T / nseq : T, longest = (len + C - 1) / C;
   const long long B = H * (equal ? nseq * (longest + 1) : T / C + 2ll * nseq);   // units; at most, with cu_seqlens
   const long long items = (long long)nseq * H;
-  const long long share = (B + slots - 1) / slots;
+  const double share = tc ? (double)((B + slots - 1) / slots) : (double)B / (double)slots;
   const double whole = equal ? (double)((items + slots - 1) / slots) * (double)(longest + 1)
-                             : (double)(share > longest ? share : longest);
+                             : std::max(share, (double)longest);
   p->cut = longest > 1 && whole > share * (1.0 + kSum) + kExtra;
+  const long long most = tc ? slots : p->cut ? 2 * slots : 4 * slots;            // groups
   long long J;
-  if (p->cut) J = (B + share - 1) / share;                               // even shares
-  else J = items < slots ? items : slots;
+  if (!p->cut) J = std::min(items, most);
+  else if (tc) J = (B + (long long)share - 1) / (long long)share;                // even shares, fewer summaries
+  else J = std::min(B, most);                                                    // shares that differ by a unit
   p->J = (int)J;
   const size_t state = (size_t)dk * dv * sizeof(float);
   p->off_0 = p->cut ? J * state : 0;
