@@ -74,8 +74,12 @@ template <typename T, bool kSum> struct Batch {
 // thread tid has column tid % dv and the ROWS rows from (tid / dv) ROWS, so a
 // warp reads a token's k and q values as broadcasts.  kSum: the summary of the
 // part before the group's cut; else the outputs, and final states.  Bound by the
-// serial chain of its tokens (two products and a sum per state element and
-// token in fp32), so the tokens are split over many short parts.
+// serial chain of its tokens (three operations per state element and token in
+// fp32, two rows to an instruction: 306 cycles a token at dk = dv = 64, and 4400
+// per batch to add up the partial sums and finish the rows), so the tokens are
+// split over many short parts.  1600 tokens, 6 heads of 64, fp32: summaries 17 us,
+// scan 12, outputs 31 (cold caches), 51 us a call; one group for a (sequence,
+// head), uncut, would take 407 us.
 template <typename T, int ROWS, bool kSum>
 __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
   extern __shared__ __align__(16) float sm[];
@@ -233,7 +237,10 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
 // written once in fp32 (8 dk dv bytes, the floor of the call: about 96% of its
 // bytes at dk = dv = 128).  A block of 256 threads per (row, head); thread tid
 // has the four columns 4 (tid % (dv / 4)) and every (256 / (dv / 4))-th row,
-// R float4 of the state, all loaded before the first is used.
+// R float4 of the state, all loaded before the first is used.  Bound by memory
+// with many rows (500 rows, 16 heads of 128: 165 us, 6.4 TB/s, 0.98 of a plain
+// copy's rate), by the fill and drain of seven blocks per SM with 64 (26.5 us, 5.1
+// TB/s), by latency and the launch with one (5.3 us).
 constexpr int kStepThreads = 256;
 
 template <typename T, int R>
