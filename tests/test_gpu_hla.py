@@ -359,6 +359,51 @@ def test_prompt_then_steps_equal_one_prompt(dtype, dk, dv):
     assert torch.isnan(pool[1]).all()
 
 
+@pytest.mark.parametrize("dtype,dk", [("bf16", 64), ("f16", 128), ("f32", 64)])
+def test_offsets_past_31_bits(dtype, dk):
+    # 70 rows 2^25 elements apart, and states behind 2^31 elements of a pool
+    d = make([40, 29], 2, 2, dk, dk, dtype, seed=32, states=True)
+    c = dev(d)
+    T, w = 69, 2 * dk
+    buf = torch.empty(T, 1 << 25, device="cuda", dtype=DT[dtype])
+    q, k, v, z, out = (buf[:, i * w:(i + 1) * w].unflatten(1, (2, dk)) for i in range(5))
+    for n, t in (("q", q), ("k", k), ("v", v), ("z", z)):
+        t.copy_(c[n])
+    far = (1 << 31) // (2 * dk * dk) + 1
+    pool = torch.empty(far + 1, 2, dk, dk, device="cuda")
+    slots = torch.tensor([far, 3], dtype=torch.int32, device="cuda")
+    pool[slots.long()] = c["S"]
+    binding.hla_fwd(q, k, v, c["g"], z, c["w"], cu_seqlens=c["cu"], scale=d["scale"], state_in=pool, state_out=pool,
+                    slots=slots, out=out)
+    ref, S = reference(d)
+    assert_close(out, ref, DT[dtype], "far rows")
+    check_states(pool[slots.long()], S)
+    rows = slice(T - 2, T)                    # the last two rows, a token of each state
+    one = dict(d, cu=torch.tensor([0, 1, 2], dtype=torch.int32), S=torch.from_numpy(S),
+               **{n: d[n][rows] for n in ("q", "k", "v", "z", "g")})
+    binding.hla_step(q[rows], k[rows], v[rows], c["g"][rows], pool, z[rows], c["w"], scale=d["scale"], slots=slots,
+                     out=out[rows])
+    ref, S = reference(one)
+    assert_close(out[rows], ref, DT[dtype], "far rows, step")
+    check_states(pool[slots.long()], S)
+
+
+def test_sequences_without_a_token_only():
+    # rows, but every sequence is empty: no row is written, the states are the initial ones
+    for dtype, dk in (("bf16", 64), ("f16", 128), ("f32", 64)):
+        d = make([70], 2, 2, dk, dk, dtype, seed=33)
+        c = dev(d)
+        S = torch.randn(3, 2, dk, dk, device="cuda")
+        fin = torch.zeros_like(S)
+        out = torch.full_like(c["v"], 7.0)
+        cu = torch.tensor([5, 5, 5, 5], dtype=torch.int32, device="cuda")
+        seen = torch.tensor([1, 0, 4], dtype=torch.int32, device="cuda")
+        binding.hla_fwd(c["q"], c["k"], c["v"], c["g"], c["z"], c["w"], cu_seqlens=cu, scale=d["scale"], state_in=S,
+                        state_out=fin, seen=seen, out=out)
+        assert (out == 7).all()
+        assert torch.equal(fin[[0, 2]], S[[0, 2]]) and (fin[1] == 0).all()
+
+
 # ------------------------------------------------- streams, graphs, repetition
 @pytest.mark.parametrize("dtype,dk,dv", [("f16", 64, 64), ("bf16", 128, 128), ("f32", 64, 64)])
 def test_captured_and_replayed_on_new_inputs(dtype, dk, dv):

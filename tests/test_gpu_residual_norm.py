@@ -67,6 +67,31 @@ def test_every_part(N, D, xd, yd):
         run_both(d, use, xd, yd, f"{N}x{D} {xd}/{yd} {use}")
 
 
+@pytest.mark.parametrize("N,D", [(300, 4096), (600, 2056), (1200, 1032), (40, 8184)])
+@pytest.mark.parametrize("xd,yd", [("f32", "f16"), ("bf16", "bf16")])
+def test_many_rows(N, D, xd, yd):
+    # two vectors a thread, whole and partly filled warps
+    d = make(N, D, xd, yd, seed=N)
+    run_both(d, ("post_w", "gate", "res_scale", "pre_w"), xd, yd, f"{N}x{D}", gate_act="silu", alpha=0.3)
+
+
+def test_offsets_past_31_bits():
+    # 2^31 + 16384 elements; the first and the last rows
+    D = 16384
+    N = (1 << 31) // D + 1
+    x = torch.empty(N, D, device="cuda", dtype=torch.float16)
+    y = torch.empty(N, D, device="cuda", dtype=torch.float16)
+    gen = torch.Generator().manual_seed(9)
+    rows = torch.tensor([0, 1, N - 2, N - 1])
+    hx, hy = torch.randn(2, 4, D, generator=gen).half()
+    x[rows.cuda()] = hx.cuda()
+    y[rows.cuda()] = hy.cuda()
+    out = binding.residual_norm(x, y, pre_norm=True)
+    ref_x, ref = oracle.residual_norm(hx, hy)
+    assert_close(x[rows.cuda()], ref_x, torch.float16, "x")
+    assert_close(out[rows.cuda()], ref, torch.float16, "out")
+
+
 @pytest.mark.parametrize("act", ["mul", "sigmoid", "silu"])
 def test_gates_alpha_eps_and_norms_without_weights(act):
     d = make(20, 264, "f32", "bf16", seed=1)
