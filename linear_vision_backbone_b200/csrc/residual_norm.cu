@@ -38,9 +38,9 @@ constexpr int kRowWarps = 8;            // rows per block where a warp has a row
 struct NormArgs {
   const void* x; void* x_out; const void* y; const float* post_w; const void* gate;
   const float* res_scale; const float* pre_w; void* out;
-  long long N, gate_rows;
+  unsigned N, gate_rows;                // a rows' group of the gate; N below 2^31
   int D, post_norm, act;
-  float alpha, eps;
+  float alpha, eps, inv_d;              // 1 / D
 };
 
 // Two 16-bit elements to and from fp32: one conversion, and no packing.
@@ -141,16 +141,16 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) residual_norm_kernel(
   __shared__ float red[2][32];
   const int G = kWarpRow ? 32 : (int)blockDim.x;
   const int t = kWarpRow ? (threadIdx.x & 31) : (int)threadIdx.x;
-  const long long row = kWarpRow ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
-                                 : (long long)blockIdx.x;
+  const unsigned row = kWarpRow ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   pdl_wait();
   pdl_trigger();
   if (row >= a.N) return;                 // whole warps only where a block has several rows
   const int nv = a.D / VEC;
-  const float inv_d = 1.0f / (float)a.D;
-  const TX* xr = (const TX*)a.x + row * a.D;
-  const TY* yr = a.y ? (const TY*)a.y + row * a.D : nullptr;
-  const TY* gr = a.gate ? (const TY*)a.gate + row / a.gate_rows * a.D : nullptr;
+  const size_t at = (size_t)row * (unsigned)a.D;
+  const TX* xr = (const TX*)a.x + at;
+  const TY* yr = a.y ? (const TY*)a.y + at : nullptr;
+  const TY* gr = nullptr;
+  if (a.gate) gr = (const TY*)a.gate + (a.gate_rows == 1 ? at : (size_t)(row / a.gate_rows) * (unsigned)a.D);
   Pack<TX, VEC> xp[kV];
   Pack<TY, VEC> yp[kV], gp[kV];
 #pragma unroll
@@ -173,12 +173,12 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) residual_norm_kernel(
 #pragma unroll
         for (int e = 0; e < VEC; ++e) s = fmaf(y[e], y[e], s);
       }
-    inv = rsqrtf(row_sum<kWarpRow>(s, red[0]) * inv_d + a.eps);
+    inv = rsqrtf(row_sum<kWarpRow>(s, red[0]) * a.inv_d + a.eps);
   }
   // x + alpha res_scale r, in fp32 until the pre-norm has used it
   float x[kV][VEC];
   float s = 0.f;
-  TX* xo = (TX*)a.x_out + row * a.D;
+  TX* xo = (TX*)a.x_out + at;
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
     const int u = t + j * G;
@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) residual_norm_kernel(
     for (int e = 0; e < VEC; ++e) s = fmaf(x[j][e], x[j][e], s);
   }
   if (!a.out) return;
-  inv = rsqrtf(row_sum<kWarpRow>(s, red[1]) * inv_d + a.eps);
-  TY* orow = (TY*)a.out + row * a.D;
+  inv = rsqrtf(row_sum<kWarpRow>(s, red[1]) * a.inv_d + a.eps);
+  TY* orow = (TY*)a.out + at;
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
     const int u = t + j * G;
@@ -247,11 +247,11 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) residual_norm_kernel(
 template <typename TX, typename TY, int VEC, int kV>
 int launch_v(const NormArgs& a, int threads, cudaStream_t st) {
   if (threads == 32) {
-    const long long blocks = (a.N + kRowWarps - 1) / kRowWarps;
-    return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, true, 32 * kRowWarps>, dim3((unsigned)blocks),
+    const unsigned blocks = (a.N + kRowWarps - 1) / kRowWarps;
+    return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, true, 32 * kRowWarps>, dim3(blocks),
                       dim3(32 * kRowWarps), 0, st, a);
   }
-  const dim3 grid((unsigned)a.N), block((unsigned)threads);
+  const dim3 grid(a.N), block((unsigned)threads);
   // Four blocks of up to 320 threads per SM rather than three, at 48 registers: 18944 gated rows of a
   // 16-bit stream take 174 us for 192 at D = 5120 and 137 for 145 at 4096, but 69.3 for 68.4 at 2048
   // (128 threads); an fp32 stream spills at 48 registers (2 % slower).
@@ -275,7 +275,7 @@ int launch_typed(const NormArgs& a, bool vec, cudaStream_t st) {
     const int nv = a.D / 8;
     if (nv <= 32) return launch_v<TX, TY, 8, 1>(a, 32, st);
     if (nv <= 64) return launch_v<TX, TY, 8, 2>(a, 32, st);
-    if (nv <= 512 && a.N * nv < 148 * 1024) return launch_v<TX, TY, 8, 1>(a, round32(nv), st);
+    if (nv <= 512 && (long long)a.N * nv < 148 * 1024) return launch_v<TX, TY, 8, 1>(a, round32(nv), st);
     return launch_v<TX, TY, 8, 2>(a, round32((nv + 1) / 2), st);
   }
   if (a.D <= 256) return launch_v<TX, TY, 1, 8>(a, 32, st);
@@ -325,8 +325,8 @@ extern "C" GTR_API gtr_status_t gtr_residual_norm(const gtr_residual_norm_args* 
   }
   const bool vec = D % 8 == 0 && aligned(x, 16) && aligned(x_out, 16) && aligned(y, 16) && aligned(gate, 16) &&
                    aligned(out, 16) && aligned(post_w, 16) && aligned(res_scale, 16) && aligned(pre_w, 16);
-  const NormArgs a{x, x_out, y, post_w, gate, res_scale, pre_w, out, N, gate ? gate_rows : 1, D, post_norm != 0,
-                   gate_act, alpha, eps};
+  const NormArgs a{x, x_out, y, post_w, gate, res_scale, pre_w, out, (unsigned)N,
+                   (unsigned)(gate ? gate_rows : 1), D, post_norm != 0, gate_act, alpha, eps, 1.0f / (float)D};
   const cudaStream_t st = (cudaStream_t)stream;
   int rc;
   if (x_dtype == GTR_F16) rc = launch_typed<__half, __half>(a, vec, st);
