@@ -27,6 +27,7 @@
 
 #include "gtr_gla.h"
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace {
 
@@ -122,6 +123,54 @@ template <int VEC> __device__ __forceinline__ void load_w(const float* p, float 
   }
 }
 
+// Elementwise on a vector in fp32, two elements to an instruction (the same
+// roundings): y *= w; y += f x; the sum of squares on top of s.
+template <int VEC> __device__ __forceinline__ void mul(float (&y)[VEC], const float (&w)[VEC]) {
+  if constexpr (VEC == 1) {
+    y[0] *= w[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const float2 r = tc::f2unpack(tc::fmul2(tc::f2pack(y[e], y[e + 1]), tc::f2pack(w[e], w[e + 1])));
+      y[e] = r.x;
+      y[e + 1] = r.y;
+    }
+  }
+}
+template <int VEC> __device__ __forceinline__ void mul(float (&y)[VEC], float f) {
+  float w[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) w[e] = f;
+  mul(y, w);
+}
+template <int VEC> __device__ __forceinline__ void add_scaled(float (&y)[VEC], float f, const float (&x)[VEC]) {
+  if constexpr (VEC == 1) {
+    y[0] = fmaf(f, x[0], y[0]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const float2 r =
+          tc::f2unpack(tc::ffma2(tc::f2pack(f, f), tc::f2pack(x[e], x[e + 1]), tc::f2pack(y[e], y[e + 1])));
+      y[e] = r.x;
+      y[e + 1] = r.y;
+    }
+  }
+}
+template <int VEC> __device__ __forceinline__ float squares(const float (&y)[VEC], float s) {
+  if constexpr (VEC == 1) {
+    return fmaf(y[0], y[0], s);
+  } else {
+    uint64_t r = tc::f2pack(s, 0.f);
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const uint64_t v = tc::f2pack(y[e], y[e + 1]);
+      r = tc::ffma2(v, v, r);
+    }
+    const float2 f = tc::f2unpack(r);
+    return f.x + f.y;
+  }
+}
+
 // Sum over the threads of a row: a warp (kWarpRow), or the whole block.
 template <bool kWarpRow>
 __device__ __forceinline__ float row_sum(float s, float* red) {
@@ -170,8 +219,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) residual_norm_kernel(
       if (t + j * G < nv) {
         float y[VEC];
         yp[j].widen(y);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s = fmaf(y[e], y[e], s);
+        s = squares(y, s);
       }
     inv = rsqrtf(row_sum<kWarpRow>(s, red[0]) * a.inv_d + a.eps);
   }
@@ -190,39 +238,32 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) residual_norm_kernel(
       if (a.post_norm) {
         if (a.post_w) {
           load_w<VEC>(a.post_w + u * VEC, w);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) y[e] *= inv * w[e];
+          mul(w, inv);
+          mul(y, w);
         } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) y[e] *= inv;
+          mul(y, inv);
         }
       }
       if (gr) {
         float z[VEC];
         gp[j].widen(z);
         // the kind is the same for all: asked once a vector
-        if (a.act == GTR_GATE_SILU) {
+        if (a.act != GTR_GATE_MUL) {
+          float sg[VEC];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) y[e] *= z[e] * sigmoid(z[e]);
-        } else if (a.act == GTR_GATE_SIGMOID) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) y[e] *= sigmoid(z[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) y[e] *= z[e];
+          for (int e = 0; e < VEC; ++e) sg[e] = sigmoid(z[e]);
+          mul(y, sg);
         }
+        if (a.act != GTR_GATE_SIGMOID) mul(y, z);
       }
       if (a.res_scale) {
         load_w<VEC>(a.res_scale + u * VEC, w);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) y[e] *= w[e];
+        mul(y, w);
       }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[j][e] = fmaf(a.alpha, y[e], x[j][e]);
+      add_scaled(x[j], a.alpha, y);
     }
     if (yr || a.x_out != a.x) Pack<TX, VEC>::store(xo + (size_t)u * VEC, x[j]);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s = fmaf(x[j][e], x[j][e], s);
+    s = squares(x[j], s);
   }
   if (!a.out) return;
   inv = rsqrtf(row_sum<kWarpRow>(s, red[1]) * a.inv_d + a.eps);
@@ -231,16 +272,13 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) residual_norm_kernel(
   for (int j = 0; j < kV; ++j) {
     const int u = t + j * G;
     if (u >= nv) continue;
-    float w[VEC];
+    mul(x[j], inv);
     if (a.pre_w) {
+      float w[VEC];
       load_w<VEC>(a.pre_w + u * VEC, w);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] *= x[j][e] * inv;
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] = x[j][e] * inv;
+      mul(x[j], w);
     }
-    Pack<TY, VEC>::store(orow + (size_t)u * VEC, w);
+    Pack<TY, VEC>::store(orow + (size_t)u * VEC, x[j]);
   }
 }
 
