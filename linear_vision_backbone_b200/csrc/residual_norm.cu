@@ -10,13 +10,15 @@
 // to the last store, so the two means cost reductions and no second read; all
 // of a thread's loads are issued before the first is used.
 //
-// Measured: 16384 rows of 384, fp32 stream, fp16 branch, pre-norm: 13.5-15.7 us,
-// 4.8-5.6 TB/s (two waves of blocks); 8191 rows of 5120 bf16 with a SiLU gate and both
-// norms: 82 us, 5.1 TB/s, 0.78 of a plain copy's rate, 18944 rows 0.87 (bound by
-// the issue of the arithmetic, 0.7 of all slots, and the waits for the two means); nine rows of
-// 4096: 5.8 us (latency).  A resident grid that copies rows ahead into shared
-// memory and keeps the weights in registers was 10 to 50 % slower at every size
-// from D = 256 to 8192 (fewer warps to hide the arithmetic).
+// Measured: 16384 rows of 384, fp32 stream, fp16 branch, pre-norm: 13.1-16 us,
+// 4.7-5.8 TB/s (two waves of blocks); 8191 rows of 5120 bf16 with a SiLU gate, a
+// scale and both norms: 75 us, 5.6 TB/s, 0.85 of a plain copy's rate, and 0.95 with
+// 18944 rows (start and end of the launch; two thirds of the issue slots are taken,
+// so conversions and products are two elements to an instruction); 18944 rows of an
+// fp32 stream without a gate run at a copy's rate from D = 2048 on; nine rows of
+// 4096: 5.7 us (latency).  A resident grid that copies rows ahead into shared memory
+// and keeps the weights in registers was 10 to 50 % slower at every size from D =
+// 256 to 8192 (fewer warps to hide the arithmetic).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -291,8 +293,8 @@ int launch_v(const NormArgs& a, int threads, cudaStream_t st) {
   }
   const dim3 grid(a.N), block((unsigned)threads);
   // Four blocks of up to 320 threads per SM rather than three, at 48 registers: 18944 gated rows of a
-  // 16-bit stream take 174 us for 192 at D = 5120 and 137 for 145 at 4096, but 69.3 for 68.4 at 2048
-  // (128 threads); an fp32 stream spills at 48 registers (2 % slower).
+  // 16-bit stream take 155 us for 174 at D = 5120 and 122 for 131 at 4096, but 63.9 for 63.7 at 2048
+  // (128 threads); an fp32 stream would spill and is at a copy's rate as it is.
   if constexpr (VEC == 8 && kV == 2 && sizeof(TX) == 2)
     if (threads > 128 && threads <= 320)
       return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, false, 320, 4>, grid, block, 0, st, a);
@@ -307,9 +309,9 @@ int launch_typed(const NormArgs& a, bool vec, cudaStream_t st) {
   if (vec) {
     // A warp for a row of up to 64 vectors; else two vectors a thread, or one
     // while that leaves at most 512 threads a row and 1024 per SM in all. Gated
-    // bf16, one and two: 888 rows of 1024 4.2 and 4.7 us, 1184 rows 5.4 and 5.2;
-    // 592 rows of 2048 5.5 and 5.5, 1184 rows 8.4 and 7.4; 148 rows of 4096 4.0
-    // and 4.7, 296 rows 5.8 and 6.0, 592 rows 9.1 and 8.3.
+    // bf16, one and two: 888 rows of 1024 3.9 and 4.5 us, 1184 rows 4.9 and 5.0;
+    // 592 rows of 2048 5.2 and 5.1, 1184 rows 7.8 and 7.0; 148 rows of 4096 3.8
+    // and 4.3, 296 rows 5.5 and 5.5, 592 rows 8.7 and 7.4.
     const int nv = a.D / 8;
     if (nv <= 32) return launch_v<TX, TY, 8, 1>(a, 32, st);
     if (nv <= 64) return launch_v<TX, TY, 8, 2>(a, 32, st);
