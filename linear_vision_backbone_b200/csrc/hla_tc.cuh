@@ -688,6 +688,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     // S in two terms as the operand of the next block's qs
     auto put = [&]() {
       uint64_t up = both(1.f);
+      int exp_s = 0;
       if (!kBf16) {
         uint32_t mx = 0;
 #pragma unroll
@@ -701,9 +702,12 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         const int e = tc::scale_exp(fmaxf(fmaxf(wmax[8], wmax[9]), fmaxf(wmax[10], wmax[11])));
         tc::named_barrier(2, 128);                               // read before the next block's are written
         up = both(tc::pow2i(e));
-        if (w4 == 0 && lane == 0) es[is & 1] = e;
+        exp_s = e;
       }
       if (!wait(kSE, (is & 1) ^ 1)) return false;
+      // the product of the state before is done, and was issued after the outputs had taken the exponent of the
+      // one before that (kOE), which this overwrites
+      if (!kBf16 && w4 == 0 && lane == 0) es[is & 1] = exp_s;
       ++is;
       uint8_t* D = sm + L::kS + r * 128;
 #pragma unroll
