@@ -291,27 +291,37 @@ __device__ __forceinline__ void peer_arrive(uint32_t bar) {
 // has slept for at most 20 us, so kProbes of them, a second or so as they are
 // seen here and 20 s at the very most, end any wait.
 constexpr uint32_t kProbes = 1u << 20;
-__device__ __forceinline__ bool probe(uint64_t* b, uint32_t parity) {
-  uint32_t n = kProbes;
+// `ok` false: one probe, no more.
+__device__ __forceinline__ void probe(uint64_t* b, uint32_t parity, bool& ok) {
+  uint32_t n = ok ? kProbes : 0;
 #pragma unroll 1
-  while (!tc::mbar_try(b, parity))
-    if (--n == 0) return false;
-  return true;
+  while (!tc::mbar_try(b, parity)) {
+    if (n == 0) {
+      ok = false;
+      return;
+    }
+    --n;
+  }
 }
 // The same, acquiring what the other block of the cluster released.
-__device__ __forceinline__ bool cluster_wait(uint64_t* b, uint32_t parity) {
-  uint32_t n = kProbes, ok = 0;
+__device__ __forceinline__ void cluster_wait(uint64_t* b, uint32_t parity, bool& ok) {
+  uint32_t n = ok ? kProbes : 0;
 #pragma unroll 1
   while (true) {
+    uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
+        : "=r"(done)
         : "r"(saddr(b)), "r"(parity), "r"(20000u)
         : "memory");
-    if (ok) return true;
-    if (--n == 0) return false;
+    if (done) return;
+    if (n == 0) {
+      ok = false;
+      return;
+    }
+    --n;
   }
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -400,18 +410,22 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   const int share = p.H / p.Hk;                                // heads of a key head
   uint32_t it = 0;                                             // blocks of tokens since the start
   uint32_t is = 0;                                             // those that had a state before them
+  // Bounded waits: a failed probe returns at the latest after 20 us, so kProbes of them end in any case.  A thread
+  // whose wait ran out (ok false) probes once where it waited, arrives nowhere and issues nothing, but walks on: what it
+  // reads and writes stays in bounds whatever the order, and the barriers of its group (bar.sync, which has no limit)
+  // still get it.  So every role comes to its end.
   bool ok = true;
-  // bounded: a failed probe returns at the latest after 20 us, so kProbes of them end in any case
-  auto wait = [&](int b, uint32_t parity) { return probe(bar + b, parity); };
+  auto wait = [&](int b, uint32_t parity) { probe(bar + b, parity, ok); };
   // two barriers: their first probes are in flight together (a probe takes about 120 cycles)
   auto wait2 = [&](int b, uint32_t pb, int c, uint32_t pc) {
     const uint32_t x = tc::mbar_try(bar + b, pb), y = tc::mbar_try(bar + c, pc);
-    return (x || probe(bar + b, pb)) && (y || probe(bar + c, pc));
+    if (!x) wait(b, pb);
+    if (!y) wait(c, pc);
   };
   // one arrival for a warp, after all its lanes
   auto warp_arrive = [&](int b) {
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive_one(bar + b);
+    if (lane == 0 && ok) tc::mbar_arrive_one(bar + b);
   };
   auto for_parts = [&](auto&& body, auto flag) {
     if constexpr (kSum) {
@@ -419,7 +433,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
     } else {
       Part g;
       Walk walk{rg.a, rg.x1 - rg.x0};
-      while (ok && next_part<kC, decltype(flag)::value>(p, walk, g)) body(g);
+      while (next_part<kC, decltype(flag)::value>(p, walk, g)) body(g);
     }
   };
   constexpr std::true_type kRecord{};                          // the role that records bad slots
@@ -437,18 +451,17 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           const uint32_t i = it + c;
           const int t = g.t0 + c * kC;
           const int sk = i % L::kNK, sv = i % L::kNV;
-          ok = wait(kKE + sk, (i / L::kNK & 1) ^ 1);
+          wait(kKE + sk, (i / L::kNK & 1) ^ 1);
           if (!ok) break;
           tc::mbar_arrive_tx(bar + kKF + sk, L::kQTile);
           for (int x = 0; x < DK / 64; ++x)
             tma_load_3d(sm + L::kK + sk * L::kQTile + x * kTile, &maps.k, x * 64, hk, t, bar + kKF + sk);
-          ok = wait(kVE + sv, (i / L::kNV & 1) ^ 1);
+          wait(kVE + sv, (i / L::kNV & 1) ^ 1);
           if (!ok) break;
           tc::mbar_arrive_tx(bar + kVF + sv, kTile);
           tma_load_3d(sm + L::kV + sv * kTile, &maps.v, half * 64, g.h, t, bar + kVF + sv);
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       it += g.nb;
     }, kRecord);
   } else if (role == kMma) {
@@ -462,7 +475,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       const int nb = (int)__reduce_max_sync(0xffffffffu, (unsigned)g.nb);
       const bool want_end = wants_end(g);
       const int terms = want_end ? L::kTerms : 2;
-      for (int c = 0; c < nb && ok; ++c) {
+      for (int c = 0; c < nb; ++c) {
         const uint32_t i = it + c, par = i & 1;
         const int sk = i % L::kNK, sv = i % L::kNV;
         const uint8_t* K = sm + L::kK + sk * L::kQTile;
@@ -473,11 +486,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         if constexpr (!kSum) {
           const int sq = i % L::kNQ;
           const uint8_t* Q = sm + L::kQ + sq * L::kQTile;
-          ok = wait2(kKF + sk, i / L::kNK & 1, kQF + sq, i / L::kNQ & 1);
-          if (!ok) break;
+          wait2(kKF + sk, i / L::kNK & 1, kQF + sq, i / L::kNQ & 1);
           tc::tc_after_sync();
           const uint64_t aq = tc::sdesc(saddr(Q), 16, 1024), bk = tc::sdesc(saddr(K), 16, 1024);
-          if (lead) {
+          if (lead && ok) {
 #pragma unroll
             for (int s = 0; s < DK / 16; ++s) {
               const uint64_t o = (uint64_t)((s >> 2) * (kTile >> 4) + (s & 3) * tc::kStepK);
@@ -487,12 +499,11 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           }
           __syncwarp();
         } else {
-          ok = wait(kKF + sk, i / L::kNK & 1);
+          wait(kKF + sk, i / L::kNK & 1);
         }
-        ok = ok && wait2(kWF + sw, pw, kKvE + sw, pw ^ 1);
-        if (!ok) break;
+        wait2(kWF + sw, pw, kKvE + sw, pw ^ 1);
         tc::tc_after_sync();
-        if ((c + 1 < nb || want_end) && lead) {
+        if ((c + 1 < nb || want_end) && lead && ok) {
           const uint64_t ak = tc::sdesc(saddr(K), kTile, 1024), bw = tc::sdesc(saddr(W), kTile, 1024);
 #pragma unroll 1
           for (int s = 0; s < kC / 16; ++s)
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
               tc::mma_f16(kv + 64, ak + s * tc::kStepMN, bw3 + s * tc::kStepMN, kIdKV3, 1u);
           }
         }
-        if (lead) {
+        if (lead && ok) {
           tc::mma_commit(bar + kKvF + sw);
           tc::mma_commit(bar + kWE + sw);
           tc::mma_commit(bar + kKE + sk);
@@ -515,12 +526,12 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           const uint64_t aq = tc::sdesc(saddr(sm + L::kQ + sq * L::kQTile), 16, 1024);
           // the terms of S; qs and pv of the block before are read
           const bool state = c > 0 || has_start(g);
-          ok = state ? wait2(kSF, is & 1, kOE, par ^ 1) : wait(kOE, par ^ 1);
-          if (!ok) break;
+          if (state) wait2(kSF, is & 1, kOE, par ^ 1);
+          else wait(kOE, par ^ 1);
           tc::tc_after_sync();
           if (state) {
             const uint64_t bs = tc::sdesc(saddr(sm + L::kS), L::kSTile, 1024);
-            if (lead) {
+            if (lead && ok) {
 #pragma unroll 1
               for (int s = 0; s < DK / 16; ++s) {
                 const uint64_t o = (uint64_t)((s >> 2) * (kTile >> 4) + (s & 3) * tc::kStepK);
@@ -530,13 +541,12 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             }
             ++is;
           }
-          if (lead) tc::mma_commit(bar + kQE + sq);
+          if (lead && ok) tc::mma_commit(bar + kQE + sq);
           __syncwarp();
-          ok = wait(kPF, par);
-          if (!ok) break;
+          wait(kPF, par);
           tc::tc_after_sync();
           const uint64_t bv = tc::sdesc(saddr(V), kTile, 1024);
-          if (lead) {
+          if (lead && ok) {
 #pragma unroll 1
             for (int s = 0; s < kC / 16; ++s)
               tc::mma_f16_ts(tm + kTmPV, tm + kTmSc + 8 * s, bv + s * tc::kStepMN, kIdPV, s > 0);
@@ -546,15 +556,15 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             tc::mma_commit(bar + kPvF);
           }
         }
-        if (lead) tc::mma_commit(bar + kVE + sv);
+        if (lead && ok) tc::mma_commit(bar + kVE + sv);
         __syncwarp();
       }
       it += nb;
     }, kQuiet);
-    if (ok && it > 0) {
+    if (it > 0) {
       // the last arrival a product makes on this memory
       const uint32_t i = it - 1;
-      ok = wait(kVE + i % L::kNV, i / L::kNV & 1);
+      wait(kVE + i % L::kNV, i / L::kNV & 1);
     }
   } else if (role == kBuild) {
     if constexpr (!kSum) set_registers<Regs<DK>::kBuild>();
@@ -565,7 +575,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       const bool want_end = wants_end(g);
       // a block ahead, and turned when it is used (rows past the end read the last one)
       float raw = g.len > 0 ? load_g(p, g.t0 + min(row, g.len - 1), g.h) : 0.f;
-      for (int c = 0; c < g.nb && ok; ++c) {
+      for (int c = 0; c < g.nb; ++c) {
         const uint32_t i = it + c;
         const int nv = min(kC, g.len - c * kC);                  // tokens of this block
         const float lc = row < nv ? log2_decay(raw) : 0.f;
@@ -590,15 +600,13 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           if (x > w4) R += ws[x];
         }
         if (sub == 0) {
-          ok = wait(kGE + (i & 1), (i >> 1 & 1) ^ 1);
-          if (!ok) break;
+          wait(kGE + (i & 1), (i >> 1 & 1) ^ 1);
           Gs[(i & 1) * kC + row] = G;
           Us[(i & 1) * kC + row] = tc::ex2(suf);
           warp_arrive(kGF + (i & 1));
         }
         const int sv = i % L::kNV, sk = i % L::kNK;
-        ok = wait(kVF + sv, i / L::kNV & 1);
-        if (!ok) break;
+        wait(kVF + sv, i / L::kNV & 1);
         uint8_t* V = sm + L::kV + sv * kTile + row * 128;
         const bool build = c + 1 < g.nb || want_end;
         const bool live = row < nv;
@@ -631,8 +639,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           up = tc::pow2i(exp_w);
         }
         const int sw = i % L::kNW;
-        ok = wait(kWE + sw, (i / L::kNW & 1) ^ 1);
-        if (!ok) break;
+        wait(kWE + sw, (i / L::kNW & 1) ^ 1);
         if (build) {
           // the tile's last product is done; the exponent of four blocks ago, in this slot, is long read
           if (!kBf16 && row == 0 && sub == 0) ew[i & 3] = exp_w;
@@ -660,8 +667,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         if (nv < kC) {
           // rows behind the sequence's last token hold others' data: zeros, so
           // that nothing of them (a NaN times a zero weight) enters a product
-          ok = wait(kKF + sk, i / L::kNK & 1);
-          if (!ok) break;
+          wait(kKF + sk, i / L::kNK & 1);
           if (!live) {
             uint8_t* K = sm + L::kK + sk * L::kQTile + row * 128;
             const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -704,7 +710,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         up = both(tc::pow2i(e));
         exp_s = e;
       }
-      if (!wait(kSE, (is & 1) ^ 1)) return false;
+      wait(kSE, (is & 1) ^ 1);
       // the product of the state before is done, and was issued after the outputs had taken the exponent of the
       // one before that (kOE), which this overwrites
       if (!kBf16 && w4 == 0 && lane == 0) es[is & 1] = exp_s;
@@ -729,7 +735,6 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       }
       tc::fence_async_smem();
       warp_arrive(kSF);
-      return true;
     };
     const size_t hs = (size_t)DK * p.dv, at = (size_t)r * p.dv + half * 64;
     auto run = [&](const Part& g) {
@@ -746,13 +751,12 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         }
       float total = 0.f;
       // c = -1: the terms of the state before the first block
-      for (int c = has_start(g) ? -1 : 0; c < g.nb && ok; ++c) {
+      for (int c = has_start(g) ? -1 : 0; c < g.nb; ++c) {
         if (c >= 0) {
           const uint32_t i = it + c;
           const int sw = i % L::kNW;
           const uint32_t kv = tm + lane_base + kTmKV - 128 * sw;
-          ok = wait2(kGF + (i & 1), i >> 1 & 1, kKvF + sw, i / L::kNW & 1);
-          if (!ok) break;
+          wait2(kGF + (i & 1), i >> 1 & 1, kKvF + sw, i / L::kNW & 1);
           const float la = Gs[(i & 1) * kC + kC - 1];
           warp_arrive(kGE + (i & 1));
           tc::tc_after_sync();
@@ -783,10 +787,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           tc::tc_before_sync();
           warp_arrive(kKvE + sw);
         }
-        if (!kSum && c + 1 < g.nb) ok = put();
+        if (!kSum && c + 1 < g.nb) put();
       }
       it += g.nb;
-      if (ok && want_end) {
+      if (want_end) {
         float* dst = kSum ? p.wsS + (size_t)group_j * hs : p.state_out + ((size_t)g.slot * p.H + g.h) * hs;
 #pragma unroll
         for (int x = 0; x < kRuns; ++x)
@@ -808,7 +812,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       Walk walk{rg.a, rg.x1 - rg.x0};
       Part g, n;
       bool have = false;
-      while (ok) {
+      while (true) {
         const bool more = next_part<kC>(p, walk, n);
         if (more) {
           const float* src = start_state(p, n, group_j);
@@ -832,10 +836,9 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         for (int b = 2 * w4 + 2; b < 8; ++b) tm_st8(tm + lane_base + kTmPlo + 8 * b, zero);
       }
       for_parts([&](const Part& g) {
-        for (int c = 0; c < g.nb && ok; ++c) {
+        for (int c = 0; c < g.nb; ++c) {
           const uint32_t i = it + c, par = i & 1;
-          ok = wait2(kGF + (i & 1), i >> 1 & 1, kScF, par);
-          if (!ok) break;
+          wait2(kGF + (i & 1), i >> 1 & 1, kScF, par);
           tc::tc_after_sync();
           const float* G = Gs + (i & 1) * kC;
           const float* U = Us + (i & 1) * kC;
@@ -926,15 +929,13 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       const uint32_t pv = tm + lane_base + kTmPV + 32 * sub, qs = tm + lane_base + kTmQS + 32 * sub;
       const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(rmsw + 32 * sub);
       for_parts([&](const Part& g) {
-        for (int c = 0; c < g.nb && ok; ++c) {
+        for (int c = 0; c < g.nb; ++c) {
           const uint32_t i = it + c, par = i & 1;
           const int nv = min(kC, g.len - c * kC);
           const int sz = i % L::kNZ;
-          ok = wait2(kGF + (i & 1), i >> 1 & 1, kZF + sz, i / L::kNZ & 1);   // z, or the buffer alone
-          if (!ok) break;
+          wait2(kGF + (i & 1), i >> 1 & 1, kZF + sz, i / L::kNZ & 1);   // z, or the buffer alone
           const float Gi = Gs[(i & 1) * kC + row];
-          ok = wait(kPvF, par);
-          if (!ok) break;
+          wait(kPvF, par);
           tc::tc_after_sync();
           const bool state = c > 0 || has_start(g);
           float f1 = p.scale * tc::ex2(Gi), f2 = p.scale;
@@ -982,8 +983,8 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
               ss += *X;
               if constexpr (kPair) {
                 // the other half's sum: its copy of ours is free once it has read the block before
-                if (row == 0) tc::mbar_arrive_tx(bar + kXF, kC * 4);
-                ok = cluster_wait(bar + kXE, par ^ 1);
+                if (row == 0 && ok) tc::mbar_arrive_tx(bar + kXF, kC * 4);
+                cluster_wait(bar + kXE, par ^ 1, ok);
                 if (ok) peer_send(peer_addr(saddr(Xs + row), rank ^ 1u), ss, peer_addr(saddr(bar + kXF), rank ^ 1u));
               }
             }
@@ -1007,9 +1008,9 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             }
             if (sub == 0) {
               if constexpr (kPair) {
-                ok = ok && cluster_wait(bar + kXF, par);
+                cluster_wait(bar + kXF, par, ok);
                 ss += *reinterpret_cast<volatile float*>(Xs + row);
-                peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));
+                if (ok) peer_arrive(peer_addr(saddr(bar + kXE), rank ^ 1u));
               }
               *X = rsqrtf(ss / (float)p.dv + kRmsEps);
             }
@@ -1049,14 +1050,13 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             const int t = g.t0 + c * kC, sq = i % L::kNQ;
             if (L::kNQ == 1)                                     // one buffer: at least from memory into L2
               for (int x = 0; x < DK / 64; ++x) tma_prefetch_3d(&maps.q, x * 64, hk, t);
-            ok = wait(kQE + sq, (i / L::kNQ & 1) ^ 1);
+            wait(kQE + sq, (i / L::kNQ & 1) ^ 1);
             if (!ok) break;
             tc::mbar_arrive_tx(bar + kQF + sq, L::kQTile);
             for (int x = 0; x < DK / 64; ++x)
               tma_load_3d(sm + L::kQ + sq * L::kQTile + x * kTile, &maps.q, x * 64, hk, t, bar + kQF + sq);
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
         it += g.nb;
       }, kQuiet);
     } else if (role == kLoadZ) {
@@ -1065,13 +1065,12 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       set_registers<Regs<DK>::kMisc>();
       int pt[L::kNZ] = {}, ph[L::kNZ] = {};                      // the block in each buffer: row (-1: no store), head
       auto finish = [&](uint32_t i, int sz) {
-        if (!wait(kOS + sz, i / L::kNZ & 1)) return false;
-        if (pt[sz] >= 0) {
+        wait(kOS + sz, i / L::kNZ & 1);
+        if (ok && pt[sz] >= 0) {
           tma_store_3d(&maps.o, sm + L::kZ + sz * kTile, half * 64, ph[sz], pt[sz]);
           tc::bulk_commit();
           tc::bulk_wait_read<0>();
         }
-        return true;
       };
       for_parts([&](const Part& g) {
         if (lane == 0) {
@@ -1081,7 +1080,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
 #pragma unroll
             for (int sz = 0; sz < L::kNZ; ++sz) {
               if (i % L::kNZ != sz) continue;
-              if (i >= L::kNZ) ok = finish(i - L::kNZ, sz);
+              if (i >= L::kNZ) finish(i - L::kNZ, sz);
               if (!ok) break;
               pt[sz] = g.len - c * kC >= kC ? t : -1;
               ph[sz] = g.h;
@@ -1096,27 +1095,25 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
             }
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
         it += g.nb;
       }, kQuiet);
-      if (lane == 0 && ok) {
+      if (lane == 0) {
 #pragma unroll
         for (int back = L::kNZ; back > 0; --back) {
           if (it < (uint32_t)back) continue;
           const uint32_t i = it - back;
 #pragma unroll
           for (int sz = 0; sz < L::kNZ; ++sz)
-            if (i % L::kNZ == sz) ok = ok && finish(i, sz);
+            if (i % L::kNZ == sz) finish(i, sz);
         }
         tc::bulk_wait<0>();
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   }
-  // a bounded wait that ran out ends every warp's walk the same way; loads and
-  // products in flight get time to land before the memory is given up
-  if (!ok && lane == 0) {
-    gtr_flag(kStatusMbarTimeout);
+  // a bounded wait ran out: loads and products in flight get time to land before the memory is given up
+  __syncwarp();
+  if (__any_sync(0xffffffffu, !ok)) {
+    if (lane == 0) gtr_flag(kStatusMbarTimeout);
     const unsigned long long t0 = tc::globaltimer();
     while (tc::globaltimer() - t0 < 2000000ull) {}
   }

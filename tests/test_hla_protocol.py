@@ -331,3 +331,37 @@ def test_steady_cases_walk_many_blocks(name):
     if len(lens) < 32:
         assert part >= 8                      # and with one state behind another in a single part
     assert cut != equal
+
+
+# ------------------------------------------------------ waits that run out
+def _role(name, following):
+    a = SOURCE.index(f"role == {name}) {{", SOURCE.index("if (role == kLoad) {"))
+    return SOURCE[a:SOURCE.index(following, a)]
+
+
+@pytest.mark.parametrize("name,following", [("kMma", "role == kBuild"), ("kBuild", "role == kState"),
+                                            ("kState", "} else if constexpr (!kSum)"), ("kP", "role == kOut"),
+                                            ("kOut", "role == kLoadQ")])
+def test_a_wait_that_ran_out_skips_no_barrier_of_its_group(name, following):
+    """bar.sync and the warp-wide instructions have no limit, so no thread of these groups may leave its walk, or take
+    another way through it, because a bounded wait of its own ran out: it may only leave out arrivals and issues."""
+    body = re.sub(r"//[^\n]*", "", _role(name, following))
+    body = body.replace("if (!more) break;", "")       # the end of the walk, the same for the whole group
+    assert "break" not in body and "return false" not in body and "continue" not in body
+    for line in body.splitlines():
+        if re.search(r"\bok\b", line):
+            assert re.search(r"if \((lead|row == 0|\(c \+ 1 < nb \|\| want_end\) && lead) && ok\)|if \(ok\) peer_|cluster_wait\(",
+                             line), line
+    for _, guarded in re.findall(r"^( *)if \([^\n]*\bok\b[^\n]*\) \{\n(.*?)^\1\}", body, re.S | re.M):
+        assert "named_barrier" not in guarded and "_arrive(" not in guarded and "sync" not in guarded
+    # the waits give nothing back that a caller could branch on
+    assert not re.search(r"=\s*wait2?\(", body) and not re.search(r"(if|while) \(!?wait2?\(", body)
+
+
+def test_every_wait_has_a_limit_and_the_walk_does_not_depend_on_it():
+    text = re.sub(r"//[^\n]*", "", SOURCE)
+    assert len(re.findall(r"mbarrier\.try_wait", text)) == 1 and "mbar_wait(" not in text
+    # both loops that probe, and end for a thread that gave up before
+    assert len(re.findall(r"uint32_t n = ok \? kProbes : 0;", text)) == 2
+    assert len(re.findall(r"if \(n == 0\) \{\s*ok = false;\s*return;\s*\}\s*--n;", text)) == 2
+    assert "while (next_part<kC" in text and "ok && next_part" not in text
