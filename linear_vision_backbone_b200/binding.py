@@ -476,7 +476,10 @@ def _pitch(t, name, dtype, shape, device):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]:
         raise ValueError(f"{name}: sequences must follow each other at the tokens' pitch")
-    return st[-3] if lead[-1] > 1 else (st[0] if len(lead) == 2 and lead[0] > 1 else 0)
+    rows = st[-3] if lead[-1] > 1 else (st[0] if len(lead) == 2 and lead[0] > 1 else 0)
+    if rows < shape[-2] * shape[-1] and (lead[-1] > 1 or lead[0] > 1):
+        raise ValueError(f"{name}: its tokens share memory (a broadcast tensor?)")   # and 0 would stand for dense
+    return rows
 
 
 @contextlib.contextmanager

@@ -1,0 +1,42 @@
+"""What the binding of the head-decay attention and the residual norm sends to the C ABI, and what it
+refuses, without a GPU: its checks run on CPU tensors, whose device is -1."""
+import pytest
+import torch
+
+from linear_vision_backbone_b200 import binding
+
+
+def pitch(t):
+    return binding._pitch(t, "q", t.dtype, t.shape, -1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_row_pitches(dtype):
+    e = lambda *s: torch.empty(*s, dtype=dtype)  # noqa: E731
+    assert pitch(e(5, 2, 64)) == 0 and pitch(e(0, 2, 64)) == 0 and pitch(e(3, 5, 2, 64)) == 0      # dense
+    assert pitch(e(5, 400)[:, 64:192].unflatten(1, (2, 64))) == 400
+    assert pitch(e(3, 5, 400)[..., 64:192].unflatten(2, (2, 64))) == 400
+    assert pitch(e(3, 1, 400)[..., 64:192].unflatten(2, (2, 64))) == 400    # one token a sequence
+    assert pitch(e(1, 5, 400)[..., 64:192].unflatten(2, (2, 64))) == 400
+    assert pitch(e(1, 400)[:, 64:192].unflatten(1, (2, 64))) == 0           # one row has no pitch
+    assert pitch(e(1, 2, 64).expand(1, 2, 64)) == 0
+
+
+@pytest.mark.parametrize("t", [
+    torch.empty(1, 2, 64).expand(10, 2, 64),                  # one row for every token
+    torch.empty(2, 64).expand(10, 2, 64),
+    torch.empty(1, 1, 64).expand(10, 1, 64),
+    torch.empty(1, 1, 2, 64).expand(3, 10, 2, 64),            # for every token of every sequence
+    torch.empty(1, 1, 2, 64).expand(3, 1, 2, 64),             # one token, a batch
+    torch.empty(1, 1, 2, 64).expand(1, 10, 2, 64),
+    torch.empty(1, 10, 2, 64).expand(3, 10, 2, 64),           # one sequence for the batch
+    torch.empty(3, 1, 2, 64).expand(3, 10, 2, 64),            # one token for each sequence
+    torch.empty(1000).as_strided((10, 2, 64), (64, 64, 1)),   # rows that share columns
+    torch.empty(1000).as_strided((3, 4, 2, 64), (256, 64, 64, 1)),
+    torch.empty(10, 1, 64).expand(10, 2, 64),                 # one head for all
+    torch.empty(10, 2, 1).expand(10, 2, 64),
+])
+def test_rows_that_share_memory_are_refused(t):
+    # a pitch of zero stands for dense rows: a broadcast tensor would be read (or written) past its end
+    with pytest.raises(ValueError):
+        pitch(t)
