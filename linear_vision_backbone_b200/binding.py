@@ -540,6 +540,8 @@ def _hla(fn, q, k, v, g, z, w, cu_seqlens, nseq, scale, state_in, state_out, slo
     if nseq is None:
         nseq = lead[0] if len(lead) == 2 else 1
         if cu_seqlens is not None:
+            if not isinstance(cu_seqlens, _Tensor):
+                raise ValueError(f"cu_seqlens must be a tensor, got {type(cu_seqlens).__name__}")
             nseq = cu_seqlens.numel() - 1
             if nseq < 0:
                 raise ValueError("cu_seqlens must have at least one entry")

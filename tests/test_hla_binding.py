@@ -40,3 +40,33 @@ def test_rows_that_share_memory_are_refused(t):
     # a pitch of zero stands for dense rows: a broadcast tensor would be read (or written) past its end
     with pytest.raises(ValueError):
         pitch(t)
+
+
+class OnDevice(torch.Tensor):
+    """A CPU tensor that says it is on cuda:0, for the checks before a launch."""
+
+    @property
+    def is_cuda(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+
+@pytest.fixture
+def no_launch(monkeypatch):
+    """The binding without a device: calls that reach the library fail the test."""
+    monkeypatch.setattr(binding, "_elsewhere", lambda device, stream: False)
+    monkeypatch.setattr(binding, "load", lambda: pytest.fail("reached the library"))
+    monkeypatch.setattr(binding, "_lib", None)
+
+
+def on_device(*shape, dtype=torch.float16):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice)
+
+
+def test_offsets_that_are_no_tensor_are_refused(no_launch):
+    q, g = on_device(6, 2, 64), on_device(6, 2, dtype=torch.float32)
+    for cu in ([0, 2, 6], (0, 6), 6):
+        with pytest.raises(ValueError, match="cu_seqlens"):
+            binding.hla_fwd(q, q, q, g, cu_seqlens=cu)
