@@ -622,8 +622,9 @@ def residual_norm(x, y=None, *, post_norm: Optional[bool] = None, post_w=None, g
     Returns RMSNorm(x_out) * pre_w in y's type (x's without y), or None without
     a pre-norm.  x: [..., D], updated in place unless x_out is given; gate: y's
     shape, or [n, D] with n dividing the rows (row r takes gate row r // (rows /
-    n)); gate_act: "mul", "sigmoid" or "silu".  post_w, res_scale, pre_w: [D]
-    fp32 or None; post_norm / pre_norm default to whether their weight is given.
+    n)); gate_act: "mul", "sigmoid" or "silu" ("none" only without a gate).
+    post_w, res_scale, pre_w: [D] fp32 or None; post_norm / pre_norm default to
+    whether their weight is given.
     """
     if not isinstance(x, _Tensor) or not x.is_cuda or x.dtype not in DTYPE_IDS or x.dim() < 1:
         raise ValueError("x must be a CUDA tensor [..., D]")
@@ -647,6 +648,8 @@ def residual_norm(x, y=None, *, post_norm: Optional[bool] = None, post_w=None, g
     if x_out is not None:
         pxo = _dense(x_out, "x_out", xt, shape, device)
     if gate is not None:
+        if gate_act == "none":
+            raise ValueError("a gate needs a gate_act of mul, sigmoid or silu")
         gs = gate.shape if isinstance(gate, _Tensor) else None
         if gs is not None and gs != shape and len(gs) == 2 and gs[0] > 0 and gs[1] == D and N % gs[0] == 0:
             rows = max(1, N // gs[0])

@@ -70,3 +70,10 @@ def test_offsets_that_are_no_tensor_are_refused(no_launch):
     for cu in ([0, 2, 6], (0, 6), 6):
         with pytest.raises(ValueError, match="cu_seqlens"):
             binding.hla_fwd(q, q, q, g, cu_seqlens=cu)
+
+
+def test_a_gate_needs_its_kind(no_launch):
+    # "none" is for calls without a gate: it would have multiplied by the raw gate
+    x = on_device(4, 64)
+    with pytest.raises(ValueError, match="gate_act"):
+        binding.residual_norm(x, x, gate=x, gate_act="none")
