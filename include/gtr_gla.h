@@ -387,6 +387,8 @@ GTR_API gtr_status_t gtr_stack_fwd(float *x, const gtr_block_weights *blocks, in
  *            outside every sequence are neither read nor written.  NULL: nseq
  *            equal sequences of T / nseq rows (nseq must divide T).  Lengths
  *            of zero are allowed (the final state is then the initial one).
+ *            With other offsets the call writes no output and no state, which
+ *            gtr_last_device_status records (bad shape).
  *   state_in, state_out  [nslots, H, dk, dv] fp32, either may be NULL (start
  *            from zero; final states not wanted); the same pointer updates
  *            the states in place.  Different pointers must not overlap.

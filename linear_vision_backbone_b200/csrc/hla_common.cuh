@@ -13,8 +13,8 @@
 // zero, and its decay) in workspace entry j, which the scan turns into the state
 // the next group starts from; there are J entries whatever the sizes.  Without,
 // a group takes the (sequence, head)s whose first block is in its range, whole.
-// Offsets that are not those of a valid cu_seqlens are clamped to [0, T], so no
-// access leaves the tensors whatever it holds.
+// With offsets that are not those of a valid cu_seqlens no group has a unit, and
+// the device status says so: their sequences may overlap, and B pass 31 bits.
 #pragma once
 #include "common.cuh"
 
@@ -83,13 +83,19 @@ struct Range {
   __device__ __forceinline__ int start(int j) const { return j >= J ? B : q * j + min(j, r); }
   __device__ __forceinline__ void set(int units, int groups, int j) {
     B = units;
-    J = min(groups, units);
+    J = max(min(groups, units), 1);
     q = (unsigned)B / (unsigned)J;
     r = B - q * J;
     x0 = start(j);
     x1 = start(j + 1);
   }
 };
+
+// Units a head of sequence n by its offsets, or -1 where they are not those of a sequence.
+template <int C> __device__ __forceinline__ int units_of(const Params& p, int n) {
+  const int a = __ldg(p.cu + n), b = __ldg(p.cu + n + 1);
+  return a < 0 || b < a || b > p.T ? -1 : n_units(b - a, C);
+}
 
 // By the whole block of threads.  `scratch`: 40 ints of shared memory, free
 // again after the caller's next barrier.
@@ -105,15 +111,16 @@ template <int C> __device__ __forceinline__ void locate(const Params& p, int j, 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   if (p.nseq <= 32) {
     // a lane for a sequence, every warp for itself: one load's latency and no barrier
-    int r;
-    const int nu = lane < p.nseq ? n_units(seq_rows<C>(p, lane, r), C) : 0;
+    const int nu = lane < p.nseq ? units_of<C>(p, lane) : 0;
+    const bool bad = __any_sync(0xffffffffu, nu < 0);
     int e = nu;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, e, d);
       if (lane >= d) e += o;
     }
-    g.set(__shfl_sync(0xffffffffu, e, 31) * p.H, p.J, j);
+    if (bad && tid == 0 && j == 0) gtr_flag(kStatusBadShape);
+    g.set(bad ? 0 : __shfl_sync(0xffffffffu, e, 31) * p.H, p.J, j);
     const int s = (e - nu) * p.H;                                // this sequence's first unit
     auto at = [&](int x, Place& q) {
       if (x >= g.B) { q.set(p.nseq, 0, 1); return; }
@@ -126,8 +133,12 @@ template <int C> __device__ __forceinline__ void locate(const Params& p, int j, 
   }
   const int per = (p.nseq + blockDim.x - 1u) / blockDim.x;       // sequences per thread, consecutive ones
   const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
-  int mine = 0, r;
-  for (int n = n0; n < n1; ++n) mine += n_units(seq_rows<C>(p, n, r), C);
+  int mine = 0, bad = 0;
+  for (int n = n0; n < n1; ++n) {
+    const int nu = units_of<C>(p, n);
+    mine += nu;
+    bad |= nu < 0;
+  }
   int inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -139,7 +150,14 @@ template <int C> __device__ __forceinline__ void locate(const Params& p, int j, 
     scratch[32] = p.nseq; scratch[33] = 0; scratch[34] = 1;
     scratch[35] = p.nseq; scratch[36] = 0; scratch[37] = 1;
   }
-  __syncthreads();
+  bad = __syncthreads_or(bad);
+  if (bad) {
+    if (tid == 0 && j == 0) gtr_flag(kStatusBadShape);
+    g.set(0, p.J, j);
+    g.a.set(p.nseq, 0, 1);
+    g.b.set(p.nseq, 0, 1);
+    return;
+  }
   int before = inc - mine, total = 0;
   for (int w = 0; w < nw; ++w) {
     if (w < warp) before += scratch[w];
@@ -147,7 +165,7 @@ template <int C> __device__ __forceinline__ void locate(const Params& p, int j, 
   }
   g.set(total * p.H, p.J, j);
   for (int n = n0; n < n1; ++n) {
-    const int nu = n_units(seq_rows<C>(p, n, r), C);
+    const int nu = units_of<C>(p, n);
     const int s = before * p.H, e = (before + nu) * p.H;
     if (s <= g.x0 && g.x0 < e) { scratch[32] = n; scratch[33] = g.x0 - s; scratch[34] = nu; }
     if (s <= g.x1 && g.x1 < e) { scratch[35] = n; scratch[36] = g.x1 - s; scratch[37] = nu; }
