@@ -22,7 +22,7 @@ namespace gtr {
 namespace hla {
 
 constexpr int kC = 128;            // tokens per block of the tensor-core kernels
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMinLog = -110.0f; // e^-110 is zero in fp32
 
 // The cuts of a (sequence, head), at the group with its first block: the

@@ -12,7 +12,6 @@ namespace hla {
 
 constexpr int kSimtThreads = 256;
 constexpr int kSimtBatch = 16;     // tokens staged in shared memory per pass: two a warp
-constexpr float kLn2 = 0.6931471805599453f;
 
 __host__ __device__ inline int simt_smem_floats(int dk, int dv, bool sum) {
   return kSimtBatch * (2 + (sum ? 1 : 2) * dk + dv + (sum ? 0 : kSimtThreads));

@@ -7,11 +7,14 @@
 //   o_i = e^{G_i} q_i S + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j
 //   S  <- e^{G_C} S + sum_j k_j^T (e^{G_C - G_j} v_j)
 //
-// every factor at most one, so nothing overflows whatever the decays: the
-// sums G_C - G_j come from a suffix sum of their own, and e^{G_i - G_j} is a
-// product e^{G_i - G_b} e^{G_b - G_j} through the end b of j's 32 tokens where
-// i is past it (one exponential per row and 32 columns), and a single
-// exponential only in the 32 x 32 squares on the diagonal.
+// every factor at most one, so nothing overflows whatever the decays.  No weight
+// is a difference of sums from the block's start, which strong decays before both
+// tokens would leave few bits of (a reset every fourth token: 2^-11): G_C - G_j is
+// a suffix sum of its own; e^{G_i - G_j} is e^{G_i - G_b} e^{G_b - G_j} through the
+// end b of j's 32 tokens where i is past it, either sum taken over just the tokens
+// in between (one exponential per row and 16 columns); and in the 32 x 32 squares
+// on the diagonal it is the product of the decays in between, column by column
+// from right to left.
 //
 // Four matrix products per block, accumulated in fp32 in tensor memory, with
 // q, k and v as they are and every computed operand in 16-bit terms (x = hi +
@@ -88,11 +91,11 @@ template <typename T, int DK, bool kSum> struct Layout {
   static constexpr int kS = kW + kNW * kWTile;        // S hi, S lo: dk rows x 64 columns each
   static constexpr int kSTile = DK * 128;
   static constexpr int kZ = kS + (kSum ? 0 : 2 * kSTile);   // z, then the outputs over it
-  static constexpr int kG = kZ + (kSum ? 0 : kNZ * kTile);         // [2][128] G
+  static constexpr int kG = kZ + (kSum ? 0 : kNZ * kTile);         // [2][128] log2-decays l, then G
   static constexpr int kU = kG + 2 * kC * 4;          // [2][128] e^{G_b - G_j}
   static constexpr int kX = kU + 2 * kC * 4;          // [128] the other half's sums of squares
   static constexpr int kRms = kX + kC * 4;            // [64] the norm's weights
-  static constexpr int kMisc = kRms + 64 * 4;         // warp sums [2][4]; the tensor memory address before them
+  static constexpr int kMisc = kRms + 64 * 4;         // [2][4] sums of l over 32 tokens; the tensor memory address before them
   static constexpr int kBars = kMisc + 32;
   // mbarriers, as indexes
   static constexpr int kQF = 0, kQE = kQF + kNQ, kKF = kQE + kNQ, kKE = kKF + kNK, kVF = kKE + kNK, kVE = kVF + kNV;
@@ -351,11 +354,11 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   constexpr bool kBf16 = L::kBf16;
   extern __shared__ __align__(1024) uint8_t tiles[];
   uint8_t* sm = tiles;
-  float* Gs = reinterpret_cast<float*>(sm + L::kG);
+  float* Ls = reinterpret_cast<float*>(sm + L::kG);
   float* Us = reinterpret_cast<float*>(sm + L::kU);
   float* Xs = reinterpret_cast<float*>(sm + L::kX);
   float* rmsw = reinterpret_cast<float*>(sm + L::kRms);
-  float* wsum = reinterpret_cast<float*>(sm + L::kMisc);           // [2][4]
+  float* wsum = reinterpret_cast<float*>(sm + L::kMisc);           // [2][4], of a block like Ls and Us
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBars);
   int8_t* pexp = reinterpret_cast<int8_t*>(sm + L::kPExp);          // fp16 only, as the next three
@@ -396,9 +399,9 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
   const uint32_t tm = *tmem_slot;
   const int half = (int)blockIdx.x % halves, group_j = (int)blockIdx.x / halves;
   Range rg;
-  locate<kC>(p, group_j, reinterpret_cast<int*>(Gs), rg);
+  locate<kC>(p, group_j, reinterpret_cast<int*>(Ls), rg);
   if (kGated && tid < 64) rmsw[tid] = p.w ? __ldg(p.w + half * 64 + tid) : 1.f;
-  __syncthreads();                                             // the scratch becomes the decay sums
+  __syncthreads();                                             // the scratch becomes the decays
   Part cut;                                                    // the summary's one part
   bool has_cut = false;
   if constexpr (kSum) {
@@ -580,31 +583,28 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
         const int nv = min(kC, g.len - c * kC);                  // tokens of this block
         const float lc = row < nv ? log2_decay(raw) : 0.f;
         if (c + 1 < g.nb) raw = load_g(p, g.t0 + min((c + 1) * kC + row, g.len - 1), g.h);
-        // inclusive sums from the front, exclusive ones from the back
-        float pre = lc, suf = lc;
+        // the sums from the back: all 32 in lane 0, then without the token itself
+        float suf = lc;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const float a = __shfl_up_sync(0xffffffffu, pre, d), b = __shfl_down_sync(0xffffffffu, suf, d);
-          if (lane >= d) pre += a;
+          const float b = __shfl_down_sync(0xffffffffu, suf, d);
           if (lane + d < 32) suf += b;
         }
-        if (lane == 31 && sub == 0) wsum[(i & 1) * 4 + w4] = pre;
-        const float in_warp = __shfl_down_sync(0xffffffffu, suf, 1);
-        suf = lane == 31 ? 0.f : in_warp;
-        tc::named_barrier(1, 128 * kSubs);
-        const float* ws = wsum + (i & 1) * 4;
-        float G = pre, R = suf;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (x < w4) G += ws[x];
-          if (x > w4) R += ws[x];
-        }
+        const float all = suf, behind = __shfl_down_sync(0xffffffffu, suf, 1);
+        suf = lane == 31 ? 0.f : behind;
         if (sub == 0) {
           wait(kGE + (i & 1), (i >> 1 & 1) ^ 1);
-          Gs[(i & 1) * kC + row] = G;
+          Ls[(i & 1) * kC + row] = lc;
           Us[(i & 1) * kC + row] = tc::ex2(suf);
+          if (lane == 0) wsum[(i & 1) * 4 + w4] = all;
           warp_arrive(kGF + (i & 1));
         }
+        tc::named_barrier(1, 128 * kSubs);
+        const float* ws = wsum + (i & 1) * 4;
+        float R = suf;
+#pragma unroll
+        for (int x = 1; x < 4; ++x)
+          if (x > w4) R += ws[x];
         const int sv = i % L::kNV, sk = i % L::kNK;
         wait(kVF + sv, i / L::kNV & 1);
         uint8_t* V = sm + L::kV + sv * kTile + row * 128;
@@ -757,7 +757,8 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           const int sw = i % L::kNW;
           const uint32_t kv = tm + lane_base + kTmKV - 128 * sw;
           wait2(kGF + (i & 1), i >> 1 & 1, kKvF + sw, i / L::kNW & 1);
-          const float la = Gs[(i & 1) * kC + kC - 1];
+          const float4 ws = *reinterpret_cast<const float4*>(wsum + (i & 1) * 4);
+          const float la = (ws.x + ws.y) + (ws.z + ws.w);
           warp_arrive(kGE + (i & 1));
           tc::tc_after_sync();
           if (c + 1 < g.nb || want_end) {
@@ -838,11 +839,30 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
       for_parts([&](const Part& g) {
         for (int c = 0; c < g.nb; ++c) {
           const uint32_t i = it + c, par = i & 1;
-          wait2(kGF + (i & 1), i >> 1 & 1, kScF, par);
-          tc::tc_after_sync();
-          const float* G = Gs + (i & 1) * kC;
+          wait(kGF + (i & 1), i >> 1 & 1);                       // long before the scores
           const float* U = Us + (i & 1) * kC;
-          const float Gi = G[row];
+          const float* ws = wsum + (i & 1) * 4;
+          // sums of l from the start of the row's 16 tokens (pre16) and of its 32 to the row
+          float* L_row = Ls + (i & 1) * kC + row;
+          const float l = *L_row;
+          float pre16 = l;
+#pragma unroll
+          for (int d = 1; d < 16; d <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, pre16, d);
+            if ((lane & 15) >= d) pre16 += y;
+          }
+          const float half0 = __shfl_sync(0xffffffffu, pre16, 15);
+          const float pre32 = lane < 16 ? pre16 : pre16 + half0;
+          // the row's own decay, to the last bit: up to 15 of them make a weight
+          const float decay = l > -1.f ? 1.f + expm1f(l * kLn2) : tc::ex2(l);
+          const float past16 = lane < 16 ? 0.f : tc::ex2(pre16);
+          // the weights of the last token one, two and three 32s before the row's
+          const float sum2 = pre32 + ws[max(w4 - 1, 0)], sum3 = sum2 + ws[max(w4 - 2, 0)];
+          const float past32 = tc::ex2(pre32), past64 = tc::ex2(sum2), past96 = tc::ex2(sum3);
+          // for the outputs: the sum from the block's start
+          *L_row = w4 == 0 ? pre32 : w4 == 1 ? sum2 : w4 == 2 ? sum3 : sum3 + ws[0];
+          wait(kScF, par);
+          tc::tc_after_sync();
           const uint32_t sc = tm + lane_base + kTmSc, plo = tm + lane_base + kTmPlo;
           float up = 1.f;
           if (!kBf16) {
@@ -867,7 +887,8 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           for (int b = 0; b < 2 * w4; ++b) {
             uint32_t x[16], hi[8], lo[8];
             tm_ld16(sc + 16 * b, x);
-            const uint64_t f = both(tc::ex2(Gi - G[16 * (b | 1) + 15]) * up);
+            const int back = w4 - (b >> 1);
+            const uint64_t f = both((back == 1 ? past32 : back == 2 ? past64 : past96) * up);
             const ulonglong2* u2 = reinterpret_cast<const ulonglong2*>(U + 16 * b);
             tm_wait(x);
 #pragma unroll
@@ -888,24 +909,27 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           for (int b = 2 * w4; b < 2 * w4 + 2; ++b) {
             uint32_t x[16], hi[8], lo[8];
             tm_ld16(sc + 16 * b, x);
-            const float4* g4 = reinterpret_cast<const float4*>(G + 16 * b);
-            const int diag = 32 * w4 + lane - 16 * b;
+            const int diag = 32 * w4 + lane - 16 * b, base = 16 * (b & 1);
+            // from the run's last column to the left, one decay a column: rows behind the run start with the weight of
+            // that column, rows in it at their own (with zeros until then, or a NaN of a later token)
+            float wt[16];
+            wt[15] = diag == 15 ? up : base == 0 ? past16 * up : 0.f;
+#pragma unroll
+            for (int e = 14; e >= 0; --e) {
+              const float y = wt[e + 1] * __shfl_sync(0xffffffffu, decay, base + e + 1);
+              wt[e] = e == diag ? up : y;
+            }
             tm_wait(x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 gj = g4[e];
-              const float d[4] = {gj.x, gj.y, gj.z, gj.w};
+            for (int e = 0; e < 16; ++e) {
+              const float m = __uint_as_float(x[e]) * wt[e];
+              x[e] = e <= diag ? __float_as_uint(m) : 0u;
+            }
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const float m = __uint_as_float(x[4 * e + y]) * (tc::ex2(Gi - d[y]) * up);
-                x[4 * e + y] = 4 * e + y <= diag ? __float_as_uint(m) : 0u;
-              }
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                uint64_t z = pack2(x[4 * e + 2 * y], x[4 * e + 2 * y + 1]);
-                hi[2 * e + y] = term<T>(z);
-                lo[2 * e + y] = narrow<T>(z);
-              }
+            for (int e = 0; e < 8; ++e) {
+              uint64_t z = pack2(x[2 * e], x[2 * e + 1]);
+              hi[e] = term<T>(z);
+              lo[e] = narrow<T>(z);
             }
             tm_st8(sc + 8 * b, hi);
             tm_st8(plo + 8 * b, lo);
@@ -933,12 +957,10 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           const uint32_t i = it + c, par = i & 1;
           const int nv = min(kC, g.len - c * kC);
           const int sz = i % L::kNZ;
-          wait2(kGF + (i & 1), i >> 1 & 1, kZF + sz, i / L::kNZ & 1);   // z, or the buffer alone
-          const float Gi = Gs[(i & 1) * kC + row];
-          wait(kPvF, par);
+          wait2(kZF + sz, i / L::kNZ & 1, kPvF, par);            // z, or the buffer alone
           tc::tc_after_sync();
           const bool state = c > 0 || has_start(g);
-          float f1 = p.scale * tc::ex2(Gi), f2 = p.scale;
+          float f1 = p.scale * tc::ex2(Ls[(i & 1) * kC + row]), f2 = p.scale;
           if (!kBf16) {
             f1 *= tc::pow2i(-es[is & 1]);
             f2 *= tc::pow2i(-(int)pexp[(i & 1) * kC + row]);

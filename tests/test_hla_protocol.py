@@ -171,11 +171,11 @@ def outputs_kernel(parts, NQ, NK, NV, NZ, gated, partial, exponent_behind_wait):
 
     for i, _, _, state, behind in blocks:
         tail = partial and not behind
+        o.wait("build", ("GE", i & 1), (i >> 1) - 1)
+        o.write("build", ("L", i & 1), (i, 0))
+        o.write("build", ("U", i & 1), (i, 0))
         o.write("build", ("wsum", i & 1), i)
         o.read("build", ("wsum", i & 1), i)
-        o.wait("build", ("GE", i & 1), (i >> 1) - 1)
-        o.write("build", ("G", i & 1), i)
-        o.write("build", ("U", i & 1), (i, 0))
         o.arrive("build", ("GF", i & 1))
         o.wait("build", ("VF", i % NV), i // NV)
         o.read("build", ("V", i % NV), (i, 0))
@@ -206,7 +206,7 @@ def outputs_kernel(parts, NQ, NK, NV, NZ, gated, partial, exponent_behind_wait):
             put()
         o.wait("state", ("GF", i & 1), i >> 1)
         o.wait("state", "KvF", i)
-        o.read("state", ("G", i & 1), i)
+        o.read("state", ("wsum", i & 1), i)
         o.arrive("state", ("GE", i & 1))
         if behind:
             o.read("state", ("ew", i & 3), i)
@@ -217,9 +217,11 @@ def outputs_kernel(parts, NQ, NK, NV, NZ, gated, partial, exponent_behind_wait):
 
     for i, *_ in blocks:
         o.wait("p", ("GF", i & 1), i >> 1)
-        o.wait("p", "ScF", i)
-        o.read("p", ("G", i & 1), i)
+        o.read("p", ("L", i & 1), (i, 0))
+        o.write("p", ("L", i & 1), (i, 1))
+        o.read("p", ("wsum", i & 1), i)
         o.read("p", ("U", i & 1), (i, 0))
+        o.wait("p", "ScF", i)
         o.write("p", ("pexp", i & 1), i)
         o.read("p", "scores", (i, 0))
         o.write("p", "scores", (i, 1))
@@ -228,10 +230,9 @@ def outputs_kernel(parts, NQ, NK, NV, NZ, gated, partial, exponent_behind_wait):
 
     m = 0
     for i, _, _, state, _ in blocks:
-        o.wait("out", ("GF", i & 1), i >> 1)
         o.wait("out", ("ZF", i % NZ), i // NZ)
-        o.read("out", ("G", i & 1), i)
         o.wait("out", "PvF", i)
+        o.read("out", ("L", i & 1), (i, 1))
         o.read("out", ("pexp", i & 1), i)
         if state:
             o.read("out", ("es", m & 1), m)
@@ -269,7 +270,7 @@ def summary_kernel(nb, NK, NV, NW):
         for b in (("KvF", i % NW), ("WE", i % NW), ("KE", i % NK), ("VE", i % NV)):
             o.arrive("tc", b, o.last["mma"])
         o.wait("build", ("GE", i & 1), (i >> 1) - 1)
-        o.write("build", ("G", i & 1), i)
+        o.write("build", ("wsum", i & 1), i)
         o.arrive("build", ("GF", i & 1))
         o.wait("build", ("VF", i % NV), i // NV)
         o.read("build", ("V", i % NV), i)
@@ -279,7 +280,7 @@ def summary_kernel(nb, NK, NV, NW):
         o.arrive("build", ("WF", i % NW))
         o.wait("state", ("GF", i & 1), i >> 1)
         o.wait("state", ("KvF", i % NW), i // NW)
-        o.read("state", ("G", i & 1), i)
+        o.read("state", ("wsum", i & 1), i)
         o.arrive("state", ("GE", i & 1))
         o.read("state", ("ew", i & 3), i)
         o.read("state", ("KV", i % NW), i)
