@@ -267,6 +267,18 @@ __device__ __forceinline__ float log2_decay(float g) {
   g = g < kMinLog ? kMinLog : g;
   return g * kLog2e;
 }
+// e^x - 1 for -ln 2 < x <= 0 by its series to x^9 (what is left out is below x^10 / 10!, 2^-26 of the result) without a branch.
+__device__ __forceinline__ float expm1_small(float x) {
+  float y = 1.f / 362880.f;
+  y = fmaf(y, x, 1.f / 40320.f);
+  y = fmaf(y, x, 1.f / 5040.f);
+  y = fmaf(y, x, 1.f / 720.f);
+  y = fmaf(y, x, 1.f / 120.f);
+  y = fmaf(y, x, 1.f / 24.f);
+  y = fmaf(y, x, 1.f / 6.f);
+  y = fmaf(y, x, 0.5f);
+  return fmaf(y, x * x, x);
+}
 // Issued where it stands (a plain load may sink to its use, behind the wait it was to cover).
 __device__ __forceinline__ float load_g(const Params& p, int t, int h) {
   float x;

@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kTcThreads, 1) hla_tc(con
           const float half0 = __shfl_sync(0xffffffffu, pre16, 15);
           const float pre32 = lane < 16 ? pre16 : pre16 + half0;
           // the row's own decay, to the last bit: up to 15 of them make a weight
-          const float decay = l > -1.f ? 1.f + expm1f(l * kLn2) : tc::ex2(l);
+          const float decay = l > -1.f ? 1.f + expm1_small(l * kLn2) : tc::ex2(l);
           const float past16 = lane < 16 ? 0.f : tc::ex2(pre16);
           // the weights of the last token one, two and three 32s before the row's
           const float sum2 = pre32 + ws[max(w4 - 1, 0)], sum3 = sum2 + ws[max(w4 - 2, 0)];
