@@ -59,9 +59,15 @@ template <> struct Two<__nv_bfloat16> {
   static __device__ __forceinline__ t from_f(float a, float b) { return __floats2bfloat162_rn(a, b); }
 };
 
-// sigmoid(z) = 1 / (1 + 2^(-z log2 e)).  Both instructions are good to about one
-// unit in the last place of fp32; a sigmoid below 2^-126 is zero.
-__device__ __forceinline__ float sigmoid(float z) {
+// sigmoid(z).  For an fp32 branch e / (1 + e) or 1 / (1 + e) with e = e^-|z|, good to the last bits of fp32 down to
+// its smallest numbers.  For a 16-bit branch 1 / (1 + 2^(-z log2 e)) by two approximate instructions (2^-22 each): the
+// rounding of z log2 e makes it |z| 2^-24 + 2^-21 relative, far below the branch's own rounding, and zero below 2^-126;
+// 8191 gated rows of 5120 bf16 are bound by instruction issue and took 84 us with the longer form, 82 with this.
+template <typename TY> __device__ __forceinline__ float sigmoid(float z) {
+  if constexpr (sizeof(TY) == 4) {
+    const float e = expf(-fabsf(z));
+    return (z < 0.f ? e : 1.f) / (1.f + e);
+  }
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) residual_norm_kernel(
         if (a.act != GTR_GATE_MUL) {
           float sg[VEC];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) sg[e] = sigmoid(z[e]);
+          for (int e = 0; e < VEC; ++e) sg[e] = sigmoid<TY>(z[e]);
           mul(y, sg);
         }
         if (a.act != GTR_GATE_SIGMOID) mul(y, z);
