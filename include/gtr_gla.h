@@ -401,7 +401,8 @@ GTR_API gtr_status_t gtr_stack_fwd(float *x, const gtr_block_weights *blocks, in
  *            far), else from zero.  NULL: every sequence does.
  *   dk, dv in {16, 32, 64, 128}; Hk divides H <= 65535; T < 2^31; for the
  *   prompt form also (T / 16 + 2 nseq) H < 2^31.
- * No element of out may be one of q, k, v, g, outgate or of a state.
+ * No element of out or state_out may be one of another argument's, but for
+ * state_out = state_in.
  * A non-finite q, k or v element reaches only its own sequence and head, but
  * there any output of its block of 128 tokens and what follows.  States, decay
  * sums and the norm are fp32; 16-bit products carry at least 16 significant

@@ -258,19 +258,23 @@ int check_args(const gtr_hla_args* a, bool step, hla::Params* p, bool* empty) {
     const uintptr_t x = (uintptr_t)a->state_in, y = (uintptr_t)a->state_out;
     if (x < y + n && y < x + n) return GTR_ERR_INVALID_ARG;
   }
-  if (a->T > 0) {
-    const Rows out{a->out, ld[4] * es, (long long)a->H * a->dv * es, a->T};
-    const long long st = (long long)a->H * a->dk * a->dv * (long long)sizeof(float);
-    const Rows in[7] = {{a->q, ld[0] * es, (long long)a->Hk * a->dk * es, a->T},
-                        {a->k, ld[1] * es, (long long)a->Hk * a->dk * es, a->T},
-                        {a->v, ld[2] * es, (long long)a->H * a->dv * es, a->T},
-                        {a->outgate, ld[3] * es, (long long)a->H * a->dv * es, a->T},
-                        {a->g, a->H * 4ll, a->H * 4ll, a->g_per_head ? 1 : a->T},
-                        {a->state_in, st, st, a->nslots},
-                        {a->state_out, st, st, a->nslots}};
-    for (const Rows& r : in)
-      if (overlap(out, r)) return GTR_ERR_INVALID_ARG;
-  }
+  // what is written shares nothing with what is read, but for states in place
+  const long long st = (long long)a->H * a->dk * a->dv * (long long)sizeof(float);
+  const Rows out{a->out, ld[4] * es, (long long)a->H * a->dv * es, a->T}, states{a->state_out, st, st, a->nslots};
+  const long long nw = a->workspace ? (long long)std::min<size_t>(a->workspace_bytes, 1ull << 46) : 0;
+  const Rows in[10] = {{a->q, ld[0] * es, (long long)a->Hk * a->dk * es, a->T},
+                       {a->k, ld[1] * es, (long long)a->Hk * a->dk * es, a->T},
+                       {a->v, ld[2] * es, (long long)a->H * a->dv * es, a->T},
+                       {a->outgate, ld[3] * es, (long long)a->H * a->dv * es, a->T},
+                       {a->g, a->H * 4ll, a->H * 4ll, a->g_per_head ? 1 : a->T},
+                       {a->rms_w, a->dv * 4ll, a->dv * 4ll, 1},
+                       {a->slots, 4, 4, a->nseq},
+                       {a->seen, 4, 4, a->nseq},
+                       {a->cu_seqlens, 4, 4, a->nseq + 1ll},
+                       {a->workspace, nw, nw, nw > 0}};
+  for (const Rows& r : in)
+    if (overlap(out, r) || overlap(states, r)) return GTR_ERR_INVALID_ARG;
+  if (overlap(out, states) || overlap(out, Rows{a->state_in, st, st, a->nslots})) return GTR_ERR_INVALID_ARG;
   *p = hla::Params{a->q, a->k, a->v, a->g, a->outgate, a->rms_w, a->out, a->state_in, a->state_out, a->slots, a->seen,
                    a->cu_seqlens, nullptr, nullptr, nullptr, nullptr, ld[0], ld[1], ld[2], ld[3], ld[4], a->nseq, a->T, a->Hk, a->H,
                    a->dk, a->dv, a->nslots, a->g_per_head != 0, a->T / a->nseq, a->scale, 0, 0};

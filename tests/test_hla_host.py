@@ -266,3 +266,22 @@ def test_every_block_is_in_one_part_and_every_cut_is_scanned():
         for j, n, h, b0, k, m in cuts:
             for u in range(m):
                 assert entry[j + u][:2] == (n, h)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rms_w=(1 << 20) + 16, outgate=9 << 24), dict(cu_seqlens=(1 << 20) + 4), dict(slots=1 << 20), dict(seen=(1 << 20) + 2044),
+    dict(workspace=(1 << 20) - 64, workspace_bytes=128),
+])
+def test_hla_output_over_what_steers_the_call_is_refused(lib, kw):
+    # out: 4 tokens, 4 heads of 64, bf16 (2048 bytes)
+    ptrs = {n: (i + 2) << 24 for i, n in enumerate(["q", "k", "v", "g"])}
+    assert lib.gtr_hla_fwd(hla_args(**{**ptrs, "out": 1 << 20, **kw}), None) == -1
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "outgate", "rms_w", "slots", "seen", "cu_seqlens", "workspace"])
+def test_hla_states_over_an_input_are_refused(lib, name):
+    # state_out: one state of 65536 bytes
+    ptrs = {n: (i + 2) << 24 for i, n in enumerate(["q", "k", "v", "g", "out"])}
+    at = (1 << 20) + 65536 - 16
+    more = {"rms_w": dict(outgate=9 << 24), "workspace": dict(workspace_bytes=64)}.get(name, {})
+    assert lib.gtr_hla_fwd(hla_args(**{**ptrs, **more, "state_out": 1 << 20, "nslots": 1, name: at}), None) == -1
