@@ -14,14 +14,11 @@
 #include "hla_tc.cuh"
 
 namespace {
-
-using namespace gtr;
-
 constexpr int kMaxDevices = 64;
+}
 
-bool valid_head_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-
+namespace gtr {
+// Multiprocessors of the current device; also the residual norm's.
 int device_sms(int* sms) {
   static std::atomic<int> count[kMaxDevices];
   int dev;
@@ -35,6 +32,14 @@ int device_sms(int* sms) {
   *sms = n;
   return GTR_OK;
 }
+}  // namespace gtr
+
+namespace {
+
+using namespace gtr;
+
+bool valid_head_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 // 16-bit types and head dims the tensor-core kernels take
 bool tc_shape(int dk, int dv, int dtype) { return dtype != GTR_F32 && dk >= 64 && dv >= 64; }

@@ -31,6 +31,10 @@
 #include "common.cuh"
 #include "tc_ptx.cuh"
 
+namespace gtr {
+int device_sms(int* sms);   // hla.cu: multiprocessors of the current device
+}
+
 namespace {
 
 using namespace gtr;
@@ -291,42 +295,43 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) residual_norm_kernel(
 }
 
 template <typename TX, typename TY, int VEC, int kV>
-int launch_v(const NormArgs& a, int threads, cudaStream_t st) {
-  if (threads == 32) {
-    const unsigned blocks = (a.N + kRowWarps - 1) / kRowWarps;
-    return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, true, 32 * kRowWarps>, dim3(blocks),
-                      dim3(32 * kRowWarps), 0, st, a);
-  }
-  const dim3 grid(a.N), block((unsigned)threads);
-  // Four blocks of up to 320 threads per SM rather than three, at 48 registers: 18944 gated rows of a
-  // 16-bit stream take 155 us for 174 at D = 5120 and 122 for 131 at 4096, but 63.9 for 63.7 at 2048
-  // (128 threads); an fp32 stream would spill and is at a copy's rate as it is.
-  if constexpr (VEC == 8 && kV == 2 && sizeof(TX) == 2)
-    if (threads > 128 && threads <= 320)
-      return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, false, 320, 4>, grid, block, 0, st, a);
-  if (threads <= 512) return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, false, 512>, grid, block, 0, st, a);
-  return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, false, 1024>, grid, block, 0, st, a);
+int launch_warp(const NormArgs& a, cudaStream_t st) {
+  const unsigned blocks = (a.N + kRowWarps - 1) / kRowWarps;
+  return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, true, 32 * kRowWarps>, dim3(blocks), dim3(32 * kRowWarps), 0,
+                    st, a);
+}
+template <typename TX, typename TY, int VEC, int kV, int kMaxThreads, int kMinBlocks = 1>
+int launch_block(const NormArgs& a, int threads, cudaStream_t st) {
+  return launch_pdl(residual_norm_kernel<TX, TY, VEC, kV, false, kMaxThreads, kMinBlocks>, dim3(a.N),
+                    dim3((unsigned)threads), 0, st, a);
 }
 
 int round32(int n) { return (n + 31) / 32 * 32; }
 
 template <typename TX, typename TY>
-int launch_typed(const NormArgs& a, bool vec, cudaStream_t st) {
+int launch_typed(const NormArgs& a, bool vec, int sms, cudaStream_t st) {
   if (vec) {
     // A warp for a row of up to 64 vectors; else two vectors a thread, or one
     // while that leaves at most 512 threads a row and 1024 per SM in all. Gated
     // bf16, one and two: 888 rows of 1024 3.9 and 4.5 us, 1184 rows 4.9 and 5.0;
     // 592 rows of 2048 5.2 and 5.1, 1184 rows 7.8 and 7.0; 148 rows of 4096 3.8
     // and 4.3, 296 rows 5.5 and 5.5, 592 rows 8.7 and 7.4.
-    const int nv = a.D / 8;
-    if (nv <= 32) return launch_v<TX, TY, 8, 1>(a, 32, st);
-    if (nv <= 64) return launch_v<TX, TY, 8, 2>(a, 32, st);
-    if (nv <= 512 && (long long)a.N * nv < 148 * 1024) return launch_v<TX, TY, 8, 1>(a, round32(nv), st);
-    return launch_v<TX, TY, 8, 2>(a, round32((nv + 1) / 2), st);
+    const int nv = a.D / 8, threads = round32((nv + 1) / 2);
+    if (nv <= 32) return launch_warp<TX, TY, 8, 1>(a, st);
+    if (nv <= 64) return launch_warp<TX, TY, 8, 2>(a, st);
+    if (nv <= 512 && (long long)a.N * nv < sms * 1024ll) return launch_block<TX, TY, 8, 1, 512>(a, round32(nv), st);
+    // Four blocks of up to 320 threads per SM rather than three, at 48 registers: 18944 gated rows of a
+    // 16-bit stream take 155 us for 174 at D = 5120 and 122 for 131 at 4096, but 63.9 for 63.7 at 2048
+    // (128 threads); an fp32 stream would spill and is at a copy's rate as it is.
+    if constexpr (sizeof(TX) == 2)
+      if (threads > 128 && threads <= 320) return launch_block<TX, TY, 8, 2, 320, 4>(a, threads, st);
+    if (threads <= 512) return launch_block<TX, TY, 8, 2, 512>(a, threads, st);
+    return launch_block<TX, TY, 8, 2, 1024>(a, threads, st);
   }
-  if (a.D <= 256) return launch_v<TX, TY, 1, 8>(a, 32, st);
-  if (a.D <= 4096) return launch_v<TX, TY, 1, 8>(a, round32((a.D + 7) / 8), st);
-  return launch_v<TX, TY, 1, 16>(a, round32((a.D + 15) / 16), st);
+  if (a.D <= 256) return launch_warp<TX, TY, 1, 8>(a, st);
+  if (a.D <= 4096) return launch_block<TX, TY, 1, 8, 512>(a, round32((a.D + 7) / 8), st);
+  if (a.D <= 8192) return launch_block<TX, TY, 1, 16, 512>(a, round32((a.D + 15) / 16), st);
+  return launch_block<TX, TY, 1, 16, 1024>(a, round32((a.D + 15) / 16), st);
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -374,11 +379,12 @@ extern "C" GTR_API gtr_status_t gtr_residual_norm(const gtr_residual_norm_args* 
   const NormArgs a{x, x_out, y, post_w, gate, res_scale, pre_w, out, (unsigned)N,
                    (unsigned)(gate ? gate_rows : 1), D, post_norm != 0, gate_act, alpha, eps, 1.0f / (float)D};
   const cudaStream_t st = (cudaStream_t)stream;
-  int rc;
-  if (x_dtype == GTR_F16) rc = launch_typed<__half, __half>(a, vec, st);
-  else if (x_dtype == GTR_BF16) rc = launch_typed<__nv_bfloat16, __nv_bfloat16>(a, vec, st);
-  else if (dtype == GTR_F32) rc = launch_typed<float, float>(a, vec, st);
-  else if (dtype == GTR_F16) rc = launch_typed<float, __half>(a, vec, st);
-  else rc = launch_typed<float, __nv_bfloat16>(a, vec, st);
+  int rc, sms;
+  if ((rc = device_sms(&sms)) != 0) return (gtr_status_t)rc;
+  if (x_dtype == GTR_F16) rc = launch_typed<__half, __half>(a, vec, sms, st);
+  else if (x_dtype == GTR_BF16) rc = launch_typed<__nv_bfloat16, __nv_bfloat16>(a, vec, sms, st);
+  else if (dtype == GTR_F32) rc = launch_typed<float, float>(a, vec, sms, st);
+  else if (dtype == GTR_F16) rc = launch_typed<float, __half>(a, vec, sms, st);
+  else rc = launch_typed<float, __nv_bfloat16>(a, vec, sms, st);
   return rc ? GTR_ERR_CUDA : GTR_OK;
 }

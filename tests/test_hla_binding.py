@@ -77,3 +77,37 @@ def test_a_gate_needs_its_kind(no_launch):
     x = on_device(4, 64)
     with pytest.raises(ValueError, match="gate_act"):
         binding.residual_norm(x, x, gate=x, gate_act="none")
+
+
+def test_every_variant_of_the_norm_has_a_call():
+    """The launch rule of residual_norm.cu over all widths and row counts reaches each kernel that it names."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(binding.__file__), "csrc", "residual_norm.cu")).read()
+    body = src[src.index("int launch_typed("):src.index("bool aligned(")]
+    named = set(re.findall(r"launch_(warp|block)<TX, TY, ([\d, ]+)>", body))
+
+    def rule(D, N, vec, sixteen, sms=148):
+        up = lambda n: (n + 31) // 32 * 32  # noqa: E731
+        if vec:
+            nv, threads = D // 8, up((D // 8 + 1) // 2)
+            if nv <= 64:
+                return "warp", "8, 1" if nv <= 32 else "8, 2"
+            if nv <= 512 and N * nv < sms * 1024:
+                assert up(nv) <= 512
+                return "block", "8, 1, 512"
+            if sixteen and 128 < threads <= 320:
+                return "block", "8, 2, 320, 4"
+            assert threads <= 1024 and threads * 2 >= nv
+            return "block", "8, 2, 512" if threads <= 512 else "8, 2, 1024"
+        if D <= 256:
+            return "warp", "1, 8"
+        if D <= 4096:
+            assert up((D + 7) // 8) <= 512
+            return "block", "1, 8, 512"
+        assert up((D + 15) // 16) <= (512 if D <= 8192 else 1024)
+        return "block", "1, 16, 512" if D <= 8192 else "1, 16, 1024"
+
+    for sixteen in (False, True):
+        got = {rule(D, N, vec, sixteen) for D in range(1, 16385) for N in (1, 100000) for vec in ((False, True) if D % 8 == 0 else (False,))}
+        assert got == (named if sixteen else named - {("block", "8, 2, 320, 4")})
