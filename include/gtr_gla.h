@@ -384,7 +384,8 @@ GTR_API gtr_status_t gtr_stack_fwd(float *x, const gtr_block_weights *blocks, in
  *   rms_w    [dv] fp32 or NULL (ones); must be NULL when outgate is.
  *   cu_seqlens  device int32 [nseq + 1], non-decreasing from >= 0 to <= T:
  *            sequence n is rows [cu_seqlens[n], cu_seqlens[n + 1]).  Rows
- *            outside every sequence are neither read nor written.  NULL: nseq
+ *            outside every sequence are not written, and nothing in them
+ *            reaches a result (blocks of 128 rows may load them).  NULL: nseq
  *            equal sequences of T / nseq rows (nseq must divide T).  Lengths
  *            of zero are allowed (the final state is then the initial one).
  *            With other offsets the call writes no output and no state, which

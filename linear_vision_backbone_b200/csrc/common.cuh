@@ -1,7 +1,8 @@
 // common.cuh -- element types, scan-order index maps and device status shared
-// by the kernels of the Key-only GLA library.  Every kernel that uses them is
-// in one translation unit (gtr_gla.cu), so device globals need no relocatable
-// device code.
+// by the kernels of the library.  The device globals are static, one set for
+// each translation unit, so they need no relocatable device code;
+// gtr_last_device_status joins those of the two units that set them (gtr_gla.cu,
+// hla.cu).
 #pragma once
 
 #include <cuda_runtime.h>

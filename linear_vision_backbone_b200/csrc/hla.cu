@@ -54,19 +54,23 @@ struct Plan {
 // (k and v before the cuts are read a second time) and two more launches; whole
 // (sequence, head)s need neither, but the longest one bounds the time.  In units
 // of one block of tokens of the outputs kernel on an SM of its own, a summary's
-// block costs about kSum and the two launches kExtra.  With cu_seqlens the
-// longest sequence may have all the tokens.  Whole and cut, gated, in us:
-//   bf16, 6 heads of 64:   1 x 256 tokens 12.4 and 17.1, 1 x 1024 28.1 and 18.2,
-//     8 x 1600 41.8 and 37.0, 24 x 1600 49 and 77
-//   bf16, 16 heads of 128: 1 x 512 24.3 and 27.9, 1 x 1024 40.1 and 32.1,
-//     8 x 1600 130 and 147
-//   fp32, 6 heads of 64:   1 x 32 11.9 and 15.3, 1 x 64 20.1 and 15.3,
-//     8 x 1600 412 and 216, 24 x 512 136 and 212
-// (over 45 such cases the choice costs 0.8 % of the better one's time with the
-// tensor cores' constants).  The CUDA-core kernel cuts for two groups per SM: 24
-// x 1600 with 4 heads of 128 takes 842 us, one group 1051, three 927, four 850;
-// with even shares rounded up, 8 x 1600 takes 313 us for 291.  Whole, an SM gains
-// nothing by a second group, and each gets a (sequence, head).
+// block costs about kSum and the two launches kExtra.  Whole and cut, gated, in us:
+//   bf16, 6 heads of 64:   1 x 256 tokens 13.2 and 18.9, 1 x 1024 30.7 and 19.7,
+//     8 x 1600 46 and 40, 24 x 1600 51 and 80
+//   bf16, 16 heads of 128: 1 x 512 24.5 and 29.4, 1 x 4096 147 and 68,
+//     8 x 1600 129 and 149
+//   fp32, 6 heads of 64:   1 x 32 11.9 and 16.1, 1 x 64 20.1 and 16.0,
+//     8 x 1600 422 and 218, 24 x 512 139 and 214
+// Without cu_seqlens the choice costs 0.3 % over 65 such cases (3.5 % at most, 24 x
+// 1600 with 4 fp32 heads of 128).  With cu_seqlens the longest sequence may have
+// all the tokens, so it is taken to: sequences that turn out equal can take longer
+// than whole (24 x 1600 above 80 us for 51, 8 x 256 24 for 14).  The CUDA-core
+// kernel cuts for twice as many groups as SMs: 24 x 1600 with 4 heads of 128 takes
+// 842 us, as many groups as SMs 1051, three times 927, four times 850, although one
+// block of its outputs is resident per SM from dk = dv = 64 on (180 registers a
+// thread and more) and the second follows it; with even shares rounded up, 8 x 1600
+// takes 313 us for 291.  Whole, an SM gains nothing by a second group, and each gets
+// a (sequence, head).
 void make_plan(int nseq, int T, int H, int dk, int dv, int dtype, bool equal, int sms, Plan* p) {
   const bool tc = tc_shape(dk, dv, dtype);
   const double kSum = tc ? 0.35 : 0.5, kExtra = tc ? 4.0 : 3.0;

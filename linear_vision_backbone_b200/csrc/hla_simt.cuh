@@ -76,9 +76,11 @@ template <typename T, bool kSum> struct Batch {
 // serial chain of its tokens (three operations per state element and token in
 // fp32, two rows to an instruction: 306 cycles a token at dk = dv = 64, and 4400
 // per batch to add up the partial sums and finish the rows), so the tokens are
-// split over many short parts.  1600 tokens, 6 heads of 64, fp32: summaries 17 us,
-// scan 12, outputs 31 (cold caches), 51 us a call; one group for a (sequence,
-// head), uncut, would take 407 us.
+// split over many short parts.  One block of the outputs is resident per SM at 16
+// rows a thread and more (180 registers; 254 at 64 rows).  1600 tokens, 6 heads of
+// 64, fp32: summaries 16 us, scan 13.5, outputs 30 (cold caches), 52 us a call; one
+// group for a (sequence, head), uncut, would take 415 us.  16-bit heads of 16 and 32
+// dims: 16384 tokens, 6 heads, 143 and 193 us a call.
 template <typename T, int ROWS, bool kSum>
 __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
   extern __shared__ __align__(16) float sm[];
@@ -237,9 +239,10 @@ __global__ void __launch_bounds__(kSimtThreads) hla_simt(const Params p) {
 // bytes at dk = dv = 128).  A block of 256 threads per (row, head); thread tid
 // has the four columns 4 (tid % (dv / 4)) and every (256 / (dv / 4))-th row,
 // R float4 of the state, all loaded before the first is used.  Bound by memory
-// with many rows (500 rows, 16 heads of 128: 165 us, 6.4 TB/s, 0.98 of a plain
-// copy's rate), by the fill and drain of seven blocks per SM with 64 (26.5 us, 5.1
-// TB/s), by latency and the launch with one (5.3 us).
+// with many rows (500 rows, 16 heads of 128: 165 us for the kernel by itself, 170 to
+// 175 call behind call, 6.1 TB/s, 0.93 of a plain copy's rate), by start and end with
+// 64 (28.7 us, 4.7 TB/s: two blocks resident per SM, so 1024 blocks are 3.5 waves),
+// by latency and the launch with one (2.7 us in a graph).
 constexpr int kStepThreads = 256;
 
 template <typename T, int R>

@@ -51,12 +51,14 @@
 //
 // Bound by the chain scores -> P -> pv -> outputs of a block and the state's kv ->
 // S -> qs beside it, each link a wait of 120-200 cycles and a pass of exponentials
-// or roundings by one or two warps a scheduler: a block of 128 tokens takes 2.6 us
-// for dk = dv = 64 and 3.9 us for 128 (3.5 and 5 with every SM busy), of which the
-// tensor cores are busy 0.7 and 1.1. Measured: 16384 tokens, 6 heads of 64, fp16, gated (one wave, cold caches):
-// summaries 17 us, scan 6.7, outputs 33.6, 50 us a call, 1.3 TB/s of the call's
-// 63 MB; 65536 tokens, 4 heads of 128, bf16: 46 + 8.6 + 140, 185 us a call, 1.8 TB/s
-// of 336 MB; 28 prompts of 4 to 7442 tokens, 16 heads of 128: 70 + 6.7 + 164, 256 us.
+// or roundings by one or two warps a scheduler: a block of 128 tokens takes 3.0 to
+// 3.4 us for dk = dv = 64 and 4.5 us for 128 (3.6 and 4.4 with every SM busy), of
+// which the tensor cores are busy 0.7 and 1.1.  A thread of the outputs kernel
+// spills 56 to 112 bytes of registers.  Measured: 16384 tokens, 6 heads of 64, fp16,
+// gated (one wave, cold caches): summaries 18 us, scan 7.6, outputs 34, 50 us a
+// call, 1.3 TB/s of the call's 63 MB; 65536 tokens, 4 heads of 128, bf16: 49 + 8.8 +
+// 145, 188 to 195 us a call, 1.8 TB/s of 336 MB; 28 prompts of 4 to 7442 tokens, 16
+// heads of 128: 71 + 7.5 + 172, 255 us.
 #pragma once
 #include "hla_common.cuh"
 #include "tc_ptx.cuh"

@@ -10,13 +10,15 @@
 // to the last store, so the two means cost reductions and no second read; all
 // of a thread's loads are issued before the first is used.
 //
-// Measured: 16384 rows of 384, fp32 stream, fp16 branch, pre-norm: 13.1-16 us,
-// 4.7-5.8 TB/s (two waves of blocks); 8191 rows of 5120 bf16 with a SiLU gate, a
-// scale and both norms: 75 us, 5.6 TB/s, 0.85 of a plain copy's rate, and 0.95 with
-// 18944 rows (start and end of the launch; two thirds of the issue slots are taken,
+// Measured: 16384 rows of 384, fp32 stream, fp16 branch, pre-norm: 15 to 16.5 us,
+// 4.6 to 5.1 TB/s (a warp's row takes 66 registers: three blocks per SM, 4.6 waves;
+// its 48 vectors leave half of the lanes idle in the second); 8191 rows of 5120 bf16
+// with a SiLU gate, a scale and both norms: 76 to 81 us on several machines, 5.2 to
+// 5.5 TB/s, 0.79 to 0.84 of a plain copy's rate, and 0.86 with 18944 rows, 0.91
+// without the scale (start and end of the launch; 0.6 of the issue slots are taken,
 // so conversions and products are two elements to an instruction); 18944 rows of an
 // fp32 stream without a gate run at a copy's rate from D = 2048 on; nine rows of
-// 4096: 5.7 us (latency).  A resident grid that copies rows ahead into shared memory
+// 4096: 3.0 us in a graph (latency).  A resident grid that copies rows ahead into shared memory
 // and keeps the weights in registers was 10 to 50 % slower at every size from D =
 // 256 to 8192 (fewer warps to hide the arithmetic).
 #include <cuda_bf16.h>
@@ -320,14 +322,16 @@ int launch_typed(const NormArgs& a, bool vec, int sms, cudaStream_t st) {
     if (nv <= 32) return launch_warp<TX, TY, 8, 1>(a, st);
     if (nv <= 64) return launch_warp<TX, TY, 8, 2>(a, st);
     if (nv <= 512 && (long long)a.N * nv < sms * 1024ll) return launch_block<TX, TY, 8, 1, 512>(a, round32(nv), st);
-    // Four blocks of up to 320 threads per SM rather than three, at 48 registers: 18944 gated rows of a
-    // 16-bit stream take 155 us for 174 at D = 5120 and 122 for 131 at 4096, but 63.9 for 63.7 at 2048
-    // (128 threads); an fp32 stream would spill and is at a copy's rate as it is.
+    // Four blocks of up to 320 threads per SM rather than three, at 48 registers: 18944 gated and scaled
+    // rows of a 16-bit stream take 173 us for 195 at D = 5120 and 137 for 148 at 4096, but as long at 2048
+    // (128 threads); more threads than 320 have no 48 registers for four blocks (6666 rows of 6144: 80 us,
+    // 0.78 of a copy's rate; 5000 of 8192: 85, 0.73); an fp32 stream would spill and is at a copy's rate.
     if constexpr (sizeof(TX) == 2)
       if (threads > 128 && threads <= 320) return launch_block<TX, TY, 8, 2, 320, 4>(a, threads, st);
     if (threads <= 512) return launch_block<TX, TY, 8, 2, 512>(a, threads, st);
     return launch_block<TX, TY, 8, 2, 1024>(a, threads, st);
   }
+  // one element an access: 8191 gated rows of 5119 bf16 take 247 us, of 5120 78
   if (a.D <= 256) return launch_warp<TX, TY, 1, 8>(a, st);
   if (a.D <= 4096) return launch_block<TX, TY, 1, 8, 512>(a, round32((a.D + 7) / 8), st);
   if (a.D <= 8192) return launch_block<TX, TY, 1, 16, 512>(a, round32((a.D + 15) / 16), st);
