@@ -592,7 +592,11 @@ def hla_fwd(q, k, v, g, z=None, w=None, *, cu_seqlens=None, scale: float = 1.0, 
     dk, dv], read at each sequence's start and written at its end, at row
     slots[n] (int32; None: n; negative: the sequence is skipped); the same
     tensor updates in place.  A sequence with seen[n] <= 0 (int32) starts from
-    zero.  Rows outside every sequence are left as they were.
+    zero.  Rows outside every sequence are left as they were.  With offsets that
+    decrease or leave 0 .. T nothing is written, and :func:`device_status` says so.
+    A token's heads and the tokens themselves may not share memory (no broadcast
+    tensors); a non-finite token reaches what follows it in its sequence and head,
+    and with 16-bit heads of 64 or 128 dims any output of its block of 128 tokens.
     """
     return _hla("gtr_hla_fwd", q, k, v, g, z, w, cu_seqlens, None, scale, state_in, state_out, slots, seen, out,
                 stream)
